@@ -26,6 +26,15 @@ from ._binding import (  # noqa: F401
     rope_write_kv_tree,
     ropekv_status_string,
 )
+from ._serving import (  # noqa: F401
+    load_serving_library,
+    mrope_freq_axis,
+    paged_attention_shared_prefix,
+    paged_attention_workspace_size,
+    paged_kv_read,
+    rope_write_kv_mrope,
+    rope_write_kv_slot_mapping_quant,
+)
 
 __all__ = [
     "NEOX", "GPTJ", "RopeKVError", "load_library", "library_path",
@@ -35,4 +44,6 @@ __all__ = [
     "paged_kv_delta_update", "paged_kv_delta_update_fused", "dflash_prepare_delta_metadata",
     "dflash_gather_delta_rope", "rope_write_kv_slot_mapping", "rope_check_capacity",
     "ropekv_set_residency_cap", "ropekv_floor_copy", "ropekv_status_string",
+    "rope_write_kv_mrope", "mrope_freq_axis", "rope_write_kv_slot_mapping_quant", "paged_kv_read",
+    "paged_attention_shared_prefix", "paged_attention_workspace_size", "load_serving_library",
 ]

@@ -1,11 +1,11 @@
 """Build libropekv.so (the C ABI and its sm_103a kernels) in-tree with nvcc,
-and libropekv_floor.so, the copy kernel the benchmark times as the floor of
-a decode-sized launch.
+libropekv_serving.so (the serving operators around the paged cache), and
+libropekv_floor.so, the copy kernel the benchmark times as the floor of a
+decode-sized launch.
 
-Each library is one translation unit compiled for sm_103a only and linked
-against the static CUDA runtime, so it loads without any other file from this
-package; the two compile in parallel. Output: ``rope_kv_cache_gb300/lib/``
-(git-ignored).
+Each library is compiled for sm_103a only and linked against the static CUDA
+runtime, so it loads without any other file from this package; all translation
+units compile in parallel. Output: ``rope_kv_cache_gb300/lib/`` (git-ignored).
 """
 from __future__ import annotations
 
@@ -20,10 +20,16 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libropekv.so")
 FLOOR_LIB_PATH = os.path.join(LIB_DIR, "libropekv_floor.so")
+SERVING_LIB_PATH = os.path.join(LIB_DIR, "libropekv_serving.so")
 SOURCES = [os.path.join(CSRC, "ropekv_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ropekv_kernels.cuh"), os.path.join(INCLUDE, "ropekv.h")]
 FLOOR_SOURCES = [os.path.join(CSRC, "ropekv_floor.cu")]
 FLOOR_DEPS = FLOOR_SOURCES + [os.path.join(INCLUDE, "ropekv_floor.h")]
+SERVING_SOURCES = [os.path.join(CSRC, "ropekv_serving.cu"),
+                   os.path.join(CSRC, "ropekv_attention.cu")]
+SERVING_DEPS = SERVING_SOURCES + [os.path.join(CSRC, n) for n in (
+    "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh")] + [
+    os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -45,22 +51,35 @@ def _stale(lib: str, deps) -> bool:
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Build both libraries where stale (or always with force); returns the
+    """Build the libraries where stale (or always with force); returns the
     path of libropekv.so."""
     os.makedirs(LIB_DIR, exist_ok=True)
     extra = ("-Xptxas", "-v") if verbose else ()
-    jobs = []
+    jobs = []   # (compilers, their objects (none: the library itself), output, library)
     for lib, sources, deps in ((LIB_PATH, SOURCES, DEPS),
-                               (FLOOR_LIB_PATH, FLOOR_SOURCES, FLOOR_DEPS)):
+                               (FLOOR_LIB_PATH, FLOOR_SOURCES, FLOOR_DEPS),
+                               (SERVING_LIB_PATH, SERVING_SOURCES, SERVING_DEPS)):
         if force or _stale(lib, deps):
             tmp = lib + f".{os.getpid()}.tmp"
-            jobs.append((subprocess.Popen(nvcc_command(tmp, extra, sources)), tmp, lib))
+            if len(sources) == 1:
+                jobs.append(([subprocess.Popen(nvcc_command(tmp, extra, sources))], [], tmp, lib))
+            else:
+                objs = [f"{tmp}.{i}.o" for i in range(len(sources))]
+                jobs.append(([subprocess.Popen([a for a in nvcc_command(o, (*extra, "-c"), [src])
+                                                if a != "-shared"])
+                              for o, src in zip(objs, sources)], objs, tmp, lib))
     failed = []
-    for proc, tmp, lib in jobs:
-        if proc.wait() != 0:
-            failed.append(os.path.basename(lib))
-        else:
+    for procs, objs, tmp, lib in jobs:
+        ok = all([p.wait() == 0 for p in procs])
+        if ok and objs:
+            ok = subprocess.run(nvcc_command(tmp, (), objs)).returncode == 0
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
+        if ok:
             os.replace(tmp, lib)
+        else:
+            failed.append(os.path.basename(lib))
     if failed:
         raise RuntimeError(f"nvcc failed for {', '.join(failed)}")
     return LIB_PATH
