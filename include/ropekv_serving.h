@@ -159,9 +159,9 @@ ROPEKV_API int64_t paged_attention_workspace_size(const ropekv_attention_dims* d
  * Sums, softmax and partial results are FP32; the weights of V are rounded to
  * FP16 once.
  * Host errors: sizes negative, tokensPerPage <= 0, seqLen > 2^15, prefixLen >
- * maxPrefixPages * tokensPerPage, 2 * numPages * tokensPerPage or
- * maxPagesPerSeq * tokensPerPage >= 2^31, or more than 2^30 query rows ->
- * ROPEKV_ERR_SHAPE; workspaceBytes too small -> ROPEKV_ERR_CAPACITY; an unknown
+ * maxPrefixPages * tokensPerPage, 2 * numPages * tokensPerPage >= 2^31,
+ * prefixLen or maxPagesPerSeq * tokensPerPage > 2^30, or more than 2^30 query
+ * rows -> ROPEKV_ERR_SHAPE; workspaceBytes too small -> ROPEKV_ERR_CAPACITY; an unknown
  * cacheFormat -> ROPEKV_ERR_STYLE; smScale not finite -> ROPEKV_ERR_SHAPE.
  */
 ROPEKV_API int paged_attention_shared_prefix(

@@ -28,7 +28,7 @@ FLOOR_DEPS = FLOOR_SOURCES + [os.path.join(INCLUDE, "ropekv_floor.h")]
 SERVING_SOURCES = [os.path.join(CSRC, "ropekv_serving.cu"),
                    os.path.join(CSRC, "ropekv_attention.cu")]
 SERVING_DEPS = SERVING_SOURCES + [os.path.join(CSRC, n) for n in (
-    "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh")] + [
+    "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh", "ropekv_prefix_kernel.cuh")] + [
     os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -8,11 +8,13 @@
 #include <stdint.h>
 
 #include "ropekv_attention_kernels.cuh"
+#include "ropekv_prefix_kernel.cuh"
 #include "ropekv_serving.h"
 
 namespace {
 
 using ropekv_attn::Args;
+using ropekv_attn::PrefixConfig;
 using ropekv_attn::RowsConfig;
 
 constexpr int kSMs = 152;
@@ -36,7 +38,8 @@ int check_dims(const ropekv_attention_dims* d)
         d->tokensPerPage <= 0 || d->maxPagesPerSeq < 0 || d->prefixLen < 0 || d->maxPrefixPages < 0)
         return ROPEKV_ERR_SHAPE;
     if (2LL * d->numPages * d->tokensPerPage > 0x7FFFFFFFLL ||
-        (long long)d->maxPagesPerSeq * d->tokensPerPage > 0x7FFFFFFFLL ||
+        (long long)d->maxPagesPerSeq * d->tokensPerPage > (1LL << 30) ||
+        d->prefixLen > (1 << 30) ||
         d->prefixLen > (long long)d->maxPrefixPages * d->tokensPerPage ||
         (long long)d->batch * d->seqLen > (1LL << 30) / d->numQHeads)
         return ROPEKV_ERR_SHAPE;
@@ -104,36 +107,103 @@ int launch_rows(const Args& a, long long tiles, long long tokens, bool dependent
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
 
+// How the prefix is cut: `tensor` rows take tcgen05 tiles of 128 (or 2 x 128)
+// rows, fewer take the rows kernel, whose cluster leaves one partial.
+struct PrefixPlan {
+    bool tensor;
+    int tiles;   // row tiles per KV head
+    int parts;   // ranges of the prefix = partials in the workspace
+};
+
+// Ranges of the prefix: their number p minimises the K/V tiles that the busiest
+// SM walks, waves(units * p) * ceil(tiles / p), where each CTA costs about three
+// tiles more to start and to write its partial.
+PrefixPlan plan_prefix(const ropekv_attention_dims* d)
+{
+    PrefixPlan plan = {false, 0, 0};
+    if (d->prefixLen <= 0 || d->batch == 0 || d->seqLen == 0)
+        return plan;
+    const long long rows = (long long)d->batch * d->seqLen * (d->numQHeads / d->numKVHeads);
+    plan.tensor = rows > 8;
+    plan.parts = 1;
+    if (!plan.tensor) {
+        plan.tiles = (int)((rows + 7) / 8);
+        return plan;
+    }
+    const int tileRows = d->headDim != 256 && rows > 128 ? 256 : 128;
+    const int tokens = d->headDim == 256 ? 64 : 128;
+    plan.tiles = (int)((rows + tileRows - 1) / tileRows);
+    const long long units = (long long)plan.tiles * d->numKVHeads;
+    const long long kv = ((long long)d->prefixLen + tokens - 1) / tokens;
+    double best = 1e30;
+    for (int p = 1; p <= 32 && p <= kv; ++p) {
+        const double waves = (double)((units * p + kSMs - 1) / kSMs);
+        const double cost = waves * ((double)((kv + p - 1) / p) + 3.0) + 0.25 * p;
+        if (cost < best) {
+            best = cost;
+            plan.parts = p;
+        }
+    }
+    return plan;
+}
+
+template <int D, int FMT, int MT>
+int launch_prefix(const Args& a, long long ctas, cudaStream_t st)
+{
+    constexpr auto kern = ropekv_attn::prefix_kernel<D, FMT, MT>;
+    using C = PrefixConfig<D, FMT, MT>;
+    if (!raise_smem<kern>(C::kSmem))
+        return ROPEKV_ERR_LAUNCH;
+    if (ctas > 0x7FFFFFFFLL)
+        return ROPEKV_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
+}
+
 // Rows per tile: 8 columns waste nothing for a GQA group of up to 8 rows.
 template <int D, int FMT>
-int launch_all(Args a, cudaStream_t st)
+int launch_all(Args a, const PrefixPlan& plan, cudaStream_t st)
 {
-    const int rows = a.S * a.G;
     int rc = ROPEKV_OK;
-    if (a.P > 0) {
-        a.tilesPerUnit = (a.rowsPrefix + 7) / 8;
-        rc = launch_rows<D, FMT, 1, true>(a, (long long)a.tilesPerUnit * a.Hkv, a.P, false, st);
-        if (rc != ROPEKV_OK)
-            return rc;
+    a.numParts = plan.parts;
+    if (plan.tensor) {
+        const long long ctas = (long long)plan.tiles * a.Hkv * plan.parts;
+        if constexpr (D != 256) {
+            rc = a.rowsPrefix > 128 ? launch_prefix<D, FMT, 2>(a, ctas, st)
+                                    : launch_prefix<D, FMT, 1>(a, ctas, st);
+        } else {
+            rc = launch_prefix<D, FMT, 1>(a, ctas, st);
+        }
+    } else if (plan.parts > 0) {
+        a.tilesPerUnit = plan.tiles;
+        rc = launch_rows<D, FMT, 1, true>(a, (long long)plan.tiles * a.Hkv, a.P, false, st);
     }
-    a.tilesPerUnit = (rows + 7) / 8;
+    if (rc != ROPEKV_OK)
+        return rc;
+    a.tilesPerUnit = (a.S * a.G + 7) / 8;
     const long long own = (long long)a.mpps * a.tpp - a.P;
-    return launch_rows<D, FMT, 1, false>(a, (long long)a.B * a.tilesPerUnit * a.Hkv, own, a.P > 0, st);
+    return launch_rows<D, FMT, 1, false>(a, (long long)a.B * a.tilesPerUnit * a.Hkv, own,
+                                         plan.parts > 0, st);
 }
 
 template <int D>
-int dispatch(const Args& a, int fmt, cudaStream_t st)
+int dispatch(const Args& a, const PrefixPlan& plan, int fmt, cudaStream_t st)
 {
     switch (fmt) {
-    case ROPEKV_CACHE_F16: return launch_all<D, ROPEKV_CACHE_F16>(a, st);
-    case ROPEKV_CACHE_E4M3: return launch_all<D, ROPEKV_CACHE_E4M3>(a, st);
-    default: return launch_all<D, ROPEKV_CACHE_INT8>(a, st);
+    case ROPEKV_CACHE_F16: return launch_all<D, ROPEKV_CACHE_F16>(a, plan, st);
+    case ROPEKV_CACHE_E4M3: return launch_all<D, ROPEKV_CACHE_E4M3>(a, plan, st);
+    default: return launch_all<D, ROPEKV_CACHE_INT8>(a, plan, st);
     }
 }
 
-int prefix_parts(const ropekv_attention_dims* d)
+int64_t workspace_size(const ropekv_attention_dims* d, const PrefixPlan& plan)
 {
-    return d->prefixLen > 0 ? 1 : 0;
+    const int64_t rows = (int64_t)d->batch * d->seqLen * d->numQHeads * plan.parts;
+    return rows * d->headDim * 4 + (rows * 4 + 15) / 16 * 16;
 }
 
 }  // namespace
@@ -145,8 +215,7 @@ int64_t paged_attention_workspace_size(const ropekv_attention_dims* dims)
     const int rc = check_dims(dims);
     if (rc != ROPEKV_OK)
         return rc;
-    const int64_t rows = (int64_t)dims->batch * dims->seqLen * dims->numQHeads;
-    return prefix_parts(dims) * (rows * dims->headDim * 4 + (rows * 4 + 15) / 16 * 16);
+    return workspace_size(dims, plan_prefix(dims));
 }
 
 int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const float* kvScales,
@@ -162,7 +231,8 @@ int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const 
         return ROPEKV_ERR_SHAPE;
     if (dims->batch == 0 || dims->seqLen == 0)
         return ROPEKV_OK;
-    const int64_t need = paged_attention_workspace_size(dims);
+    const PrefixPlan plan = plan_prefix(dims);
+    const int64_t need = workspace_size(dims, plan);
     const bool f16 = dims->cacheFormat == ROPEKV_CACHE_F16;
     if (!q || !kvLens || !out || (!kvCache && dims->numPages > 0) ||
         (!f16 && !kvScales && dims->numPages > 0) || (!prefixTable && dims->prefixLen > 0) ||
@@ -195,14 +265,13 @@ int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const 
     a.P = dims->prefixLen;
     a.prefixPages = dims->maxPrefixPages;
     a.rowsPrefix = dims->batch * dims->seqLen * a.G;
-    a.numParts = prefix_parts(dims);
     a.partO = (float*)workspace;
-    a.partL = a.partO + (size_t)a.numParts * a.rowsPrefix * a.Hkv * dims->headDim;
+    a.partL = a.partO + (size_t)plan.parts * a.rowsPrefix * a.Hkv * dims->headDim;
     cudaStream_t st = (cudaStream_t)stream;
     switch (dims->headDim) {
-    case 64: return dispatch<64>(a, dims->cacheFormat, st);
-    case 128: return dispatch<128>(a, dims->cacheFormat, st);
-    default: return dispatch<256>(a, dims->cacheFormat, st);
+    case 64: return dispatch<64>(a, plan, dims->cacheFormat, st);
+    case 128: return dispatch<128>(a, plan, dims->cacheFormat, st);
+    default: return dispatch<256>(a, plan, dims->cacheFormat, st);
     }
 }
 

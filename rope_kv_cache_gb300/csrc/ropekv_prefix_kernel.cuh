@@ -1,0 +1,616 @@
+// ropekv_prefix_kernel.cuh -- the shared prefix of
+// paged_attention_shared_prefix on the 5th-generation tensor cores.
+//
+// For one KV head the B * S * G query rows of the batch form a matrix Q, the
+// prefix matrices K and V: S = Q K^T, P = 2^(c S - M), O += P V, with M and the
+// row sums kept per row. One CTA takes MT tiles of 128 rows and one range of the
+// prefix, and leaves (O / l, M + log2 l) of every row in the workspace.
+//
+//   warps 0-3 (and 4-7 with MT = 2)  softmax: a thread owns one row, which is
+//                     one TMEM lane; S comes by tcgen05.ld, P goes back by
+//                     tcgen05.st over the columns of S that it was made from
+//   warp 8            issues tcgen05.mma from one thread: S from shared memory
+//                     (both operands K-major), O with P from TMEM and V from
+//                     shared memory (N-major: V is stored as it lies in the cache)
+//   warps 9-11        fetch pages: a ring of tiles K0, V0, K1, V1, ... in shared
+//                     memory, 128-byte swizzled rows of 64 dims. FP16 rows come by
+//                     cp.async; 8-bit rows are decoded to FP16 (exact) on the way
+//
+// Items i = 0, 1, ... alternate between two TMEM slots for S. With two row tiles
+// item i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i: either way
+// the tensor cores work on one slot while the softmax works on the other. The
+// issue order S(0) S(1) [O(i) S(i + 2)]... makes each S overwrite its slot only
+// after the P in it was read.
+//
+// M moves only when a row's scores exceed it by more than 2^8, in which case the
+// row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: a token's K
+// scale multiplies its column of S, its V scale its column of P. With 2^e the
+// largest V scale of a tile, M follows max(s) + e: then P times scale stays near
+// [0, 2^9], and as O and l share M nothing has to be undone.
+//
+// Every wait on an mbarrier is bounded; a wait that runs out makes the CTA stop
+// waiting and write NaN.
+#pragma once
+
+#include "ropekv_attention_kernels.cuh"
+
+namespace ropekv_attn {
+
+template <int D, int FMT, int MT>
+struct PrefixConfig {
+    static constexpr int kTile = D == 256 ? 64 : 128;      // tokens of a K/V tile
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kStages = 4;
+    static constexpr int kMeta = 4;                        // tiles whose scales are kept
+    static constexpr int kQBytes = MT * 128 * D * 2;
+    static constexpr int kGroups = kTile / 32;             // 32 rows of a tile: one warp's copy
+    static constexpr int kThreads = 384;
+    // TMEM columns: S slots, then O of each row tile
+    static constexpr int kColO = 2 * kTile;
+    static constexpr int kCols = 512;
+    static constexpr int kOffRing = kQBytes;
+    static constexpr int kOffKs = kOffRing + kStages * kTileBytes;
+    static constexpr int kOffVs = kOffKs + kMeta * kTile * 4;
+    static constexpr int kOffMask = kOffVs + kMeta * kTile * 4;
+    static constexpr int kOffExp = kOffMask + kMeta * 16;
+    static constexpr int kOffBar = kOffExp + kMeta * 16;
+    static constexpr int kUsed = kOffBar + (2 * kStages + 6) * 8 + 16;
+    // one CTA per SM (each takes all of TMEM)
+    static constexpr int kSmem = (kUsed > 120 * 1024 ? kUsed : 120 * 1024) + 1024;
+};
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, int count)
+{
+    asm volatile("mbarrier.init.shared.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, int parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+// Bounded wait: gives up (for the whole CTA) after some seconds at most.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, int parity, volatile int* failed)
+{
+    if (mbar_try(bar, parity))
+        return;
+    for (int i = 0; i < (1 << 20); ++i) {
+        if (mbar_try(bar, parity))
+            return;
+        if ((i & 255) == 255 && *failed)
+            return;
+    }
+    *failed = 1;
+}
+
+__device__ __forceinline__ void fence_async_smem()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_load32(float* f, uint32_t addr)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(f);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(addr),
+           "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_load()
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Ties 32 loaded values to this point, behind the wait: nothing that uses them
+// can be scheduled before it.
+__device__ __forceinline__ void pin32(float* f)
+{
+    asm volatile(""
+        : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
+          "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]),
+          "+f"(f[16]), "+f"(f[17]), "+f"(f[18]), "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]),
+          "+f"(f[24]), "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30]), "+f"(f[31]));
+}
+
+__device__ __forceinline__ void tmem_wait_store()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(bar) : "memory");
+}
+
+// D[128 x N] (+)= A[128 x 16] B[16 x N], A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+
+// The same with A in TMEM (FP16, two per column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+
+// Shared-memory matrix descriptor: 128-byte swizzle, offsets in bytes.
+__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t leading, uint32_t stride)
+{
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(leading >> 4) << 16) |
+           ((uint64_t)(stride >> 4) << 32) | (1ULL << 46) | (2ULL << 61);
+}
+
+// Instruction descriptor: FP16 x FP16 -> FP32, M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool bIsNMajor)
+{
+    return (1u << 4) | ((bIsNMajor ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+// Position of 16-byte chunk c (8 dims) of row r in a tile of `rows` rows: blocks
+// of 64 dims, rows of 128 bytes, chunks permuted by the row within eight.
+__device__ __forceinline__ uint32_t tile_pos(int rows, int r, int c)
+{
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+template <int D, int FMT, int MT>
+__global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ Args a)
+{
+    using C = PrefixConfig<D, FMT, MT>;
+    constexpr int TN = C::kTile, NS = C::kStages, GP = C::kGroups;
+    constexpr int kEsize = FMT == kF16 ? 2 : 1;
+    extern __shared__ uint8_t smemRaw[];
+    const uint32_t rawAddr = smem_u32(smemRaw);
+    const uint32_t base = (rawAddr + 1023u) & ~1023u;
+    uint8_t* smem = smemRaw + (base - rawAddr);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const uint32_t bars = base + C::kOffBar;
+    const uint32_t kvFull = bars, kvEmpty = bars + NS * 8, sFull = bars + 2 * NS * 8,
+                   pFull = sFull + 16, oDone = pFull + 16;
+    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffBar + (2 * NS + 6) * 8);
+    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + (2 * NS + 6) * 8 + 8);
+
+    // blockIdx.x = (row tile * Hkv + head) * parts + part
+    const int part = blockIdx.x % a.numParts;
+    const int unit = blockIdx.x / a.numParts;
+    const int h = unit % a.Hkv;
+    const int row0 = (unit / a.Hkv) * (MT * 128);
+    const int tilesAll = (a.P + TN - 1) / TN;
+    const int perPart = (tilesAll + a.numParts - 1) / a.numParts;
+    const int tile0 = part * perPart;
+    const int J = max(0, min(tilesAll, tile0 + perPart) - tile0);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(kvFull + 8 * i, GP);
+            mbar_init(kvEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sFull + 8 * i, 1);
+            mbar_init(pFull + 8 * i, 128);
+            mbar_init(oDone + 8 * i, 1);
+        }
+        *failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tmemSlot)), "n"(C::kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // Q, zeros past the last row
+    for (int i = threadIdx.x; i < MT * 128 * (D / 8); i += C::kThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        const int row = row0 + r;
+        const bool ok = row < a.rowsPrefix;
+        const size_t tok = ok ? row / a.G : 0;
+        const int g = ok ? row % a.G : 0;
+        copy16(base + (r >> 7) * (128 * D * 2) + tile_pos(128, r & 127, c),
+               a.q + (tok * a.Hq + h * a.G + g) * D + c * 8, ok);
+    }
+    copy_commit();
+    copy_wait<0>();
+    fence_async_smem();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *tmemSlot;
+    const int items = MT * J;
+
+    if (warp == 8) {
+        // ------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t descS = mma_desc(TN, false), descO = mma_desc(D, true);
+            auto issue_s = [&](int i) {
+                const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
+                const int st = (2 * j) % NS;
+                if (tile == 0)
+                    mbar_wait(kvFull + 8 * st, ((2 * j) / NS) & 1, failed);
+                tmem_fence_after();
+                const uint32_t qa = base + tile * (128 * D * 2);
+                const uint32_t ka = base + C::kOffRing + st * C::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tmem + (i & 1) * TN,
+                           matrix_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
+                           matrix_desc(ka + (k >> 2) * (TN * 128) + (k & 3) * 32, 16, 1024),
+                           descS, k > 0);
+                mma_commit(sFull + 8 * (i & 1));
+                if (tile == MT - 1 && 2 * j + NS < 2 * J)  // the stage will be filled again
+                    mma_commit(kvEmpty + 8 * st);
+            };
+            auto issue_o = [&](int i) {
+                const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
+                const int st = (2 * j + 1) % NS;
+                mbar_wait(pFull + 8 * (i & 1), (i >> 1) & 1, failed);
+                if (tile == 0)
+                    mbar_wait(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed);
+                tmem_fence_after();
+                const uint32_t va = base + C::kOffRing + st * C::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < TN / 16; ++k)
+                    mma_ts(tmem + C::kColO + tile * D, tmem + (i & 1) * TN + k * 8,
+                           matrix_desc(va + k * 2048, TN * 128, 1024), descO, j > 0 || k > 0);
+                mma_commit(oDone + 8 * (i & 1));
+                if (tile == MT - 1 && 2 * j + 1 + NS < 2 * J)
+                    mma_commit(kvEmpty + 8 * st);
+            };
+            if (items > 0)
+                issue_s(0);
+            if (items > 1)
+                issue_s(1);
+            for (int i = 0; i < items; ++i) {
+                issue_o(i);
+                if (i + 2 < items)
+                    issue_s(i + 2);
+            }
+        }
+    } else if (warp > 8) {
+        // ------------------------------------------------------- page fetch
+        const int me = warp - 9;
+        const int groups = 2 * J * GP;
+        const size_t rowStride = (size_t)a.Hkv * D * kEsize;
+        const uint8_t* headBase = a.pool + (size_t)h * D * kEsize;
+        constexpr int kVecs = D * kEsize / 16;         // 16-byte vectors of a row
+        constexpr int kPerLane = kVecs;                // 32 rows of kVecs vectors over 32 lanes
+
+        int idK = -1, idV = -1;                        // page ids of this lane's row of a group
+        auto fetch_ids = [&](int u) {
+            idK = idV = -1;
+            const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
+            if (u < groups && pos < a.P) {
+                const int lp = pos / a.tpp;
+                idK = __ldg(a.prefixTable + lp);
+                idV = __ldg(a.prefixTable + a.prefixPages + lp);
+            }
+        };
+        // Row of the pool for this lane's token and the mask of mapped tokens; for K
+        // groups also the token's scales.
+        auto locate = [&](int u, uint32_t& mask) -> uint32_t {
+            const int t = u / GP, g = u % GP;
+            const int pos = (tile0 + (t >> 1)) * TN + g * 32 + lane;
+            const bool ok = idK >= 0 && idK < a.numPages && idV >= a.numPages &&
+                            idV - a.numPages < a.numPages;
+            mask = __ballot_sync(0xffffffffu, ok);
+            const int inPage = pos % a.tpp;
+            return ok ? (uint32_t)((t & 1) ? idV : idK) * (uint32_t)a.tpp + inPage : 0u;
+        };
+        // 8-bit: the scales of a K group's tokens (K's times c, V's), fetched with the ids' group
+        auto write_meta = [&](int u, uint32_t mask, float ks, float vs) {
+            const int j = (u / GP) >> 1, g = u % GP, slot = j % C::kMeta;
+            if (FMT != kF16) {
+                reinterpret_cast<float*>(smem + C::kOffKs)[slot * TN + g * 32 + lane] = ks * a.scaleLog2;
+                reinterpret_cast<float*>(smem + C::kOffVs)[slot * TN + g * 32 + lane] = vs;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs) & 0x7fffffffu);
+                if (lane == 0)
+                    reinterpret_cast<int*>(smem + C::kOffExp)[slot * 4 + g] = (int)(top >> 23) - 127;
+            }
+            if (lane == 0)
+                reinterpret_cast<uint32_t*>(smem + C::kOffMask)[slot * 4 + g] = mask;
+        };
+        auto wait_empty = [&](int u) {
+            const int t = u / GP;
+            if (t >= NS)
+                mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
+            __syncwarp();
+        };
+        auto publish = [&](int u) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(kvFull + 8 * ((u / GP) % NS));
+        };
+
+        fetch_ids(me);
+        if (FMT == kF16) {
+            int pending = -1;
+            for (int u = me; u < groups; u += 3) {
+                uint32_t mask;
+                const uint32_t row = locate(u, mask);
+                fetch_ids(u + 3);
+                wait_empty(u);
+                const uint32_t dst = base + C::kOffRing + ((u / GP) % NS) * C::kTileBytes;
+                const int r0 = (u % GP) * 32;
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) {
+                    const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
+                    const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                    copy16(dst + tile_pos(TN, r0 + r, c), headBase + (size_t)src * rowStride + c * 16,
+                           (mask >> r) & 1);
+                }
+                copy_commit();
+                if (!((u / GP) & 1))
+                    write_meta(u, mask, 0.0f, 0.0f);
+                if (pending >= 0) {
+                    copy_wait<1>();
+                    publish(pending);
+                }
+                pending = u;
+            }
+            copy_wait<0>();
+            if (pending >= 0)
+                publish(pending);
+        } else {
+            uint4 buf[kPerLane];
+            float ks = 0.0f, vs = 0.0f;
+            uint32_t mask = 0;
+            auto load = [&](int u) {
+                const uint32_t row = locate(u, mask);
+                ks = vs = 0.0f;
+                if (!((u / GP) & 1) && ((mask >> lane) & 1)) {
+                    const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
+                    const int inPage = pos % a.tpp;
+                    ks = __ldg(a.scales + ((size_t)idK * a.Hkv + h) * a.tpp + inPage);
+                    vs = __ldg(a.scales + ((size_t)idV * a.Hkv + h) * a.tpp + inPage);
+                }
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) {
+                    const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
+                    const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                    buf[i] = make_uint4(0, 0, 0, 0);
+                    if ((mask >> r) & 1)
+                        buf[i] = __ldg(reinterpret_cast<const uint4*>(headBase + (size_t)src * rowStride + c * 16));
+                }
+            };
+            if (me < groups)
+                load(me);
+            fetch_ids(me + 3);
+            for (int u = me; u < groups; u += 3) {
+                uint4 cur[kPerLane];
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i)
+                    cur[i] = buf[i];
+                const uint32_t curMask = mask;
+                const float curK = ks, curV = vs;
+                if (u + 3 < groups)
+                    load(u + 3);
+                fetch_ids(u + 6);
+                wait_empty(u);
+                uint8_t* dst = smem + C::kOffRing + ((u / GP) % NS) * C::kTileBytes;
+                const int r0 = (u % GP) * 32;
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) {
+                    const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
+                    const bool ok = (curMask >> r) & 1;   // zeros, not codes of zero, where unmapped
+                    const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = ok ? decode_pair<FMT, 0x10>(w[k]) : 0u;
+                        o[2 * k + 1] = ok ? decode_pair<FMT, 0x32>(w[k]) : 0u;
+                    }
+                    *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                if (!((u / GP) & 1))
+                    write_meta(u, curMask, curK, curV);
+                publish(u);
+            }
+        }
+    } else if (warp < 4 * MT) {
+        // ----------------------------------------------------------- softmax
+        const int tile = warp >> 2;
+        const uint32_t laneBase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t oAddr = laneBase + C::kColO + tile * D;
+        float M = -INFINITY, l = 0.0f;
+        for (int j = 0; j < J; ++j) {
+            const int i = MT == 2 ? 2 * j + tile : j;
+            const int slot = i & 1;
+            const uint32_t sAddr = laneBase + slot * TN;
+            mbar_wait(sFull + 8 * slot, (i >> 1) & 1, failed);
+            __syncwarp();
+            tmem_fence_after();
+            float s[TN];
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k)
+                tmem_load32(s + 32 * k, sAddr + 32 * k);
+            const int meta = j % C::kMeta;
+            const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kOffMask) + meta * 4;
+            const float* ks = reinterpret_cast<const float*>(smem + C::kOffKs) + meta * TN;
+            const float* vs = reinterpret_cast<const float*>(smem + C::kOffVs) + meta * TN;
+            uint32_t all = 0xffffffffu;
+#pragma unroll
+            for (int g = 0; g < GP; ++g)
+                all &= mask[g];
+            int e = 0;
+            if (FMT != kF16) {
+                e = -60;
+#pragma unroll
+                for (int g = 0; g < GP; ++g)
+                    e = max(e, reinterpret_cast<const int*>(smem + C::kOffExp)[meta * 4 + g]);
+                e = min(e, 40);
+            }
+            tmem_wait_load();
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k)
+                pin32(s + 32 * k);
+            if (FMT != kF16) {
+#pragma unroll
+                for (int k = 0; k < TN; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(ks + k);
+                    s[k] *= f.x; s[k + 1] *= f.y; s[k + 2] *= f.z; s[k + 3] *= f.w;
+                }
+            } else {
+                // the sign of c decides between maximum and minimum, so scale first
+#pragma unroll
+                for (int k = 0; k < TN; ++k)
+                    s[k] *= a.scaleLog2;
+            }
+            if (all != 0xffffffffu) {
+#pragma unroll
+                for (int k = 0; k < TN; ++k)
+                    s[k] = (mask[k >> 5] >> (k & 31)) & 1 ? s[k] : -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < TN; ++k)
+                top = fmaxf(top, s[k]);
+            top += (float)e;
+            if (__any_sync(0xffffffffu, top > M + 8.0f)) {
+                const float next = fmaxf(M, top);
+                const float f = M == next ? 1.0f : exp2_fast(M - next);
+                M = next;
+                l *= f;
+                if (j > 0) {
+                    // O of this row tile is at rest: its last product has finished
+                    if (MT == 1)
+                        mbar_wait(oDone + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, failed);
+                    else
+                        mbar_wait(oDone + 8 * slot, ((i >> 1) - 1) & 1, failed);
+                    __syncwarp();
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        float o[32];
+                        tmem_load32(o, oAddr + k);
+                        tmem_wait_load();
+                        pin32(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] *= f;
+                        tmem_store32(oAddr + k, reinterpret_cast<const uint32_t*>(o));
+                    }
+                    tmem_wait_store();
+                }
+            }
+            const float mm = M == -INFINITY ? 0.0f : M;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < TN; k += 64) {
+                uint32_t p[32];
+#pragma unroll
+                for (int x = 0; x < 64; x += 4) {
+                    float v[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        v[y] = exp2_fast(s[k + x + y] - mm);
+                        sum[y] += v[y];
+                    }
+                    if (FMT != kF16) {
+                        const float4 f = *reinterpret_cast<const float4*>(vs + k + x);
+                        v[0] *= f.x; v[1] *= f.y; v[2] *= f.z; v[3] *= f.w;
+                    }
+                    p[x / 2] = half2_bits(v[0], v[1]);
+                    p[x / 2 + 1] = half2_bits(v[2], v[3]);
+                }
+                tmem_store32(sAddr + k / 2, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_store();
+            tmem_fence_before();
+            mbar_arrive(pFull + 8 * slot);
+        }
+        // the last products of this row tile
+        if (J > 0) {
+            const int last = MT == 2 ? 2 * (J - 1) + tile : J - 1;
+            if (MT == 1 && last > 0)
+                mbar_wait(oDone + 8 * ((last - 1) & 1), ((last - 1) >> 1) & 1, failed);
+            mbar_wait(oDone + 8 * (last & 1), (last >> 1) & 1, failed);
+        }
+        __syncwarp();
+        tmem_fence_after();
+        const int row = row0 + (int)threadIdx.x;       // threads 0..127: tile 0, 128..255: tile 1
+        const bool live = row < a.rowsPrefix;
+        const size_t r = ((size_t)part * a.Hkv + h) * a.rowsPrefix + (live ? row : 0);
+        const bool none = J == 0 || l == 0.0f;
+        const float inv = none ? 0.0f : 1.0f / l;
+        const float bad = *failed ? __int_as_float(0x7fc00000) : 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            float o[32];
+            if (J > 0) {
+                tmem_load32(o, oAddr + k);
+                tmem_wait_load();
+                pin32(o);
+            }
+            if (live) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<float4*>(a.partO + r * D + k + x) =
+                        none ? make_float4(bad, bad, bad, bad)
+                             : make_float4(o[x] * inv + bad, o[x + 1] * inv + bad, o[x + 2] * inv + bad, o[x + 3] * inv + bad);
+            }
+        }
+        if (live)
+            a.partL[r] = none ? -INFINITY + bad : M + log2f(l) + bad;
+        tmem_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                     :: "r"(tmem), "n"(C::kCols));
+    }
+}
+
+}  // namespace ropekv_attn

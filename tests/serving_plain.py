@@ -136,8 +136,8 @@ class AttentionCase:
         x = decode(self.pool, self.fmt)
         return x if self.scales is None else x * self.scales.astype(np.float64).transpose(0, 1, 3, 2)[..., None]
 
-    def solve(self, sm_scale=None):
-        """(out, lse, tol_out, tol_lse) in 64 bits.
+    def solve(self, sm_scale=None, batch=None):
+        """(out, lse, tol_out, tol_lse) in 64 bits, of the sequences in `batch` (default: all).
 
         Bounds, with s the scores in natural units, w = softmax, N positions:
           score: D products of FP16 values are exact, their FP32 sum (tensor cores may
@@ -166,7 +166,7 @@ class AttentionCase:
                     vs.append(kv[1, j, p % self.tpp])
             return ks, vs
         pre = rows(self.prefix_table, 0, self.P)
-        for b in range(self.B):
+        for b in range(self.B) if batch is None else batch:
             mine = rows(self.page_table[b], self.P, int(self.kv_lens[b]))
             ks, vs = pre[0] + mine[0], pre[1] + mine[1]
             if not ks:

@@ -90,6 +90,42 @@ def test_shapes(idx, fmt):
     run(AttentionCase(400 + idx, *SHAPES[idx], fmt))
 
 
+LONG = [
+    # enough row tiles that one CTA walks many tiles of the prefix: B, S, Hq, Hkv, D, tpp, prefix
+    (25, 200, 8, 8, 64, 16, 1500),
+    (40, 250, 4, 4, 128, 64, 1111),
+    (38, 256, 2, 2, 256, 32, 705),
+    (100, 1, 160, 160, 64, 16, 700),
+]
+
+
+@pytest.mark.parametrize("fmt", [F16, E4M3, INT8])
+@pytest.mark.parametrize("idx", range(len(LONG)))
+def test_many_prefix_tiles_per_cta(idx, fmt):
+    B, S, Hq, Hkv, D, tpp, P = LONG[idx]
+    c = AttentionCase(450 + idx, B, S, Hq, Hkv, D, tpp, P, [S + i % 7 for i in range(B)], fmt,
+                      q_scale=2.0, unmapped=0.1 if idx == 1 else 0.0)
+    # scores that grow along the prefix move the running maximum again and again
+    grow = np.linspace(0.2, 4.0, P)
+    for p in range(P):
+        page = c.prefix_table[0, p // tpp]
+        if 0 <= page < c.pages:
+            if fmt == F16:
+                c.pool[0, page, p % tpp] *= np.float16(grow[p])
+            else:
+                c.scales[0, page, :, p % tpp] *= np.float32(grow[p])
+    t = tensors(c)
+    call(c, t)
+    torch.cuda.synchronize()
+    pick = [0, B // 2, B - 1]
+    out, lse, tol_o, tol_l = c.solve(batch=pick)
+    got, gl = t["out"].cpu().numpy().astype(np.float64), t["lse"].cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all() and np.isfinite(gl).all()
+    err, el = np.abs(got - out)[pick], np.abs(gl - lse)[pick]
+    assert (err <= tol_o[pick]).all(), float((err / tol_o[pick]).max())
+    assert (el <= tol_l[pick]).all(), float((el / tol_l[pick]).max())
+
+
 @pytest.mark.parametrize("fmt", [F16, E4M3, INT8])
 @pytest.mark.parametrize("B,S,G,D", [(5, 1, 4, 128), (3, 4, 2, 64), (24, 2, 8, 128), (20, 1, 2, 256)])
 def test_unmapped_pages_and_inactive_sequences(B, S, G, D, fmt):
