@@ -64,11 +64,11 @@ bool raise_smem(int bytes)
 }
 
 // CTAs of a cluster that share one tile's tokens: enough of them for two CTAs
-// per SM, but at least four warps' steps of 16 tokens for each.
-int cluster_size(long long tiles, long long tokens)
+// per SM, but at least one step of 16 tokens for each of their warps.
+int cluster_size(long long tiles, long long tokens, int warps)
 {
     int c = 1;
-    while (c < 8 && tiles * c < 2 * kSMs && tokens > 64LL * c)
+    while (c < ropekv_attn::kMaxCluster && tiles * c < 2 * kSMs && tokens > 16LL * warps * c)
         c *= 2;
     return c;
 }
@@ -80,12 +80,13 @@ int launch_rows(const Args& a, long long tiles, long long tokens, bool dependent
     constexpr int smem = RowsConfig<D, FMT, NT>::kSmem;
     if (!raise_smem<kern>(smem))
         return ROPEKV_ERR_LAUNCH;
-    const int c = cluster_size(tiles, tokens);
+    constexpr int warps = RowsConfig<D, FMT, NT>::kWarps;
+    const int c = cluster_size(tiles, tokens, warps);
     if (tiles * c > 0x7FFFFFFFLL)
         return ROPEKV_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -136,7 +137,7 @@ PrefixPlan plan_prefix(const ropekv_attention_dims* d)
     const long long units = (long long)plan.tiles * d->numKVHeads;
     const long long kv = ((long long)d->prefixLen + tokens - 1) / tokens;
     double best = 1e30;
-    for (int p = 1; p <= 32 && p <= kv; ++p) {
+    for (int p = 1; p <= ropekv_attn::kMaxParts && p <= kv; ++p) {
         const double waves = (double)((units * p + kSMs - 1) / kSMs);
         const double cost = waves * ((double)((kv + p - 1) / p) + 3.0) + 0.25 * p;
         if (cost < best) {
@@ -164,7 +165,16 @@ int launch_prefix(const Args& a, long long ctas, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
 
-// Rows per tile: 8 columns waste nothing for a GQA group of up to 8 rows.
+// The sequences' own tokens: tiles of 8 rows, or of 16 or 32 (D = 256: 16) where
+// a sequence has more, so that its tokens are fetched once.
+template <int D, int FMT, int NT>
+int launch_own(Args& a, bool dependent, cudaStream_t st)
+{
+    a.tilesPerUnit = (a.S * a.G + 8 * NT - 1) / (8 * NT);
+    const long long own = (long long)a.mpps * a.tpp - a.P;
+    return launch_rows<D, FMT, NT, false>(a, (long long)a.B * a.tilesPerUnit * a.Hkv, own, dependent, st);
+}
+
 template <int D, int FMT>
 int launch_all(Args a, const PrefixPlan& plan, cudaStream_t st)
 {
@@ -184,10 +194,14 @@ int launch_all(Args a, const PrefixPlan& plan, cudaStream_t st)
     }
     if (rc != ROPEKV_OK)
         return rc;
-    a.tilesPerUnit = (a.S * a.G + 7) / 8;
-    const long long own = (long long)a.mpps * a.tpp - a.P;
-    return launch_rows<D, FMT, 1, false>(a, (long long)a.B * a.tilesPerUnit * a.Hkv, own,
-                                         plan.parts > 0, st);
+    const int rows = a.S * a.G;
+    if (rows <= 8)
+        return launch_own<D, FMT, 1>(a, plan.parts > 0, st);
+    if constexpr (D != 256) {
+        if (rows > 16)
+            return launch_own<D, FMT, 4>(a, plan.parts > 0, st);
+    }
+    return launch_own<D, FMT, 2>(a, plan.parts > 0, st);
 }
 
 template <int D>

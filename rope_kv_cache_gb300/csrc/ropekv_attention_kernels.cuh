@@ -152,7 +152,7 @@ __device__ __forceinline__ int swizzle(int r, int c)
 // S^T's accumulator layout has tokens down and rows across; two movmatrix
 // transposes per 16 tokens make it the B operand of the second product.
 //
-// A CTA is four warps that never meet until the end: each walks its own steps
+// A CTA is a few warps that never meet until the end: each walks its own steps
 // of 16 tokens with its own ring of cp.async stages and its own (m, l, O). The
 // page ids of a step are fetched one step before its copies are issued. Steps
 // begin at multiples of 16 positions. The tokens of one tile are split over the
@@ -164,32 +164,48 @@ __device__ __forceinline__ int swizzle(int r, int c)
 // instead of the shuffles of a maximum and no rescaling.
 //
 // 8-bit caches: the codes go into the products as FP16 (exact); a token's K
-// scale multiplies its scores, its V scale its weights 2^(s - m). To keep those
-// products inside FP16's range whatever the scales, a warp divides them by the
-// largest power of two seen so far (eV) and multiplies it back at the end.
+// scale multiplies its scores, its V scale its weights 2^(s - m). With 2^e the
+// largest V scale of a step, m follows max(s) + e instead of max(s): weight times
+// scale stays below 2^9 whatever the scales, and as l and O share m nothing has
+// to be undone at the end.
 // The order of dims inside a k-step of the first product is that in which
 // ldmatrix delivers bytes (lane j: codes 4j..4j+3); Q's fragments follow it.
+constexpr int kMaxParts = 32;    // prefix partials at most
+constexpr int kMaxCluster = 8;
+
+// Exponent of the largest of a step's V scales, kept where 2^(s - m) cannot leave FP32.
+__device__ __forceinline__ int scale_exponent(uint32_t bits)
+{
+    return max(-60, min(40, (int)(bits >> 23) - 127));
+}
+
 template <int D, int FMT, int NT>
 struct RowsConfig {
     static constexpr int kEsize = FMT == kF16 ? 2 : 1;
     static constexpr int kRowBytes = D * kEsize;
     static constexpr int kChunks = kRowBytes / 16;
-    static constexpr int kStages = kRowBytes >= 256 ? 3 : 4;
+    static constexpr int kWarps = kRowBytes > 256 ? 2 : 4;
+    static constexpr int kStages = 3;
     static constexpr int kStageBytes = 32 * kRowBytes + 256;  // K, V, 32 scales, mask
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kMaxCluster = 8;
-    // partials of four warps (aliasing the stages), then (m, l) and join weights
-    static constexpr int kPartBytes = 4 * kRows * D * 4;
-    static constexpr int kRing = 4 * kWarpBytes > kPartBytes ? 4 * kWarpBytes : kPartBytes;
-    static constexpr int kSmem = kRing + 4 * kRows * 8 + 4 * kMaxCluster * kRows * 4 + kRows * 8;
+    static constexpr int kPitch = D + 4;                      // floats of a partial's row
+    // the warps' partials alias the stages; then (m, l) and join weights of every partial
+    static constexpr int kPartBytes = kWarps * kRows * kPitch * 4;
+    static constexpr int kRing = kWarps * kWarpBytes > kPartBytes ? kWarps * kWarpBytes : kPartBytes;
+    static constexpr int kMaxPartials = kWarps * kMaxCluster + kMaxParts;
+    static constexpr int kOffMl = kRing;
+    static constexpr int kOffAll = kOffMl + kWarps * kRows * 8;
+    static constexpr int kOffTotal = kOffAll + kMaxPartials * kRows * 8;
+    static constexpr int kSmem = kOffTotal + kRows * 8;
 };
 
 template <int D, int FMT, int NT, bool PREFIX>
-__global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(RowsConfig<D, FMT, NT>::kWarps * 32)
+rows_kernel(const __grid_constant__ Args a)
 {
     using C = RowsConfig<D, FMT, NT>;
-    constexpr int kRowBytes = C::kRowBytes, kChunks = C::kChunks, kRows = C::kRows;
+    constexpr int kRowBytes = C::kRowBytes, kChunks = C::kChunks, kRows = C::kRows, W = C::kWarps;
     constexpr int MT = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     cg::cluster_group cluster = cg::this_cluster();
@@ -225,12 +241,10 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
     };
 
     const int lo = PREFIX ? 0 : a.P;
-    int hi = a.P;
-    bool diagonal = false;  // rows of the tile see different positions
+    int hi = a.P, last0 = a.P - 1;
     if (!PREFIX) {
-        const int nLast = min(kRows, rowsOfUnit - row0) - 1;
-        hi = max(lo, last_of(nLast) + 1);
-        diagonal = last_of(0) != last_of(nLast);
+        hi = max(lo, last_of(min(kRows, rowsOfUnit - row0) - 1) + 1);
+        last0 = last_of(0);       // the rows of the tile see different positions from here on
     }
     const int firstStep = lo >> 4;
     const int steps = hi > lo ? ((hi + 15) >> 4) - firstStep : 0;
@@ -280,6 +294,16 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
             *reinterpret_cast<uint32_t*>(ring + stage * C::kStageBytes + 32 * kRowBytes + 128) = ok;
     };
 
+    // ---- ring: kStages - 1 steps in flight, ids one step further ahead
+    int id = fetch_id(stepBegin);
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+        const int next = fetch_id(stepBegin + W * (i + 1));
+        issue(stepBegin + W * i, i, id);
+        copy_commit();
+        id = next;
+    }
+
     // Q as B fragments: column n = lane / 4, k = (lane % 4) * 2 + {0, 1} (+8).
     uint32_t qf[NT][MT][2];
     int lastCol[NT][2];
@@ -303,7 +327,6 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
 
     float acc[NT][MT][4];
     float m[NT][2], l[NT][2];
-    int eV = 1;  // biased exponent of the power of two that divides the V scales
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -313,22 +336,13 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
         l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    // ---- ring: kStages - 1 steps in flight, ids one step further ahead
-    int id = fetch_id(stepBegin);
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-        const int next = fetch_id(stepBegin + 4 * (i + 1));
-        issue(stepBegin + 4 * i, i, id);
-        copy_commit();
-        id = next;
-    }
     int stage = 0, fill = C::kStages - 1;
-    for (int step = stepBegin; step < stepEnd; step += 4) {
+    for (int step = stepBegin; step < stepEnd; step += W) {
         copy_wait<C::kStages - 2>();
         __syncwarp();
         {
-            const int ahead = step + 4 * (C::kStages - 1);
-            const int next = fetch_id(ahead + 4);
+            const int ahead = step + W * (C::kStages - 1);
+            const int next = fetch_id(ahead + W);
             issue(ahead, fill, id);
             copy_commit();
             id = next;
@@ -375,10 +389,14 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
         const int t0 = lane >> 2;
         const int pos0 = step * 16 + t0;
         const bool okA = (ok >> t0) & 1, okB = (ok >> (t0 + 8)) & 1;
-        float ks0 = a.scaleLog2, ks1 = a.scaleLog2;
+        float ks0 = a.scaleLog2, ks1 = a.scaleLog2, vs0 = 1.0f, vs1 = 1.0f, e = 0.0f;
         if (FMT != kF16) {
             ks0 *= sc[t0];
             ks1 *= sc[t0 + 8];
+            vs0 = sc[16 + t0];
+            vs1 = sc[16 + t0 + 8];
+            e = (float)scale_exponent(__reduce_max_sync(
+                0xffffffffu, max(__float_as_uint(vs0) & 0x7fffffffu, __float_as_uint(vs1) & 0x7fffffffu)));
         }
         bool grow = false;
 #pragma unroll
@@ -387,7 +405,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
             for (int j = 0; j < 2; ++j) {
                 s[nt][j] = okA && pos0 <= lastCol[nt][j] ? s[nt][j] * ks0 : -INFINITY;
                 s[nt][2 + j] = okB && pos0 + 8 <= lastCol[nt][j] ? s[nt][2 + j] * ks1 : -INFINITY;
-                grow = grow || fmaxf(s[nt][j], s[nt][2 + j]) > m[nt][j] + 8.0f;
+                grow = grow || fmaxf(s[nt][j], s[nt][2 + j]) + e > m[nt][j] + 8.0f;
             }
         }
         if (__any_sync(0xffffffffu, grow)) {
@@ -399,7 +417,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    const float top = fmaxf(m[nt][j], x);
+                    const float top = fmaxf(m[nt][j], x + e);
                     const float f = m[nt][j] == top ? 1.0f : exp2_fast(m[nt][j] - top);
                     m[nt][j] = top;
                     l[nt][j] *= f;
@@ -410,29 +428,6 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
                     }
                 }
             }
-        }
-
-        // V scales as multiples of 2^(eV - 127)
-        float vs0 = 1.0f, vs1 = 1.0f;
-        if (FMT != kF16) {
-            vs0 = sc[16 + t0];
-            vs1 = sc[16 + t0 + 8];
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(vs0), __float_as_uint(vs1)) & 0x7fffffffu);
-            const int e = min((int)(top >> 23), 252);
-            if (e > eV) {
-                const float f = exp2_fast((float)(eV - e));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[nt][mt][j] *= f;
-                eV = e;
-            }
-            const float inv = __uint_as_float((uint32_t)(254 - eV) << 23);
-            vs0 *= inv;
-            vs1 *= inv;
         }
 
         // P^T as the B operand (columns: rows of Q; k: the step's 16 tokens)
@@ -455,7 +450,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
         // Where rows see different tokens a weight of 0 can meet an infinity or
         // NaN in V that another row sees: such values are taken out of the tile
         // and added to the rows that do see them.
-        if (!PREFIX && diagonal && step * 16 + 15 > last_of(0)) {
+        if (!PREFIX && last0 + 1 < hi && step * 16 + 15 > last0) {
             auto value = [&](int t, int d) -> float {
                 const uint8_t* p = stagePtr + 16 * kRowBytes +
                     swizzle<kChunks>(t, d * C::kEsize / 16) + (d * C::kEsize) % 16;
@@ -465,8 +460,8 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
                 return __half2float(__ushort_as_half((unsigned short)(two & 0xffff)));
             };
             bool bad = false;
-            for (int e = lane; e < 16 * D; e += 32)
-                bad = bad || !(fabsf(value(e / D, e % D)) < INFINITY);
+            for (int x = lane; x < 16 * D; x += 32)
+                bad = bad || !(fabsf(value(x / D, x % D)) < INFINITY);
             if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -476,6 +471,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
                         for (int j = 0; j < 4; ++j) {
                             const int d = mt * 16 + (FMT == kF16 ? (lane >> 2) + (j >> 1) * 8
                                                                  : (lane >> 2) * 2 + (j >> 1));
+#pragma unroll 1
                             for (int t = 0; t < 16; ++t) {
                                 const float v = value(t, d);
                                 if (!(fabsf(v) < INFINITY) && ((ok >> t) & 1) &&
@@ -484,8 +480,8 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
                             }
                         }
                 __syncwarp();
-                for (int e = lane; e < 16 * D; e += 32) {
-                    const int t = e / D, d = e % D;
+                for (int x = lane; x < 16 * D; x += 32) {
+                    const int t = x / D, d = x % D;
                     if (!(fabsf(value(t, d)) < INFINITY)) {
                         uint8_t* p = stagePtr + 16 * kRowBytes +
                             swizzle<kChunks>(t, d * C::kEsize / 16) + (d * C::kEsize) % 16;
@@ -533,12 +529,10 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
 
     // ---- join: warps and ranks through (distributed) shared memory
     __syncthreads();  // every warp is done with its ring, which the partials reuse
-    float* part = reinterpret_cast<float*>(smem);                       // [4][kRows][D]
-    float2* ml = reinterpret_cast<float2*>(smem + C::kRing);            // [4][kRows]
-    float* weight = reinterpret_cast<float*>(smem + C::kRing + 4 * kRows * 8);  // [4 * ranks][kRows]
-    float2* total = reinterpret_cast<float2*>(smem + C::kRing + 4 * kRows * 8 +
-                                              4 * C::kMaxCluster * kRows * 4);  // [kRows]: max, sum
-    const float unscale = FMT == kF16 ? 1.0f : exp2_fast((float)(eV - 127));
+    float* part = reinterpret_cast<float*>(smem);                           // [W][kRows][kPitch]
+    float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);               // [W][kRows]
+    float2* all = reinterpret_cast<float2*>(smem + C::kOffAll);             // [partials][kRows]: m, l, then weights
+    float2* total = reinterpret_cast<float2*>(smem + C::kOffTotal);         // [kRows]: max, sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -557,7 +551,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
                 const int n = nt * 8 + (lane & 3) * 2 + (j & 1);
                 const int d = mt * 16 + (FMT == kF16 ? (lane >> 2) + (j >> 1) * 8
                                                      : (lane >> 2) * 2 + (j >> 1));
-                part[(warp * kRows + n) * D + d] = acc[nt][mt][j] * unscale;
+                part[(warp * kRows + n) * C::kPitch + d] = acc[nt][mt][j];
             }
     }
     if (!PREFIX)  // the prefix partials, and everything before them, are complete
@@ -567,57 +561,71 @@ __global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args 
     else
         __syncthreads();
 
-    for (int n = threadIdx.x; n < kRows; n += 128) {
-        float top = -INFINITY;
-        for (int i = 0; i < 4 * ranks; ++i) {
-            const float2* p = ranks > 1 ? cluster.map_shared_rank(ml, i >> 2) : ml;
-            top = fmaxf(top, p[(i & 3) * kRows + n].x);
-        }
-        const bool seen = !PREFIX && last_of(n) != kNoRow;
-        const size_t r = (size_t)h * a.rowsPrefix + (size_t)unit * a.S * a.G + row0 + n;
-        const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
-        if (seen)
-            for (int j = 0; j < a.numParts; ++j)
-                top = fmaxf(top, a.partL[j * partStride + r]);
+    // Every partial's (m, l) of every row, the prefix's as (m + log2 l, 1)
+    const int own = W * ranks, partials = own + (PREFIX ? 0 : a.numParts);
+    const size_t headRow = (size_t)h * a.rowsPrefix + (PREFIX ? 0 : (size_t)unit * a.S * a.G) + row0;
+    const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
+    const int rowsHere = min(kRows, rowsOfUnit - row0);
+    for (int i = threadIdx.x; i < partials * kRows; i += W * 32) {
+        const int k = i / kRows, n = i % kRows;
+        float2 v = make_float2(-INFINITY, 0.0f);
+        if (k < own)
+            v = (ranks > 1 ? cluster.map_shared_rank(ml, k / W) : ml)[(k % W) * kRows + n];
+        else if (n < rowsHere && last_of(n) != kNoRow)
+            v = make_float2(a.partL[(size_t)(k - own) * partStride + headRow + n], 1.0f);
+        all[i] = v;
+    }
+    __syncthreads();
+    for (int n = threadIdx.x; n < kRows; n += W * 32) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < partials; ++k)
+            top = fmaxf(top, all[k * kRows + n].x);
         const float mm = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-        for (int i = 0; i < 4 * ranks; ++i) {
-            const float2* p = ranks > 1 ? cluster.map_shared_rank(ml, i >> 2) : ml;
-            const float2 v = p[(i & 3) * kRows + n];
+#pragma unroll 4
+        for (int k = 0; k < partials; ++k) {
+            const float2 v = all[k * kRows + n];
             const float w = exp2_fast(v.x - mm);
-            weight[i * kRows + n] = w;
+            all[k * kRows + n].x = w;
             sum += w * v.y;
         }
-        if (seen)
-            for (int j = 0; j < a.numParts; ++j)
-                sum += exp2_fast(a.partL[j * partStride + r] - mm);
         total[n] = make_float2(mm, sum);
     }
     __syncthreads();
 
-    const int rowsHere = min(kRows, rowsOfUnit - row0);
-    for (int e = rank * 128 + (int)threadIdx.x; e < rowsHere * D; e += ranks * 128) {
-        const int n = e / D, d = e % D;
-        float o = 0.0f;
-        for (int i = 0; i < 4 * ranks; ++i) {
-            const float* p = ranks > 1 ? cluster.map_shared_rank(part, i >> 2) : part;
-            o += weight[i * kRows + n] * p[((i & 3) * kRows + n) * D + d];
+    for (int f = rank * W * 32 + (int)threadIdx.x; f < rowsHere * (D / 4); f += ranks * W * 32) {
+        const int n = f / (D / 4), d = f % (D / 4) * 4;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto add = [&](float w, const float4& v) {
+            o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+        };
+        for (int k = 0; k < ranks; ++k) {
+            const float* p = (ranks > 1 ? cluster.map_shared_rank(part, k) : part) + n * C::kPitch + d;
+#pragma unroll
+            for (int x = 0; x < W; ++x)
+                add(all[(k * W + x) * kRows + n].x, *reinterpret_cast<const float4*>(p + x * kRows * C::kPitch));
         }
         const float2 t = total[n];
-        const size_t r = (size_t)h * a.rowsPrefix + (PREFIX ? 0 : (size_t)unit * a.S * a.G) + row0 + n;
+        const float inv = t.y == 0.0f ? 0.0f : 1.0f / t.y;
         if (PREFIX) {
-            a.partO[r * D + d] = t.y == 0.0f ? 0.0f : o / t.y;
+            *reinterpret_cast<float4*>(a.partO + (headRow + n) * D + d) =
+                t.y == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                            : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             if (d == 0)
-                a.partL[r] = t.y == 0.0f ? -INFINITY : t.x + log2f(t.y);
+                a.partL[headRow + n] = t.y == 0.0f ? -INFINITY : t.x + log2f(t.y);
         } else {
-            const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
-            if (last_of(n) != kNoRow)
-                for (int j = 0; j < a.numParts; ++j)
-                    o += exp2_fast(a.partL[j * partStride + r] - t.x) * a.partO[(j * partStride + r) * D + d];
+            if (last_of(n) != kNoRow) {
+#pragma unroll 4
+                for (int k = 0; k < a.numParts; ++k)
+                    add(all[(own + k) * kRows + n].x, *reinterpret_cast<const float4*>(
+                            a.partO + (k * partStride + headRow + n) * D + d));
+            }
             const size_t y = (size_t)token_of(n) * a.Hq + h * a.G + (row0 + n) % a.G;
-            a.out[y * D + d] = __half_as_ushort(__float2half_rn(t.y == 0.0f ? 0.0f : o / t.y));
+            const bool none = t.y == 0.0f;
+            *reinterpret_cast<uint2*>(a.out + y * D + d) =
+                none ? make_uint2(0, 0) : make_uint2(half2_bits(o.x * inv, o.y * inv), half2_bits(o.z * inv, o.w * inv));
             if (d == 0 && a.lse != nullptr)
-                a.lse[y] = t.y == 0.0f ? -INFINITY : kLn2 * (t.x + log2f(t.y));
+                a.lse[y] = none ? -INFINITY : kLn2 * (t.x + log2f(t.y));
         }
     }
     if (ranks > 1)

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                 reinterpret_cast<float*>(smem + C::kOffVs)[slot * TN + g * 32 + lane] = vs;
                 const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs) & 0x7fffffffu);
                 if (lane == 0)
-                    reinterpret_cast<int*>(smem + C::kOffExp)[slot * 4 + g] = (int)(top >> 23) - 127;
+                    reinterpret_cast<int*>(smem + C::kOffExp)[slot * 4 + g] = scale_exponent(top);
             }
             if (lane == 0)
                 reinterpret_cast<uint32_t*>(smem + C::kOffMask)[slot * 4 + g] = mask;
@@ -487,7 +487,6 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int g = 0; g < GP; ++g)
                     e = max(e, reinterpret_cast<const int*>(smem + C::kOffExp)[meta * 4 + g]);
-                e = min(e, 40);
             }
             tmem_wait_load();
 #pragma unroll
