@@ -125,8 +125,8 @@ typedef struct {
     int32_t cacheFormat;    /* a ropekv_cache_format                                */
 } ropekv_attention_dims;
 
-/* Bytes of workspace that paged_attention_shared_prefix needs for these sizes
- * (0 when prefixLen is 0), or a negative ropekv_status. Host only. */
+/* Bytes of workspace that paged_attention_shared_prefix needs for these sizes,
+ * or a negative ropekv_status. Host only. */
 ROPEKV_API int64_t paged_attention_workspace_size(const ropekv_attention_dims* dims);
 
 /*

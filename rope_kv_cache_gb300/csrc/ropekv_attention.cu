@@ -14,8 +14,9 @@
 namespace {
 
 using ropekv_attn::Args;
+using ropekv_attn::make_divisor;
 using ropekv_attn::PrefixConfig;
-using ropekv_attn::RowsConfig;
+using ropekv_attn::StreamConfig;
 
 constexpr int kSMs = 152;
 
@@ -63,161 +64,181 @@ bool raise_smem(int bytes)
     return true;
 }
 
-// CTAs of a cluster that share one tile's tokens: enough of them for two CTAs
-// per SM, but at least one step of 16 tokens for each of their warps.
-int cluster_size(long long tiles, long long tokens, int warps)
+template <typename Kern, typename... A>
+int launch(Kern kern, long long grid, int threads, int smem, bool dependent, cudaStream_t st, const A&... args)
 {
-    int c = 1;
-    while (c < ropekv_attn::kMaxCluster && tiles * c < 2 * kSMs && tokens > 16LL * warps * c)
-        c *= 2;
-    return c;
-}
-
-template <int D, int FMT, int NT, bool PREFIX>
-int launch_rows(const Args& a, long long tiles, long long tokens, bool dependent, cudaStream_t st)
-{
-    constexpr auto kern = ropekv_attn::rows_kernel<D, FMT, NT, PREFIX>;
-    constexpr int smem = RowsConfig<D, FMT, NT>::kSmem;
-    if (!raise_smem<kern>(smem))
-        return ROPEKV_ERR_LAUNCH;
-    constexpr int warps = RowsConfig<D, FMT, NT>::kWarps;
-    const int c = cluster_size(tiles, tokens, warps);
-    if (tiles * c > 0x7FFFFFFFLL)
+    if (grid > 0x7FFFFFFFLL)
         return ROPEKV_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * c));
-    cfg.blockDim = dim3(warps * 32);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (c > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = c;
-        attr[n].val.clusterDim.y = 1;
-        attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (dependent) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = dependent ? attr : nullptr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
 
-// How the prefix is cut: `tensor` rows take tcgen05 tiles of 128 (or 2 x 128)
-// rows, fewer take the rows kernel, whose cluster leaves one partial.
-struct PrefixPlan {
-    bool tensor;
-    int tiles;   // row tiles per KV head
-    int parts;   // ranges of the prefix = partials in the workspace
+// How a call is cut into launches, from its sizes alone.
+struct Plan {
+    int nt;             // row tiles of the stream kernel: 8, 16 or 32 rows
+    bool tensor;        // the prefix goes to the tensor-core kernel
+    int parts;          // its ranges of the prefix
+    int prefixTiles;    // its row tiles per KV head
+    int tilesPrefix;    // row tiles of the stream kernel's prefix unit (0: none)
+    int tilesSeq;       // and of a sequence
+    int pitch;
+    int ctas, warps;    // stream grid
+    int64_t partRows, slots, units;
 };
 
-// Ranges of the prefix: their number p minimises the K/V tiles that the busiest
-// SM walks, waves(units * p) * ceil(tiles / p), where each CTA costs about three
-// tiles more to start and to write its partial.
-PrefixPlan plan_prefix(const ropekv_attention_dims* d)
+int stream_warps(int D, int fmt, int nt);
+
+// Tiles of 8 rows, or of 16 or 32 (D = 256: 16 at most) where a sequence has
+// more, so that its tokens are fetched once. The prefix joins the stream if all
+// rows of a KV head fit into one such tile.
+// Ranges of a tensor-core prefix: their number p minimises the K/V tiles that the
+// busiest SM walks, waves(units * p) * ceil(tiles / p), where each CTA costs about
+// three tiles more to start and to write its partial.
+Plan make_plan(const ropekv_attention_dims* d)
 {
-    PrefixPlan plan = {false, 0, 0};
-    if (d->prefixLen <= 0 || d->batch == 0 || d->seqLen == 0)
-        return plan;
-    const long long rows = (long long)d->batch * d->seqLen * (d->numQHeads / d->numKVHeads);
-    plan.tensor = rows > 8;
-    plan.parts = 1;
-    if (!plan.tensor) {
-        plan.tiles = (int)((rows + 7) / 8);
-        return plan;
-    }
-    const int tileRows = d->headDim != 256 && rows > 128 ? 256 : 128;
-    const int tokens = d->headDim == 256 ? 64 : 128;
-    plan.tiles = (int)((rows + tileRows - 1) / tileRows);
-    const long long units = (long long)plan.tiles * d->numKVHeads;
-    const long long kv = ((long long)d->prefixLen + tokens - 1) / tokens;
-    double best = 1e30;
-    for (int p = 1; p <= ropekv_attn::kMaxParts && p <= kv; ++p) {
-        const double waves = (double)((units * p + kSMs - 1) / kSMs);
-        const double cost = waves * ((double)((kv + p - 1) / p) + 3.0) + 0.25 * p;
-        if (cost < best) {
-            best = cost;
-            plan.parts = p;
+    Plan p = {};
+    const long long G = d->numQHeads / d->numKVHeads, rowsSeq = d->seqLen * G, rows = d->batch * rowsSeq;
+    p.nt = rowsSeq <= 8 ? 1 : rowsSeq <= 16 || d->headDim == 256 ? 2 : 4;
+    p.tilesSeq = (int)((rowsSeq + 8 * p.nt - 1) / (8 * p.nt));
+    p.tensor = d->prefixLen > 0 && rows > 8 * p.nt;
+    p.tilesPrefix = d->prefixLen > 0 && !p.tensor ? 1 : 0;
+    const long long longest = p.tilesPrefix ? rows : rowsSeq;
+    p.pitch = (int)(longest < 8 * p.nt ? longest : 8 * p.nt);
+    p.units = d->batch + p.tilesPrefix;
+    // the table's capacity bounds the steps; at least two of them make a share
+    const long long own = (long long)d->maxPagesPerSeq * d->tokensPerPage - d->prefixLen;
+    const long long items = (long long)d->batch * p.tilesSeq * d->numKVHeads;
+    const long long steps = items * (own > 0 ? own / 16 + 2 : 0) +
+                            (p.tilesPrefix ? (long long)d->numKVHeads * (d->prefixLen / 16 + 1) : 0);
+    p.ctas = (int)(steps / 2 < 1 ? 1 : steps / 2 < kSMs ? steps / 2 : kSMs);
+    p.warps = p.ctas * stream_warps(d->headDim, d->cacheFormat, p.nt);
+    p.slots = items + (long long)p.tilesPrefix * d->numKVHeads + p.warps;
+    if (p.tensor) {
+        const int tileRows = d->headDim != 256 && rows > 128 ? 256 : 128;
+        const int tokens = d->headDim == 256 ? 64 : 128;
+        p.prefixTiles = (int)((rows + tileRows - 1) / tileRows);
+        const long long units = (long long)p.prefixTiles * d->numKVHeads;
+        const long long kv = ((long long)d->prefixLen + tokens - 1) / tokens;
+        double best = 1e30;
+        for (int k = 1; k <= ropekv_attn::kMaxParts && k <= kv; ++k) {
+            const double waves = (double)((units * k + kSMs - 1) / kSMs);
+            const double cost = waves * ((double)((kv + k - 1) / k) + 3.0) + 0.25 * k;
+            if (cost < best) {
+                best = cost;
+                p.parts = k;
+            }
         }
+        p.partRows = (int64_t)p.parts * d->numKVHeads * rows;
     }
-    return plan;
+    return p;
+}
+
+// Workspace: partO, partL, segO, segL, offsets, each on a 256-byte boundary.
+struct Layout {
+    int64_t partL, segO, segL, offsets, size;
+};
+
+Layout make_layout(const Plan& p, int D)
+{
+    auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    Layout w;
+    w.partL = up(p.partRows * D * 4);
+    w.segO = w.partL + up(p.partRows * 4);
+    w.segL = w.segO + up(p.slots * p.pitch * D * 4);
+    w.offsets = w.segL + up(p.slots * p.pitch * 4);
+    w.size = w.offsets + up((p.units + 2) * 8);
+    return w;
 }
 
 template <int D, int FMT, int MT>
-int launch_prefix(const Args& a, long long ctas, cudaStream_t st)
+int launch_prefix(const Args& a, const Plan& p, cudaStream_t st)
 {
     constexpr auto kern = ropekv_attn::prefix_kernel<D, FMT, MT>;
     using C = PrefixConfig<D, FMT, MT>;
     if (!raise_smem<kern>(C::kSmem))
         return ROPEKV_ERR_LAUNCH;
-    if (ctas > 0x7FFFFFFFLL)
-        return ROPEKV_ERR_SHAPE;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
+    return launch(kern, (long long)p.prefixTiles * a.Hkv * p.parts, C::kThreads, C::kSmem, false, st, a);
 }
 
-// The sequences' own tokens: tiles of 8 rows, or of 16 or 32 (D = 256: 16) where
-// a sequence has more, so that its tokens are fetched once.
 template <int D, int FMT, int NT>
-int launch_own(Args& a, bool dependent, cudaStream_t st)
+int launch_stream(const Args& a, const Plan& p, cudaStream_t st)
 {
-    a.tilesPerUnit = (a.S * a.G + 8 * NT - 1) / (8 * NT);
-    const long long own = (long long)a.mpps * a.tpp - a.P;
-    return launch_rows<D, FMT, NT, false>(a, (long long)a.B * a.tilesPerUnit * a.Hkv, own, dependent, st);
+    constexpr auto kern = ropekv_attn::stream_kernel<D, FMT, NT>;
+    using C = StreamConfig<D, FMT, NT>;
+    if (!raise_smem<kern>(C::kSmem))
+        return ROPEKV_ERR_LAUNCH;
+    return launch(kern, p.ctas, C::kWarps * 32, C::kSmem, p.tensor, st, a);
 }
 
 template <int D, int FMT>
-int launch_all(Args a, const PrefixPlan& plan, cudaStream_t st)
+int launch_all(const Args& a, const Plan& p, cudaStream_t st)
 {
     int rc = ROPEKV_OK;
-    a.numParts = plan.parts;
-    if (plan.tensor) {
-        const long long ctas = (long long)plan.tiles * a.Hkv * plan.parts;
+    if (p.tensor) {
         if constexpr (D != 256) {
-            rc = a.rowsPrefix > 128 ? launch_prefix<D, FMT, 2>(a, ctas, st)
-                                    : launch_prefix<D, FMT, 1>(a, ctas, st);
+            rc = a.rowsPrefix > 128 ? launch_prefix<D, FMT, 2>(a, p, st) : launch_prefix<D, FMT, 1>(a, p, st);
         } else {
-            rc = launch_prefix<D, FMT, 1>(a, ctas, st);
+            rc = launch_prefix<D, FMT, 1>(a, p, st);
         }
-    } else if (plan.parts > 0) {
-        a.tilesPerUnit = plan.tiles;
-        rc = launch_rows<D, FMT, 1, true>(a, (long long)plan.tiles * a.Hkv, a.P, false, st);
     }
     if (rc != ROPEKV_OK)
         return rc;
-    const int rows = a.S * a.G;
-    if (rows <= 8)
-        return launch_own<D, FMT, 1>(a, plan.parts > 0, st);
-    if constexpr (D != 256) {
-        if (rows > 16)
-            return launch_own<D, FMT, 4>(a, plan.parts > 0, st);
-    }
-    return launch_own<D, FMT, 2>(a, plan.parts > 0, st);
+    if (p.nt == 1)
+        rc = launch_stream<D, FMT, 1>(a, p, st);
+    else if (p.nt == 2)
+        rc = launch_stream<D, FMT, 2>(a, p, st);
+    else if constexpr (D != 256)
+        rc = launch_stream<D, FMT, 4>(a, p, st);
+    if (rc != ROPEKV_OK)
+        return rc;
+    // few rows whose items many warps share: all groups of a CTA join one row
+    const long long rows = (long long)a.B * a.S * a.Hq;
+    constexpr int perCta = 1024 / D;
+    if (rows < 4LL * kSMs)
+        return launch(ropekv_attn::join_kernel<D, true>, rows, 256, 0, true, st, a, 8 * p.nt);
+    return launch(ropekv_attn::join_kernel<D, false>, (rows + perCta - 1) / perCta, 256, 0, true, st, a, 8 * p.nt);
 }
 
 template <int D>
-int dispatch(const Args& a, const PrefixPlan& plan, int fmt, cudaStream_t st)
+int dispatch(const Args& a, const Plan& p, int fmt, cudaStream_t st)
 {
     switch (fmt) {
-    case ROPEKV_CACHE_F16: return launch_all<D, ROPEKV_CACHE_F16>(a, plan, st);
-    case ROPEKV_CACHE_E4M3: return launch_all<D, ROPEKV_CACHE_E4M3>(a, plan, st);
-    default: return launch_all<D, ROPEKV_CACHE_INT8>(a, plan, st);
+    case ROPEKV_CACHE_F16: return launch_all<D, ROPEKV_CACHE_F16>(a, p, st);
+    case ROPEKV_CACHE_E4M3: return launch_all<D, ROPEKV_CACHE_E4M3>(a, p, st);
+    default: return launch_all<D, ROPEKV_CACHE_INT8>(a, p, st);
     }
 }
 
-int64_t workspace_size(const ropekv_attention_dims* d, const PrefixPlan& plan)
+template <int D, int FMT>
+int stream_warps_nt(int nt)
 {
-    const int64_t rows = (int64_t)d->batch * d->seqLen * d->numQHeads * plan.parts;
-    return rows * d->headDim * 4 + (rows * 4 + 15) / 16 * 16;
+    if constexpr (D != 256) {
+        if (nt == 4)
+            return StreamConfig<D, FMT, 4>::kWarps;
+    }
+    return nt == 1 ? StreamConfig<D, FMT, 1>::kWarps : StreamConfig<D, FMT, 2>::kWarps;
+}
+
+template <int D>
+int stream_warps_fmt(int fmt, int nt)
+{
+    return fmt == ROPEKV_CACHE_F16 ? stream_warps_nt<D, ROPEKV_CACHE_F16>(nt)
+                                   : stream_warps_nt<D, ROPEKV_CACHE_E4M3>(nt);
+}
+
+int stream_warps(int D, int fmt, int nt)
+{
+    return D == 64 ? stream_warps_fmt<64>(fmt, nt) : D == 128 ? stream_warps_fmt<128>(fmt, nt)
+                                                              : stream_warps_fmt<256>(fmt, nt);
 }
 
 }  // namespace
@@ -229,7 +250,9 @@ int64_t paged_attention_workspace_size(const ropekv_attention_dims* dims)
     const int rc = check_dims(dims);
     if (rc != ROPEKV_OK)
         return rc;
-    return workspace_size(dims, plan_prefix(dims));
+    if (dims->batch == 0 || dims->seqLen == 0)
+        return 0;
+    return make_layout(make_plan(dims), dims->headDim).size;
 }
 
 int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const float* kvScales,
@@ -245,18 +268,18 @@ int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const 
         return ROPEKV_ERR_SHAPE;
     if (dims->batch == 0 || dims->seqLen == 0)
         return ROPEKV_OK;
-    const PrefixPlan plan = plan_prefix(dims);
-    const int64_t need = workspace_size(dims, plan);
+    const Plan plan = make_plan(dims);
+    const Layout at = make_layout(plan, dims->headDim);
     const bool f16 = dims->cacheFormat == ROPEKV_CACHE_F16;
     if (!q || !kvLens || !out || (!kvCache && dims->numPages > 0) ||
         (!f16 && !kvScales && dims->numPages > 0) || (!prefixTable && dims->prefixLen > 0) ||
-        (!pageTable && dims->maxPagesPerSeq > 0) || (!workspace && need > 0))
+        (!pageTable && dims->maxPagesPerSeq > 0) || !workspace)
         return ROPEKV_ERR_NULL_POINTER;
     if (!aligned16(q) || !aligned16(kvCache) || !aligned16(kvScales) || !aligned16(prefixTable) ||
         !aligned16(pageTable) || !aligned16(kvLens) || !aligned16(out) || !aligned16(lse) ||
         !aligned16(workspace))
         return ROPEKV_ERR_MISALIGNED;
-    if (workspaceBytes < need)
+    if (workspaceBytes < at.size)
         return ROPEKV_ERR_CAPACITY;
     Args a = {};
     a.q = q;
@@ -279,8 +302,22 @@ int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const 
     a.P = dims->prefixLen;
     a.prefixPages = dims->maxPrefixPages;
     a.rowsPrefix = dims->batch * dims->seqLen * a.G;
-    a.partO = (float*)workspace;
-    a.partL = a.partO + (size_t)plan.parts * a.rowsPrefix * a.Hkv * dims->headDim;
+    uint8_t* ws = (uint8_t*)workspace;
+    a.partO = (float*)ws;
+    a.partL = (float*)(ws + at.partL);
+    a.segO = (float*)(ws + at.segO);
+    a.segL = (float*)(ws + at.segL);
+    a.offsets = (long long*)(ws + at.offsets);
+    a.numParts = plan.parts;
+    a.prefixUnit = plan.tilesPrefix;
+    a.tilesPrefix = plan.tilesPrefix;
+    a.tilesSeq = plan.tilesSeq;
+    a.pitch = plan.pitch;
+    a.warps = plan.warps;
+    a.divTpp = make_divisor(a.tpp);
+    a.divG = make_divisor(a.G);
+    a.divHkv = make_divisor(a.Hkv);
+    a.divS = make_divisor(a.S);
     cudaStream_t st = (cudaStream_t)stream;
     switch (dims->headDim) {
     case 64: return dispatch<64>(a, plan, dims->cacheFormat, st);

@@ -5,7 +5,7 @@
 //   s_t = c * (q . k_t),  m = max s_t,  l = sum 2^(s_t - m),
 //   out = sum 2^(s_t - m) v_t / l,      lse = ln 2 * (m + log2 l).
 // Any split of the positions can be reduced on its own to (m, l, O) and joined
-// later: that is how warps, the CTAs of a cluster and the two parts below meet.
+// later, which is how the parts below meet.
 //
 // Two parts. The prefix is the same for all sequences, so for one KV head all
 // B * S * G query rows (G = Hq / Hkv) multiply the same K and V: each byte of it
@@ -13,7 +13,6 @@
 // tokens are read by its S * G rows alone, which is bound by HBM.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
@@ -22,10 +21,29 @@
 
 namespace ropekv_attn {
 
-namespace cg = cooperative_groups;
-
 constexpr int kF16 = ROPEKV_CACHE_F16, kE4M3 = ROPEKV_CACHE_E4M3, kInt8 = ROPEKV_CACHE_INT8;
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// n / d for 0 <= n < 2^31: a multiplication and a shift (multiplier
+// ceil(2^p / d), p = 31 + ceil(log2 d): the excess n * (m d - 2^p) stays below 2^p).
+struct Divisor {
+    uint32_t mul, shift;
+    int32_t d;
+};
+
+inline Divisor make_divisor(int32_t d)
+{
+    uint32_t c = 0;
+    while ((1LL << c) < d)
+        ++c;
+    const uint64_t m = ((1ULL << (31 + c)) + (uint64_t)d - 1) / (uint64_t)d;
+    return {(uint32_t)m, 31 + c, d};
+}
+
+__device__ __forceinline__ int divide(int n, const Divisor& v)
+{
+    return (int)(((uint64_t)(uint32_t)n * v.mul) >> v.shift);
+}
 
 struct Args {
     const uint16_t* q;           // [B, S, Hq, D]
@@ -36,13 +54,23 @@ struct Args {
     const int32_t* kvLens;       // [B]
     uint16_t* out;               // [B, S, Hq, D]
     float* lse;                  // [B, S, Hq] or NULL
-    float* partO;                // [numParts, Hkv, B*S*G, D]  prefix partials, each divided by its sum
-    float* partL;                // [numParts, Hkv, B*S*G]     m + log2(l) of each
+    // partial results: O divided by its sum, and m + log2(l)
+    float* partO;                // [numParts, Hkv, B*S*G, D]  ranges of the prefix (tensor cores)
+    float* partL;                // [numParts, Hkv, B*S*G]
+    float* segO;                 // [slots, pitch, D]          segments of the streamed tokens
+    float* segL;                 // [slots, pitch]
+    long long* offsets;          // [units + 2]: first step of each unit, their sum, steps per warp
     float scaleLog2;             // smScale * log2(e)
     int32_t B, S, Hq, Hkv, G, numPages, tpp, mpps, P, prefixPages;
     int32_t rowsPrefix;          // B * S * G
-    int32_t numParts;            // prefix partials (0: no prefix)
-    int32_t tilesPerUnit;        // row tiles of a sequence (own tokens) or of the batch (prefix)
+    int32_t numParts;            // prefix partials of the tensor cores
+    // streamed units: the prefix (if it is not on the tensor cores), then the sequences
+    int32_t prefixUnit;          // 1: unit 0 is the prefix
+    int32_t tilesPrefix;         // row tiles of the prefix unit (0 without one)
+    int32_t tilesSeq;            // row tiles of a sequence
+    int32_t pitch;               // rows of a segment's slot
+    int32_t warps;               // warps of the stream grid
+    Divisor divTpp, divG, divHkv, divS;
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -62,6 +90,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copy16_full(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok)
@@ -142,7 +175,7 @@ __device__ __forceinline__ int swizzle(int r, int c)
     return (r * CPR + (CPR >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3)))) * 16;
 }
 
-// ------------------------------------------------------------ rows kernel --
+// ---------------------------------------------------------- stream kernel --
 //
 // Few query rows against a stream of tokens: bound by HBM, so the matrix
 // products only have to keep up. They are taken transposed, S^T = K Q^T and
@@ -152,206 +185,304 @@ __device__ __forceinline__ int swizzle(int r, int c)
 // S^T's accumulator layout has tokens down and rows across; two movmatrix
 // transposes per 16 tokens make it the B operand of the second product.
 //
-// A CTA is a few warps that never meet until the end: each walks its own steps
-// of 16 tokens with its own ring of cp.async stages and its own (m, l, O). The
-// page ids of a step are fetched one step before its copies are issued. Steps
-// begin at multiples of 16 positions. The tokens of one tile are split over the
-// CTAs of a cluster (grid x = tile * cluster + rank), and the cluster's warps
-// join through distributed shared memory.
+// Work. A unit is a sequence's own tokens (or the prefix, when few rows share
+// it), an item one row tile and KV head of a unit, a step 16 tokens of an item
+// (steps begin at multiples of 16 positions). All steps of all items form one
+// sequence, and every warp of a persistent grid takes an equal share of it,
+// whatever the lengths: lengths are on the device, so each CTA sums them first.
+// A warp's share covers the end of an item, whole items, the start of another:
+// its segments. Warps never wait for one another. A warp's ring of cp.async
+// stages runs ahead across segment borders, so the loads do not drain between
+// items; page ids are fetched a step before the copies that need them. Each
+// segment leaves (O / l, m + log2 l) in slot item + warp, which no other segment
+// has, as the next segment in order has a larger item or a larger warp.
 //
 // m follows the maximum lazily: it moves only when a score exceeds it by more
 // than 8 (2^8 stays far inside FP16 and FP32), so most steps need one vote
 // instead of the shuffles of a maximum and no rescaling.
 //
 // 8-bit caches: the codes go into the products as FP16 (exact); a token's K
-// scale multiplies its scores, its V scale its weights 2^(s - m). With 2^e the
-// largest V scale of a step, m follows max(s) + e instead of max(s): weight times
-// scale stays below 2^9 whatever the scales, and as l and O share m nothing has
-// to be undone at the end.
+// scale multiplies its scores, its V scale its weights 2^(s - m). With e_t the
+// exponent of token t's V scale, m follows max(s_t + e_t) instead of max(s_t):
+// weight times scale stays below 2^9, and the largest near 1, whatever the
+// scales; as l and O share m nothing has to be undone at the end.
 // The order of dims inside a k-step of the first product is that in which
 // ldmatrix delivers bytes (lane j: codes 4j..4j+3); Q's fragments follow it.
 constexpr int kMaxParts = 32;    // prefix partials at most
-constexpr int kMaxCluster = 8;
 
-// Exponent of the largest of a step's V scales, kept where 2^(s - m) cannot leave FP32.
-__device__ __forceinline__ int scale_exponent(uint32_t bits)
+// Exponent of a V scale, kept where 2^(s - m) cannot leave FP32.
+__device__ __forceinline__ float scale_exponent(float scale)
 {
-    return max(-60, min(40, (int)(bits >> 23) - 127));
+    return (float)max(-60, min(40, (int)((__float_as_uint(scale) >> 23) & 0xff) - 127));
 }
 
 template <int D, int FMT, int NT>
-struct RowsConfig {
+struct StreamConfig {
     static constexpr int kEsize = FMT == kF16 ? 2 : 1;
     static constexpr int kRowBytes = D * kEsize;
     static constexpr int kChunks = kRowBytes / 16;
-    static constexpr int kWarps = kRowBytes > 256 ? 2 : 4;
     static constexpr int kStages = 3;
-    static constexpr int kStageBytes = 32 * kRowBytes + 256;  // K, V, 32 scales, mask
+    static constexpr int kMeta = 32 * kRowBytes;              // K, V, then 32 scales, meta
+    static constexpr int kStageBytes = 32 * kRowBytes + 256;
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kPitch = D + 4;                      // floats of a partial's row
-    // the warps' partials alias the stages; then (m, l) and join weights of every partial
-    static constexpr int kPartBytes = kWarps * kRows * kPitch * 4;
-    static constexpr int kRing = kWarps * kWarpBytes > kPartBytes ? kWarps * kWarpBytes : kPartBytes;
-    static constexpr int kMaxPartials = kWarps * kMaxCluster + kMaxParts;
-    static constexpr int kOffMl = kRing;
-    static constexpr int kOffAll = kOffMl + kWarps * kRows * 8;
-    static constexpr int kOffTotal = kOffAll + kMaxPartials * kRows * 8;
-    static constexpr int kSmem = kOffTotal + kRows * 8;
+    // one CTA per SM, its warps limited by shared memory and by registers (accumulators)
+    static constexpr int kBySmem = 210 * 1024 / kWarpBytes;
+    static constexpr int kByRegs = NT * D <= 128 ? 16 : 8;
+    static constexpr int kFit = kBySmem < kByRegs ? kBySmem : kByRegs;
+    static constexpr int kWarps = kFit >= 16 ? 16 : kFit >= 8 ? 8 : 4;
+    static constexpr int kOffScan = kWarps * kWarpBytes;
+    static constexpr int kSmem = kOffScan + (kWarps * 32 + 1) * 8 + kWarps * 8;
 };
 
-template <int D, int FMT, int NT, bool PREFIX>
-__global__ void __launch_bounds__(RowsConfig<D, FMT, NT>::kWarps * 32)
-rows_kernel(const __grid_constant__ Args a)
+// Tokens of unit u: positions [lo, hi).
+__device__ __forceinline__ void unit_range(const Args& a, int u, int& lo, int& hi)
 {
-    using C = RowsConfig<D, FMT, NT>;
-    constexpr int kRowBytes = C::kRowBytes, kChunks = C::kChunks, kRows = C::kRows, W = C::kWarps;
-    constexpr int MT = D / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ranks = (int)cluster.num_blocks();
-    const int rank = (int)cluster.block_rank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (PREFIX)
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    const int tile = blockIdx.x / ranks;
-    const int h = tile % a.Hkv;
-    const int unitTile = tile / a.Hkv;
-    const int unit = unitTile / a.tilesPerUnit;          // sequence (0 for the prefix)
-    const int row0 = (unitTile - unit * a.tilesPerUnit) * kRows;
-    const int rowsOfUnit = PREFIX ? a.rowsPrefix : a.S * a.G;
-
-    // The token (b * S + s) of row n of the tile, or -1.
-    auto token_of = [&](int n) {
-        const int r = row0 + n;
-        return r < rowsOfUnit ? (PREFIX ? 0 : unit * a.S) + r / a.G : -1;
-    };
-    // Last position that the row sees; kNoRow for rows that are not there or lie before P.
-    constexpr int kNoRow = -2;
-    const int tableEnd = max(a.mpps * a.tpp, a.P);
-    auto last_of = [&](int n) {
-        const int tok = token_of(n);
-        if (tok < 0)
-            return kNoRow;
-        const int b = tok / a.S;
-        const long long p = (long long)__ldg(a.kvLens + b) - a.S + (tok - b * a.S);
-        return p < a.P ? kNoRow : (int)min(p, (long long)tableEnd - 1);
-    };
-
-    const int lo = PREFIX ? 0 : a.P;
-    int hi = a.P, last0 = a.P - 1;
-    if (!PREFIX) {
-        hi = max(lo, last_of(min(kRows, rowsOfUnit - row0) - 1) + 1);
-        last0 = last_of(0);       // the rows of the tile see different positions from here on
+    if (u < a.prefixUnit) {
+        lo = 0;
+        hi = a.P;
+    } else {
+        lo = a.P;
+        hi = max(a.P, min(__ldg(a.kvLens + u - a.prefixUnit), a.mpps * a.tpp));
     }
-    const int firstStep = lo >> 4;
-    const int steps = hi > lo ? ((hi + 15) >> 4) - firstStep : 0;
-    const int perRank = (steps + ranks - 1) / ranks;
-    const int stepEnd = firstStep + min(steps, (rank + 1) * perRank);
-    const int stepBegin = firstStep + rank * perRank + warp;
+}
 
-    const int32_t* table = PREFIX ? a.prefixTable : a.pageTable + (size_t)unit * 2 * a.mpps;
-    const int planeStride = PREFIX ? a.prefixPages : a.mpps;
-    const uint8_t* headBase = a.pool + (size_t)h * kRowBytes;
-    const size_t rowStride = (size_t)a.Hkv * kRowBytes;
+__device__ __forceinline__ int unit_steps(int lo, int hi)
+{
+    return hi > lo ? ((hi + 15) >> 4) - (lo >> 4) : 0;
+}
+
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(StreamConfig<D, FMT, NT>::kWarps * 32, 1)
+stream_kernel(const __grid_constant__ Args a)
+{
+    using C = StreamConfig<D, FMT, NT>;
+    constexpr int kRowBytes = C::kRowBytes, kChunks = C::kChunks, kRows = C::kRows;
+    constexpr int MT = D / 16, NS = C::kStages, T = C::kWarps * 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = a.B + a.prefixUnit;
+
+    // ---- shares: sum of all units' steps, then this warp's range
+    long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);   // [T + 1] exclusive sums
+    long long* warpSum = scan + T + 1;
+    const int perThread = (units + T - 1) / T;
+    auto weight = [&](int u) -> long long {
+        int lo, hi;
+        unit_range(a, u, lo, hi);
+        return (long long)unit_steps(lo, hi) * ((u < a.prefixUnit ? a.tilesPrefix : a.tilesSeq) * (long long)a.Hkv);
+    };
+    const int u0 = min(units, (int)threadIdx.x * perThread), u1 = min(units, u0 + perThread);
+    long long mine = 0;
+    for (int u = u0; u < u1; ++u)
+        mine += weight(u);
+    long long sum = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, x);
+        if (lane >= x)
+            sum += y;
+    }
+    if (lane == 31)
+        warpSum[warp] = sum;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int x = 0; x < C::kWarps; ++x) {
+        before += x < warp ? warpSum[x] : 0;
+        total += warpSum[x];
+    }
+    scan[threadIdx.x] = before + sum - mine;
+    const long long share = max(2LL, (total + a.warps - 1) / a.warps);
+    if (blockIdx.x == 0) {
+        long long at = before + sum - mine;
+        for (int u = u0; u < u1; ++u) {
+            a.offsets[u] = at;
+            at += weight(u);
+        }
+        if (threadIdx.x == 0) {
+            a.offsets[units] = total;
+            a.offsets[units + 1] = share;
+        }
+    }
+    __syncthreads();
+
+    // warps next to one another in the sequence of steps sit on different SMs
+    const int w = warp * gridDim.x + blockIdx.x;
+    const long long begin = w * share;
+    const long long count = max(0LL, min(total - begin, share));
 
     uint8_t* ring = smem + warp * C::kWarpBytes;
     const uint32_t ringAddr = smem_u32(ring);
+    const size_t rowStride = (size_t)a.Hkv * kRowBytes;
+    const bool pagesAligned = a.tpp % 16 == 0;
+    // where this lane copies from inside 16 consecutive rows, and to
+    const size_t laneSrc = (size_t)(lane / kChunks) * rowStride + (lane % kChunks) * 16;
 
-    // Page id of this lane's token of a step (lanes 0..15: K plane, 16..31: V plane).
-    auto fetch_id = [&](int step) {
-        const int pos = step * 16 + (lane & 15);
-        return step < stepEnd && pos >= lo && pos < hi
-                   ? __ldg(table + (size_t)(lane >> 4) * planeStride + pos / a.tpp) : -1;
+    // ---- producer: the step to issue next
+    int pu = 0, pSub = 0, pStep = 0, pEnd = 0, pFirst = 0, pLo = 0, pHi = 0, pSubs = 1;
+    const int32_t* table = nullptr;
+    int id = -1, pHead = 0;
+    bool pNew = true;         // first step of a segment
+    auto enter_unit = [&]() {
+        unit_range(a, pu, pLo, pHi);
+        pFirst = pLo >> 4;
+        pEnd = pFirst + unit_steps(pLo, pHi);
+        pSubs = (pu < a.prefixUnit ? a.tilesPrefix : a.tilesSeq) * a.Hkv;
+        table = pu < a.prefixUnit ? a.prefixTable : a.pageTable + (size_t)(pu - a.prefixUnit) * 2 * a.mpps;
     };
-    auto issue = [&](int step, int stage, int id) {
-        if (step >= stepEnd)
-            return;
-        const int pos = step * 16 + (lane & 15);
+    // page id of this lane's token of the step (lanes 0..15: K plane, 16..31: V plane)
+    auto fetch_id = [&]() {
+        const int pos = pStep * 16 + (lane & 15);
+        const int stride = pu < a.prefixUnit ? a.prefixPages : a.mpps;
+        id = pos >= pLo && pos < pHi ? __ldg(table + (size_t)(lane >> 4) * stride + divide(pos, a.divTpp)) : -1;
+    };
+    auto issue = [&](int stage, bool isLast) {
         const int plane = lane >> 4;
+        const int pos = pStep * 16 + (lane & 15);
         const bool mapped = id >= plane * a.numPages && id - plane * a.numPages < a.numPages;
         const uint32_t both = __ballot_sync(0xffffffffu, mapped);
         const uint32_t ok = both & (both >> 16) & 0xffff;
-        const int inPage = pos % a.tpp;
+        const int inPage = pos - divide(pos, a.divTpp) * a.tpp;
         const uint32_t row = mapped ? (uint32_t)id * (uint32_t)a.tpp + inPage : 0u;
         const uint32_t base = ringAddr + stage * C::kStageBytes;
+        const uint8_t* headBase = a.pool + (size_t)pHead * kRowBytes;
+        if (pagesAligned && ok == 0xffff) {
+            // 16 consecutive rows of one K page and one V page
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            // 32 * kChunks chunks of 16 bytes: rows 0..15 are K, 16..31 V
-            const int idx = i * 32 + lane;
-            const int r = idx / kChunks, c = idx % kChunks;
-            const uint32_t src = __shfl_sync(0xffffffffu, row, r);
-            copy16(base + (r >> 4) * 16 * kRowBytes + swizzle<kChunks>(r & 15, c),
-                   headBase + (size_t)src * rowStride + c * 16, (ok >> (r & 15)) & 1);
+            for (int p = 0; p < 2; ++p) {
+                const uint8_t* src = headBase + (size_t)__shfl_sync(0xffffffffu, row, 16 * p) * rowStride + laneSrc;
+#pragma unroll
+                for (int i = 0; i < kChunks / 2; ++i) {
+                    const int r = i * (32 / kChunks) + lane / kChunks;
+                    copy16_full(base + p * 16 * kRowBytes + swizzle<kChunks>(r, lane % kChunks), src);
+                    src += (32 / kChunks) * rowStride;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                // 32 * kChunks chunks of 16 bytes: rows 0..15 are K, 16..31 V
+                const int idx = i * 32 + lane;
+                const int r = idx / kChunks, c = idx % kChunks;
+                const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                copy16(base + (r >> 4) * 16 * kRowBytes + swizzle<kChunks>(r & 15, c),
+                       headBase + (size_t)src * rowStride + c * 16, (ok >> (r & 15)) & 1);
+            }
         }
         if (FMT != kF16) {
-            const float* s = a.scales + ((size_t)(mapped ? id : 0) * a.Hkv + h) * a.tpp + (mapped ? inPage : 0);
-            copy4(base + 32 * kRowBytes + lane * 4, s, (ok >> (lane & 15)) & 1);
+            const float* s = a.scales + ((size_t)(mapped ? id : 0) * a.Hkv + pHead) * a.tpp + (mapped ? inPage : 0);
+            copy4(base + C::kMeta + lane * 4, s, (ok >> (lane & 15)) & 1);
         }
         if (lane == 0)
-            *reinterpret_cast<uint32_t*>(ring + stage * C::kStageBytes + 32 * kRowBytes + 128) = ok;
+            *reinterpret_cast<int4*>(ring + stage * C::kStageBytes + C::kMeta + 128) =
+                make_int4((int)ok | (pNew ? 1 << 16 : 0) | (isLast ? 1 << 17 : 0), pStep, pu, pSub);
     };
-
-    // ---- ring: kStages - 1 steps in flight, ids one step further ahead
-    int id = fetch_id(stepBegin);
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-        const int next = fetch_id(stepBegin + W * (i + 1));
-        issue(stepBegin + W * i, i, id);
-        copy_commit();
-        id = next;
-    }
-
-    // Q as B fragments: column n = lane / 4, k = (lane % 4) * 2 + {0, 1} (+8).
-    uint32_t qf[NT][MT][2];
-    int lastCol[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int n = nt * 8 + (lane >> 2);
-        const int tok = token_of(n);
-        const uint16_t* qr = tok < 0 ? nullptr
-            : a.q + ((size_t)tok * a.Hq + h * a.G + (row0 + n) % a.G) * D;
-#pragma unroll
-        for (int kk = 0; kk < MT; ++kk) {
-            const int d0 = kk * 16 + (FMT == kF16 ? (lane & 3) * 2 : (lane & 3) * 4);
-            const int d1 = d0 + (FMT == kF16 ? 8 : 2);
-            qf[nt][kk][0] = qr ? __ldg(reinterpret_cast<const uint32_t*>(qr + d0)) : 0u;
-            qf[nt][kk][1] = qr ? __ldg(reinterpret_cast<const uint32_t*>(qr + d1)) : 0u;
+    auto advance = [&]() {
+        pNew = false;
+        if (++pStep < pEnd)
+            return;
+        pNew = true;
+        ++pSub;
+        pHead = pHead + 1 == a.Hkv ? 0 : pHead + 1;
+        if (pSub == pSubs) {
+            pSub = 0;
+            do {
+                if (++pu >= units)
+                    return;
+                enter_unit();
+            } while (pFirst == pEnd);
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            lastCol[nt][j] = PREFIX ? a.P - 1 : last_of(nt * 8 + (lane & 3) * 2 + j);
+        pStep = pFirst;
+    };
+    if (count > 0) {
+        int chunk = 0;
+        for (int x = 0; x < T; x += 32)
+            chunk += __popc(__ballot_sync(0xffffffffu, scan[x + lane] <= begin));
+        pu = (chunk - 1) * perThread;
+        long long at = scan[chunk - 1];
+        for (;; ++pu) {
+            const long long n = weight(pu);
+            if (at + n > begin)
+                break;
+            at += n;
+        }
+        enter_unit();
+        const int n = pEnd - pFirst;
+        const long long in = begin - at;
+        pSub = (int)(in / n);
+        pStep = pFirst + (int)(in - (long long)pSub * n);
+        pHead = pSub - divide(pSub, a.divHkv) * a.Hkv;
+        fetch_id();
     }
+    long long issued = 0;
+    auto feed = [&](int stage) {
+        if (issued < count) {
+            issue(stage, pStep + 1 == pEnd || issued + 1 == count);
+            if (++issued < count) {
+                advance();
+                fetch_id();
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i)
+        feed(i);
 
+    // ---- consumer
+    uint32_t qf[NT][MT][2];
     float acc[NT][MT][4];
     float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.0f;
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.0f;
-    }
-
-    int stage = 0, fill = C::kStages - 1;
-    for (int step = stepBegin; step < stepEnd; step += W) {
-        copy_wait<C::kStages - 2>();
+    int last0 = 0, row0 = 0, rowsOfUnit = 0, base0 = 0, head = 0;
+    int stage = 0, fill = NS - 1;
+    // Last position that row n of the tile sees (-1 for rows that are not there or see nothing)
+    auto last_of = [&](int n, bool prefix) {
+        if (row0 + n >= rowsOfUnit)
+            return -1;
+        return prefix ? a.P - 1 : base0 + divide(row0 + n, a.divG);
+    };
+    for (long long it = 0; it < count; ++it) {
+        copy_wait<NS - 2>();
         __syncwarp();
-        {
-            const int ahead = step + W * (C::kStages - 1);
-            const int next = fetch_id(ahead + W);
-            issue(ahead, fill, id);
-            copy_commit();
-            id = next;
-            fill = fill + 1 == C::kStages ? 0 : fill + 1;
-        }
+        feed(fill);
+        fill = fill + 1 == NS ? 0 : fill + 1;
         const uint32_t kBase = ringAddr + stage * C::kStageBytes;
         const uint32_t vBase = kBase + 16 * kRowBytes;
         uint8_t* stagePtr = ring + stage * C::kStageBytes;
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+        stage = stage + 1 == NS ? 0 : stage + 1;
+        const int4 meta = *reinterpret_cast<const int4*>(stagePtr + C::kMeta + 128);
+        const uint32_t ok = meta.x & 0xffff;
+        const int pos16 = meta.y * 16;
+        const bool prefix = meta.z < a.prefixUnit;
+
+        if (meta.x & (1 << 16)) {
+            // a segment begins: its rows, Q as B fragments (column n = lane / 4,
+            // k = (lane % 4) * 2 + {0, 1} (+8))
+            const int t = divide(meta.w, a.divHkv);
+            head = meta.w - t * a.Hkv;
+            row0 = t * kRows;
+            rowsOfUnit = prefix ? a.rowsPrefix : a.S * a.G;
+            const int b = meta.z - a.prefixUnit;
+            base0 = prefix ? 0 : __ldg(a.kvLens + b) - a.S;
+            last0 = last_of(0, prefix);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = row0 + nt * 8 + (lane >> 2);
+                const int s = divide(r, a.divG), g = r - s * a.G;
+                const size_t tok = (prefix ? 0 : (size_t)b * a.S) + s;
+                const uint16_t* qr = a.q + (tok * a.Hq + head * a.G + g) * D;
+#pragma unroll
+                for (int kk = 0; kk < MT; ++kk) {
+                    const int d0 = kk * 16 + (FMT == kF16 ? (lane & 3) * 2 : (lane & 3) * 4);
+                    const int d1 = d0 + (FMT == kF16 ? 8 : 2);
+                    qf[nt][kk][0] = r < rowsOfUnit ? __ldg(reinterpret_cast<const uint32_t*>(qr + d0)) : 0u;
+                    qf[nt][kk][1] = r < rowsOfUnit ? __ldg(reinterpret_cast<const uint32_t*>(qr + d1)) : 0u;
+                    acc[nt][kk][0] = acc[nt][kk][1] = acc[nt][kk][2] = acc[nt][kk][3] = 0.0f;
+                }
+                m[nt][0] = m[nt][1] = -INFINITY;
+                l[nt][0] = l[nt][1] = 0.0f;
+            }
+        }
 
         // S^T: rows are the step's tokens lane / 4 and lane / 4 + 8
         float s[NT][4];
@@ -370,12 +501,12 @@ rows_kernel(const __grid_constant__ Args a)
         } else {
 #pragma unroll
             for (int kk = 0; kk < MT; kk += 2) {
-                uint32_t w[4];
-                ldmatrix4(w, kBase + swizzle<kChunks>(lane & 15, kk + (lane >> 4)));
+                uint32_t x[4];
+                ldmatrix4(x, kBase + swizzle<kChunks>(lane & 15, kk + (lane >> 4)));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t k4[4] = {decode_pair<FMT, 0x10>(w[2 * u]), decode_pair<FMT, 0x10>(w[2 * u + 1]),
-                                            decode_pair<FMT, 0x32>(w[2 * u]), decode_pair<FMT, 0x32>(w[2 * u + 1])};
+                    const uint32_t k4[4] = {decode_pair<FMT, 0x10>(x[2 * u]), decode_pair<FMT, 0x10>(x[2 * u + 1]),
+                                            decode_pair<FMT, 0x32>(x[2 * u]), decode_pair<FMT, 0x32>(x[2 * u + 1])};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma16816(s[nt], k4, qf[nt][kk + u]);
@@ -384,40 +515,55 @@ rows_kernel(const __grid_constant__ Args a)
         }
 
         // scale, mask, running maximum
-        const uint32_t ok = *reinterpret_cast<const uint32_t*>(stagePtr + 32 * kRowBytes + 128);
-        const float* sc = reinterpret_cast<const float*>(stagePtr + 32 * kRowBytes);
+        const float* sc = reinterpret_cast<const float*>(stagePtr + C::kMeta);
         const int t0 = lane >> 2;
-        const int pos0 = step * 16 + t0;
-        const bool okA = (ok >> t0) & 1, okB = (ok >> (t0 + 8)) & 1;
-        float ks0 = a.scaleLog2, ks1 = a.scaleLog2, vs0 = 1.0f, vs1 = 1.0f, e = 0.0f;
+        float ks0 = a.scaleLog2, ks1 = a.scaleLog2, vs0 = 1.0f, vs1 = 1.0f, e0 = 0.0f, e1 = 0.0f;
         if (FMT != kF16) {
             ks0 *= sc[t0];
             ks1 *= sc[t0 + 8];
             vs0 = sc[16 + t0];
             vs1 = sc[16 + t0 + 8];
-            e = (float)scale_exponent(__reduce_max_sync(
-                0xffffffffu, max(__float_as_uint(vs0) & 0x7fffffffu, __float_as_uint(vs1) & 0x7fffffffu)));
+            e0 = scale_exponent(vs0);
+            e1 = scale_exponent(vs1);
         }
-        bool grow = false;
+        const bool masked = ok != 0xffff || pos16 + 15 > last0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                s[nt][j] = okA && pos0 <= lastCol[nt][j] ? s[nt][j] * ks0 : -INFINITY;
-                s[nt][2 + j] = okB && pos0 + 8 <= lastCol[nt][j] ? s[nt][2 + j] * ks1 : -INFINITY;
-                grow = grow || fmaxf(s[nt][j], s[nt][2 + j]) + e > m[nt][j] + 8.0f;
+                s[nt][j] *= ks0;
+                s[nt][2 + j] *= ks1;
             }
         }
+        if (masked) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int last = last_of(nt * 8 + (lane & 3) * 2 + j, prefix);
+                    if (!((ok >> t0) & 1) || pos16 + t0 > last)
+                        s[nt][j] = -INFINITY;
+                    if (!((ok >> (t0 + 8)) & 1) || pos16 + t0 + 8 > last)
+                        s[nt][2 + j] = -INFINITY;
+                }
+            }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                grow = grow || fmaxf(s[nt][j] + e0, s[nt][2 + j] + e1) > m[nt][j] + 8.0f;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(s[nt][j], s[nt][2 + j]);
+                    float x = fmaxf(s[nt][j] + e0, s[nt][2 + j] + e1);
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    const float top = fmaxf(m[nt][j], x + e);
+                    const float top = fmaxf(m[nt][j], x);
                     const float f = m[nt][j] == top ? 1.0f : exp2_fast(m[nt][j] - top);
                     m[nt][j] = top;
                     l[nt][j] *= f;
@@ -440,8 +586,13 @@ rows_kernel(const __grid_constant__ Args a)
                 const float mm = m[nt][j & 1] == -INFINITY ? 0.0f : m[nt][j & 1];
                 p[j] = exp2_fast(s[nt][j] - mm);
                 l[nt][j & 1] += p[j];
-                if (FMT != kF16)  // a token that the row does not see may have any scale
-                    p[j] = s[nt][j] == -INFINITY ? 0.0f : p[j] * (j < 2 ? vs0 : vs1);
+                if (FMT != kF16)
+                    p[j] *= j < 2 ? vs0 : vs1;
+            }
+            if (FMT != kF16 && masked) {  // a token that the row does not see may have any scale
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    p[j] = s[nt][j] == -INFINITY ? 0.0f : p[j];
             }
             pf[nt][0] = transpose8(half2_bits(p[0], p[1]));
             pf[nt][1] = transpose8(half2_bits(p[2], p[3]));
@@ -450,7 +601,7 @@ rows_kernel(const __grid_constant__ Args a)
         // Where rows see different tokens a weight of 0 can meet an infinity or
         // NaN in V that another row sees: such values are taken out of the tile
         // and added to the rows that do see them.
-        if (!PREFIX && last0 + 1 < hi && step * 16 + 15 > last0) {
+        if (a.S > 1 && !prefix && pos16 + 15 > last0) {
             auto value = [&](int t, int d) -> float {
                 const uint8_t* p = stagePtr + 16 * kRowBytes +
                     swizzle<kChunks>(t, d * C::kEsize / 16) + (d * C::kEsize) % 16;
@@ -471,11 +622,11 @@ rows_kernel(const __grid_constant__ Args a)
                         for (int j = 0; j < 4; ++j) {
                             const int d = mt * 16 + (FMT == kF16 ? (lane >> 2) + (j >> 1) * 8
                                                                  : (lane >> 2) * 2 + (j >> 1));
+                            const int last = last_of(nt * 8 + (lane & 3) * 2 + (j & 1), prefix);
 #pragma unroll 1
                             for (int t = 0; t < 16; ++t) {
                                 const float v = value(t, d);
-                                if (!(fabsf(v) < INFINITY) && ((ok >> t) & 1) &&
-                                    step * 16 + t <= lastCol[nt][j & 1])
+                                if (!(fabsf(v) < INFINITY) && ((ok >> t) & 1) && pos16 + t <= last)
                                     acc[nt][mt][j] += v;
                             }
                         }
@@ -510,126 +661,163 @@ rows_kernel(const __grid_constant__ Args a)
             // transposed as pairs of codes: a lane gets dims 2p, 2p + 1 of two tokens
 #pragma unroll
             for (int mt = 0; mt < MT; mt += 2) {
-                uint32_t w[4];
-                ldmatrix4_trans(w, vBase + swizzle<kChunks>((lane & 7) + ((lane >> 3) & 1) * 8,
+                uint32_t x[4];
+                ldmatrix4_trans(x, vBase + swizzle<kChunks>((lane & 7) + ((lane >> 3) & 1) * 8,
                                                             mt + (lane >> 4)));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t v4[4] = {decode_pair<FMT, 0x20>(w[2 * u]), decode_pair<FMT, 0x31>(w[2 * u]),
-                                            decode_pair<FMT, 0x20>(w[2 * u + 1]), decode_pair<FMT, 0x31>(w[2 * u + 1])};
+                    const uint32_t v4[4] = {decode_pair<FMT, 0x20>(x[2 * u]), decode_pair<FMT, 0x31>(x[2 * u]),
+                                            decode_pair<FMT, 0x20>(x[2 * u + 1]), decode_pair<FMT, 0x31>(x[2 * u + 1])};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma16816(acc[nt][mt + u], v4, pf[nt]);
                 }
             }
         }
+
+        if (meta.x & (1 << 17)) {
+            // the segment ends: slot item + warp
+            const long long item = (long long)(prefix ? 0 : a.tilesPrefix) * a.Hkv +
+                (prefix ? 0LL : (long long)(meta.z - a.prefixUnit) * a.tilesSeq * a.Hkv) + meta.w;
+            const size_t slot = (size_t)(item + w) * a.pitch;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = l[nt][j];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    const int n = nt * 8 + (lane & 3) * 2 + j;
+                    if (n >= a.pitch)
+                        continue;
+                    const float inv = x == 0.0f ? 0.0f : 1.0f / x;
+                    if (lane < 4)
+                        a.segL[slot + n] = x == 0.0f ? -INFINITY : m[nt][j] + log2f(x);
+                    float* dst = a.segO + (slot + n) * D;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const float y0 = x == 0.0f ? 0.0f : acc[nt][mt][j] * inv;
+                        const float y1 = x == 0.0f ? 0.0f : acc[nt][mt][2 + j] * inv;
+                        if (FMT == kF16) {
+                            dst[mt * 16 + (lane >> 2)] = y0;
+                            dst[mt * 16 + (lane >> 2) + 8] = y1;
+                        } else {
+                            *reinterpret_cast<float2*>(dst + mt * 16 + (lane >> 2) * 2) = make_float2(y0, y1);
+                        }
+                    }
+                }
+            }
+        }
         __syncwarp();  // the stage may be filled again
     }
     copy_wait<0>();
+    // The next grid (the join) may start; this one ends only after the grid before it
+    // (the prefix on the tensor cores) has, so that the join finds both complete.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
-    // ---- join: warps and ranks through (distributed) shared memory
-    __syncthreads();  // every warp is done with its ring, which the partials reuse
-    float* part = reinterpret_cast<float*>(smem);                           // [W][kRows][kPitch]
-    float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);               // [W][kRows]
-    float2* all = reinterpret_cast<float2*>(smem + C::kOffAll);             // [partials][kRows]: m, l, then weights
-    float2* total = reinterpret_cast<float2*>(smem + C::kOffTotal);         // [kRows]: max, sum
+// ------------------------------------------------------------ join kernel --
+//
+// Joins the partials of every output row: the prefix's (numParts ranges, or the
+// segments of the prefix unit) and the row's own segments, in that order. A group
+// of D / 4 threads holds a row; SPLIT: the CTA's groups share one row's partials
+// (few rows with many segments each).
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int rowsPerTile)
+{
+    constexpr int TG = D / 4, kGroups = 256 / TG;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int group = threadIdx.x / TG, d = threadIdx.x % TG * 4;
+    const int hv = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * kGroups + group;   // (token, q head)
+    const int rows = a.B * a.S * a.Hq;
+    if (!SPLIT && hv >= rows)
+        return;
+    const int tok = hv / a.Hq, hq = hv - tok * a.Hq;
+    const int h = divide(hq, a.divG), g = hq - h * a.G;
+    const int b = divide(tok, a.divS), s = tok - b * a.S;
+    const bool active = __ldg(a.kvLens + b) - (long long)a.S + s >= a.P;
+
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // four partials at a time: their loads are in flight together
+    auto join4 = [&](const float* L, size_t strideL, const float* O, size_t strideO, long long k, long long n) {
+        float x[4];
+        float4 v[4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float x = l[nt][j];
-            x += __shfl_xor_sync(0xffffffffu, x, 4);
-            x += __shfl_xor_sync(0xffffffffu, x, 8);
-            x += __shfl_xor_sync(0xffffffffu, x, 16);
-            if (lane < 4)
-                ml[warp * kRows + nt * 8 + lane * 2 + j] = make_float2(m[nt][j], x);
+        for (int j = 0; j < 4; ++j) {
+            const bool in = k + j < n;
+            x[j] = in ? L[(k + j) * strideL] : -INFINITY;
+            v[j] = in ? *reinterpret_cast<const float4*>(O + (k + j) * strideO) : make_float4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = nt * 8 + (lane & 3) * 2 + (j & 1);
-                const int d = mt * 16 + (FMT == kF16 ? (lane >> 2) + (j >> 1) * 8
-                                                     : (lane >> 2) * 2 + (j >> 1));
-                part[(warp * kRows + n) * C::kPitch + d] = acc[nt][mt][j];
-            }
-    }
-    if (!PREFIX)  // the prefix partials, and everything before them, are complete
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (ranks > 1)
-        cluster.sync();
-    else
-        __syncthreads();
-
-    // Every partial's (m, l) of every row, the prefix's as (m + log2 l, 1)
-    const int own = W * ranks, partials = own + (PREFIX ? 0 : a.numParts);
-    const size_t headRow = (size_t)h * a.rowsPrefix + (PREFIX ? 0 : (size_t)unit * a.S * a.G) + row0;
-    const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
-    const int rowsHere = min(kRows, rowsOfUnit - row0);
-    for (int i = threadIdx.x; i < partials * kRows; i += W * 32) {
-        const int k = i / kRows, n = i % kRows;
-        float2 v = make_float2(-INFINITY, 0.0f);
-        if (k < own)
-            v = (ranks > 1 ? cluster.map_shared_rank(ml, k / W) : ml)[(k % W) * kRows + n];
-        else if (n < rowsHere && last_of(n) != kNoRow)
-            v = make_float2(a.partL[(size_t)(k - own) * partStride + headRow + n], 1.0f);
-        all[i] = v;
-    }
-    __syncthreads();
-    for (int n = threadIdx.x; n < kRows; n += W * 32) {
-        float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < partials; ++k)
-            top = fmaxf(top, all[k * kRows + n].x);
-        const float mm = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-        for (int k = 0; k < partials; ++k) {
-            const float2 v = all[k * kRows + n];
-            const float w = exp2_fast(v.x - mm);
-            all[k * kRows + n].x = w;
-            sum += w * v.y;
+        for (int j = 0; j < 4; ++j) {
+            const float top = fmaxf(m, x[j]);
+            const float mm = top == -INFINITY ? 0.0f : top;
+            const float f = exp2_fast(m - mm), w = exp2_fast(x[j] - mm);
+            m = top;
+            l = l * f + w;
+            o.x = o.x * f + w * v[j].x;
+            o.y = o.y * f + w * v[j].y;
+            o.z = o.z * f + w * v[j].z;
+            o.w = o.w * f + w * v[j].w;
         }
-        total[n] = make_float2(mm, sum);
-    }
-    __syncthreads();
-
-    for (int f = rank * W * 32 + (int)threadIdx.x; f < rowsHere * (D / 4); f += ranks * W * 32) {
-        const int n = f / (D / 4), d = f % (D / 4) * 4;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        auto add = [&](float w, const float4& v) {
-            o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+    };
+    if (active) {
+        const int first = SPLIT ? 4 * group : 0, stride = SPLIT ? 4 * kGroups : 4;
+        const size_t headRow = (size_t)h * a.rowsPrefix + (size_t)tok * a.G + g;
+        const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
+        for (int k = first; k < a.numParts; k += stride)
+            join4(a.partL + headRow, partStride, a.partO + headRow * D + d, partStride * D, k, a.numParts);
+        const int units = a.B + a.prefixUnit;
+        const long long share = a.offsets[units + 1];
+        auto join_segments = [&](int u, int row, int tiles, long long itemBase) {
+            const long long at = a.offsets[u], all = a.offsets[u + 1] - at;
+            if (all == 0)
+                return;
+            const int t = row / rowsPerTile, sub = t * a.Hkv + h;
+            const long long n = all / ((long long)tiles * a.Hkv);
+            const long long w0 = (at + sub * n) / share, w1 = (at + sub * n + n - 1) / share;
+            const size_t slot = (size_t)(itemBase + sub + w0) * a.pitch + (row - t * rowsPerTile);
+            for (long long k = first; k < w1 - w0 + 1; k += stride)
+                join4(a.segL + slot, a.pitch, a.segO + slot * D + d, (size_t)a.pitch * D, k, w1 - w0 + 1);
         };
-        for (int k = 0; k < ranks; ++k) {
-            const float* p = (ranks > 1 ? cluster.map_shared_rank(part, k) : part) + n * C::kPitch + d;
-#pragma unroll
-            for (int x = 0; x < W; ++x)
-                add(all[(k * W + x) * kRows + n].x, *reinterpret_cast<const float4*>(p + x * kRows * C::kPitch));
+        if (a.prefixUnit)
+            join_segments(0, tok * a.G + g, a.tilesPrefix, 0);
+        join_segments(b + a.prefixUnit, s * a.G + g, a.tilesSeq,
+                      ((long long)a.tilesPrefix + (long long)b * a.tilesSeq) * a.Hkv);
+    }
+    if (SPLIT) {
+        __shared__ float sm[kGroups], sl[kGroups];
+        __shared__ float4 so[256];
+        if (d == 0) {
+            sm[group] = m;
+            sl[group] = l;
         }
-        const float2 t = total[n];
-        const float inv = t.y == 0.0f ? 0.0f : 1.0f / t.y;
-        if (PREFIX) {
-            *reinterpret_cast<float4*>(a.partO + (headRow + n) * D + d) =
-                t.y == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                            : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-            if (d == 0)
-                a.partL[headRow + n] = t.y == 0.0f ? -INFINITY : t.x + log2f(t.y);
-        } else {
-            if (last_of(n) != kNoRow) {
-#pragma unroll 4
-                for (int k = 0; k < a.numParts; ++k)
-                    add(all[(own + k) * kRows + n].x, *reinterpret_cast<const float4*>(
-                            a.partO + (k * partStride + headRow + n) * D + d));
-            }
-            const size_t y = (size_t)token_of(n) * a.Hq + h * a.G + (row0 + n) % a.G;
-            const bool none = t.y == 0.0f;
-            *reinterpret_cast<uint2*>(a.out + y * D + d) =
-                none ? make_uint2(0, 0) : make_uint2(half2_bits(o.x * inv, o.y * inv), half2_bits(o.z * inv, o.w * inv));
-            if (d == 0 && a.lse != nullptr)
-                a.lse[y] = none ? -INFINITY : kLn2 * (t.x + log2f(t.y));
+        so[threadIdx.x] = o;
+        __syncthreads();
+        if (group > 0)
+            return;
+        for (int k = 1; k < kGroups; ++k)
+            m = fmaxf(m, sm[k]);
+        const float mm = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < kGroups; ++k) {
+            const float w = exp2_fast(sm[k] - mm);
+            const float4 v = so[k * TG + threadIdx.x];
+            l += w * sl[k];
+            o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
         }
     }
-    if (ranks > 1)
-        cluster.sync();  // no CTA leaves while another reads its shared memory
+    const bool none = l == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2*>(a.out + (size_t)hv * D + d) =
+        none ? make_uint2(0, 0) : make_uint2(half2_bits(o.x * inv, o.y * inv), half2_bits(o.z * inv, o.w * inv));
+    if (d == 0 && a.lse != nullptr)
+        a.lse[hv] = none ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
 }  // namespace ropekv_attn

@@ -22,11 +22,12 @@
 // issue order S(0) S(1) [O(i) S(i + 2)]... makes each S overwrite its slot only
 // after the P in it was read.
 //
-// M moves only when a row's scores exceed it by more than 2^8, in which case the
-// row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: a token's K
-// scale multiplies its column of S, its V scale its column of P. With 2^e the
-// largest V scale of a tile, M follows max(s) + e: then P times scale stays near
-// [0, 2^9], and as O and l share M nothing has to be undone.
+// M moves only when a row's scores exceed it by more than 8, in which case the
+// row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: with ks and vs
+// a token's scales, x = ks c s + log2(vs) and P = 2^(x - M) is weight times V scale
+// in one exponential, near [0, 2^8] whatever the scales; the row sum adds P / vs.
+// (A V row with scale 0 is fetched as zeros with vs = 1, one with a negative scale
+// as its negative.)
 //
 // Every wait on an mbarrier is bounded; a wait that runs out makes the CTA stop
 // waiting and write NaN.
@@ -51,9 +52,9 @@ struct PrefixConfig {
     static constexpr int kOffRing = kQBytes;
     static constexpr int kOffKs = kOffRing + kStages * kTileBytes;
     static constexpr int kOffVs = kOffKs + kMeta * kTile * 4;
-    static constexpr int kOffMask = kOffVs + kMeta * kTile * 4;
-    static constexpr int kOffExp = kOffMask + kMeta * 16;
-    static constexpr int kOffBar = kOffExp + kMeta * 16;
+    static constexpr int kOffRv = kOffVs + kMeta * kTile * 4;
+    static constexpr int kOffMask = kOffRv + kMeta * kTile * 4;
+    static constexpr int kOffBar = kOffMask + kMeta * 16;
     static constexpr int kUsed = kOffBar + (2 * kStages + 6) * 8 + 16;
     // one CTA per SM (each takes all of TMEM)
     static constexpr int kSmem = (kUsed > 120 * 1024 ? kUsed : 120 * 1024) + 1024;
@@ -179,6 +180,23 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
 
+// Two FP32 operations in one instruction: d = a * b + c, d += a.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1)
+{
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1)
+{
+    asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\t"
+        "add.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
+}
+
 // Shared-memory matrix descriptor: 128-byte swizzle, offsets in bytes.
 __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t leading, uint32_t stride)
 {
@@ -252,8 +270,8 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
         const int r = i / (D / 8), c = i % (D / 8);
         const int row = row0 + r;
         const bool ok = row < a.rowsPrefix;
-        const size_t tok = ok ? row / a.G : 0;
-        const int g = ok ? row % a.G : 0;
+        const size_t tok = ok ? divide(row, a.divG) : 0;
+        const int g = ok ? row - (int)tok * a.G : 0;
         copy16(base + (r >> 7) * (128 * D * 2) + tile_pos(128, r & 127, c),
                a.q + (tok * a.Hq + h * a.G + g) * D + c * 8, ok);
     }
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
             idK = idV = -1;
             const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
             if (u < groups && pos < a.P) {
-                const int lp = pos / a.tpp;
+                const int lp = divide(pos, a.divTpp);
                 idK = __ldg(a.prefixTable + lp);
                 idV = __ldg(a.prefixTable + a.prefixPages + lp);
             }
@@ -341,18 +359,19 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
             const bool ok = idK >= 0 && idK < a.numPages && idV >= a.numPages &&
                             idV - a.numPages < a.numPages;
             mask = __ballot_sync(0xffffffffu, ok);
-            const int inPage = pos % a.tpp;
+            const int inPage = pos - divide(pos, a.divTpp) * a.tpp;
             return ok ? (uint32_t)((t & 1) ? idV : idK) * (uint32_t)a.tpp + inPage : 0u;
         };
-        // 8-bit: the scales of a K group's tokens (K's times c, V's), fetched with the ids' group
+        // what the softmax needs of a K group's tokens: the mask and (8-bit) the K scale
+        // times c, log2 and reciprocal of the V scale's magnitude
         auto write_meta = [&](int u, uint32_t mask, float ks, float vs) {
             const int j = (u / GP) >> 1, g = u % GP, slot = j % C::kMeta;
             if (FMT != kF16) {
-                reinterpret_cast<float*>(smem + C::kOffKs)[slot * TN + g * 32 + lane] = ks * a.scaleLog2;
-                reinterpret_cast<float*>(smem + C::kOffVs)[slot * TN + g * 32 + lane] = vs;
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs) & 0x7fffffffu);
-                if (lane == 0)
-                    reinterpret_cast<int*>(smem + C::kOffExp)[slot * 4 + g] = scale_exponent(top);
+                const int at = slot * TN + g * 32 + lane;
+                const float v = vs == 0.0f ? 1.0f : fabsf(vs);
+                reinterpret_cast<float*>(smem + C::kOffKs)[at] = ks * a.scaleLog2;
+                reinterpret_cast<float*>(smem + C::kOffVs)[at] = log2f(v);
+                reinterpret_cast<float*>(smem + C::kOffRv)[at] = 1.0f / v;
             }
             if (lane == 0)
                 reinterpret_cast<uint32_t*>(smem + C::kOffMask)[slot * 4 + g] = mask;
@@ -406,9 +425,9 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
             auto load = [&](int u) {
                 const uint32_t row = locate(u, mask);
                 ks = vs = 0.0f;
-                if (!((u / GP) & 1) && ((mask >> lane) & 1)) {
+                if ((mask >> lane) & 1) {
                     const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
-                    const int inPage = pos % a.tpp;
+                    const int inPage = pos - divide(pos, a.divTpp) * a.tpp;
                     ks = __ldg(a.scales + ((size_t)idK * a.Hkv + h) * a.tpp + inPage);
                     vs = __ldg(a.scales + ((size_t)idV * a.Hkv + h) * a.tpp + inPage);
                 }
@@ -431,6 +450,10 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                     cur[i] = buf[i];
                 const uint32_t curMask = mask;
                 const float curK = ks, curV = vs;
+                // V rows whose scale is 0 or negative
+                const bool isV = (u / GP) & 1;
+                const uint32_t dead = isV ? __ballot_sync(0xffffffffu, curV == 0.0f) : ~curMask;
+                const uint32_t flip = isV ? __ballot_sync(0xffffffffu, curV < 0.0f) : 0u;
                 if (u + 3 < groups)
                     load(u + 3);
                 fetch_ids(u + 6);
@@ -440,13 +463,14 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int i = 0; i < kPerLane; ++i) {
                     const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
-                    const bool ok = (curMask >> r) & 1;   // zeros, not codes of zero, where unmapped
+                    const bool ok = !((dead >> r) & 1);   // else zeros: unmapped tokens among them
+                    const uint32_t sign = (flip >> r) & 1 ? 0x80008000u : 0u;
                     const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = ok ? decode_pair<FMT, 0x10>(w[k]) : 0u;
-                        o[2 * k + 1] = ok ? decode_pair<FMT, 0x32>(w[k]) : 0u;
+                        o[2 * k] = ok ? decode_pair<FMT, 0x10>(w[k]) ^ sign : 0u;
+                        o[2 * k + 1] = ok ? decode_pair<FMT, 0x32>(w[k]) ^ sign : 0u;
                     }
                     *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -462,6 +486,8 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
         const uint32_t laneBase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t oAddr = laneBase + C::kColO + tile * D;
         float M = -INFINITY, l = 0.0f;
+        // |c|, kept above 0 so that a masked -infinity stays one (c = 0: all scores are 0)
+        const float scale = fmaxf(fabsf(a.scaleLog2), 1e-30f);
         for (int j = 0; j < J; ++j) {
             const int i = MT == 2 ? 2 * j + tile : j;
             const int slot = i & 1;
@@ -476,18 +502,12 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
             const int meta = j % C::kMeta;
             const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kOffMask) + meta * 4;
             const float* ks = reinterpret_cast<const float*>(smem + C::kOffKs) + meta * TN;
-            const float* vs = reinterpret_cast<const float*>(smem + C::kOffVs) + meta * TN;
+            const float* lv = reinterpret_cast<const float*>(smem + C::kOffVs) + meta * TN;
+            const float* rv = reinterpret_cast<const float*>(smem + C::kOffRv) + meta * TN;
             uint32_t all = 0xffffffffu;
 #pragma unroll
             for (int g = 0; g < GP; ++g)
                 all &= mask[g];
-            int e = 0;
-            if (FMT != kF16) {
-                e = -60;
-#pragma unroll
-                for (int g = 0; g < GP; ++g)
-                    e = max(e, reinterpret_cast<const int*>(smem + C::kOffExp)[meta * 4 + g]);
-            }
             tmem_wait_load();
 #pragma unroll
             for (int k = 0; k < TN / 32; ++k)
@@ -496,24 +516,32 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int k = 0; k < TN; k += 4) {
                     const float4 f = *reinterpret_cast<const float4*>(ks + k);
-                    s[k] *= f.x; s[k + 1] *= f.y; s[k + 2] *= f.z; s[k + 3] *= f.w;
+                    const float4 v = *reinterpret_cast<const float4*>(lv + k);
+                    fma2(s[k], s[k + 1], s[k], s[k + 1], f.x, f.y, v.x, v.y);
+                    fma2(s[k + 2], s[k + 3], s[k + 2], s[k + 3], f.z, f.w, v.z, v.w);
                 }
-            } else {
-                // the sign of c decides between maximum and minimum, so scale first
+            } else if (a.scaleLog2 < 0.0f) {
 #pragma unroll
                 for (int k = 0; k < TN; ++k)
-                    s[k] *= a.scaleLog2;
+                    s[k] = -s[k];
             }
             if (all != 0xffffffffu) {
 #pragma unroll
                 for (int k = 0; k < TN; ++k)
                     s[k] = (mask[k >> 5] >> (k & 31)) & 1 ? s[k] : -INFINITY;
             }
-            float top = -INFINITY;
+            // FP16: s is unscaled until the exponential takes c s - M
+            float top4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int k = 0; k < TN; ++k)
-                top = fmaxf(top, s[k]);
-            top += (float)e;
+            for (int k = 4; k < TN; k += 4) {
+                top4[0] = fmaxf(top4[0], s[k]);
+                top4[1] = fmaxf(top4[1], s[k + 1]);
+                top4[2] = fmaxf(top4[2], s[k + 2]);
+                top4[3] = fmaxf(top4[3], s[k + 3]);
+            }
+            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+            if (FMT == kF16)
+                top = top == -INFINITY ? top : top * scale;
             if (__any_sync(0xffffffffu, top > M + 8.0f)) {
                 const float next = fmaxf(M, top);
                 const float f = M == next ? 1.0f : exp2_fast(M - next);
@@ -542,6 +570,7 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                 }
             }
             const float mm = M == -INFINITY ? 0.0f : M;
+            const float mul = FMT == kF16 ? scale : 1.0f;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < TN; k += 64) {
@@ -549,14 +578,18 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int x = 0; x < 64; x += 4) {
                     float v[4];
+                    fma2(v[0], v[1], s[k + x], s[k + x + 1], mul, mul, -mm, -mm);
+                    fma2(v[2], v[3], s[k + x + 2], s[k + x + 3], mul, mul, -mm, -mm);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        v[y] = exp2_fast(s[k + x + y] - mm);
-                        sum[y] += v[y];
-                    }
-                    if (FMT != kF16) {
-                        const float4 f = *reinterpret_cast<const float4*>(vs + k + x);
-                        v[0] *= f.x; v[1] *= f.y; v[2] *= f.z; v[3] *= f.w;
+                    for (int y = 0; y < 4; ++y)
+                        v[y] = exp2_fast(v[y]);
+                    if (FMT == kF16) {
+                        add2(sum[0], sum[1], v[0], v[1]);
+                        add2(sum[2], sum[3], v[2], v[3]);
+                    } else {
+                        const float4 f = *reinterpret_cast<const float4*>(rv + k + x);
+                        fma2(sum[0], sum[1], v[0], v[1], f.x, f.y, sum[0], sum[1]);
+                        fma2(sum[2], sum[3], v[2], v[3], f.z, f.w, sum[2], sum[3]);
                     }
                     p[x / 2] = half2_bits(v[0], v[1]);
                     p[x / 2 + 1] = half2_bits(v[2], v[3]);

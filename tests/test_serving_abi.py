@@ -145,7 +145,7 @@ def test_attention_refuses_bad_arguments(lib):
 
 def test_workspace_size(lib):
     size = lib.paged_attention_workspace_size
-    assert size(ctypes.byref(_dims(prefixLen=0))) == 0
+    assert size(ctypes.byref(_dims(batch=0))) == 0 and size(ctypes.byref(_dims(seqLen=0))) == 0
     assert size(ctypes.byref(_dims())) >= 4 * 32 * 128 * 4
     assert size(ctypes.byref(_dims(headDim=32))) == HEAD_DIM
     assert size(None) == NULL
