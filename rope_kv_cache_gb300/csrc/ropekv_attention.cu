@@ -82,6 +82,12 @@ int launch(Kern kern, long long grid, int threads, int smem, bool dependent, cud
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
 
+// CTAs of the stream grid for each that fits on the GPU.
+#ifndef ROPEKV_OVER
+#define ROPEKV_OVER 1
+#endif
+constexpr int kOver = ROPEKV_OVER;
+
 // How a call is cut into launches, from its sizes alone.
 struct Plan {
     int nt;             // row tiles of the stream kernel: 8, 16 or 32 rows
@@ -91,11 +97,28 @@ struct Plan {
     int tilesPrefix;    // row tiles of the stream kernel's prefix unit (0: none)
     int tilesSeq;       // and of a sequence
     int pitch;
-    int ctas, warps;    // stream grid
+    int teams, teamSize, groups;   // stream grid: CTAs, their warps, head groups
     int64_t partRows, slots, units;
 };
 
 int stream_warps(int D, int fmt, int nt);
+
+// KV heads that a CTA reads side by side: the largest divisor of Hkv that leaves
+// at most a quarter of an SM's warps idle, else the one that leaves fewest.
+int team_size(int Hkv, int perSm)
+{
+    int best = 1, used = perSm;
+    for (int t = 1, bestUsed = 0; t <= perSm && t <= Hkv; ++t) {
+        if (Hkv % t != 0)
+            continue;
+        used = perSm / t * t;
+        if (4 * used >= 3 * perSm || used > bestUsed) {
+            best = t;
+            bestUsed = used;
+        }
+    }
+    return best;
+}
 
 // Tiles of 8 rows, or of 16 or 32 (D = 256: 16 at most) where a sequence has
 // more, so that its tokens are fetched once. The prefix joins the stream if all
@@ -114,14 +137,17 @@ Plan make_plan(const ropekv_attention_dims* d)
     const long long longest = p.tilesPrefix ? rows : rowsSeq;
     p.pitch = (int)(longest < 8 * p.nt ? longest : 8 * p.nt);
     p.units = d->batch + p.tilesPrefix;
+    const int perSm = stream_warps(d->headDim, d->cacheFormat, p.nt);
+    p.teamSize = team_size(d->numKVHeads, perSm);
+    p.groups = d->numKVHeads / p.teamSize;
     // the table's capacity bounds the steps; at least two of them make a share
     const long long own = (long long)d->maxPagesPerSeq * d->tokensPerPage - d->prefixLen;
-    const long long items = (long long)d->batch * p.tilesSeq * d->numKVHeads;
+    const long long items = (long long)d->batch * p.tilesSeq * p.groups;
     const long long steps = items * (own > 0 ? own / 16 + 2 : 0) +
-                            (p.tilesPrefix ? (long long)d->numKVHeads * (d->prefixLen / 16 + 1) : 0);
-    p.ctas = (int)(steps / 2 < 1 ? 1 : steps / 2 < kSMs ? steps / 2 : kSMs);
-    p.warps = p.ctas * stream_warps(d->headDim, d->cacheFormat, p.nt);
-    p.slots = items + (long long)p.tilesPrefix * d->numKVHeads + p.warps;
+                            (p.tilesPrefix ? (long long)p.groups * (d->prefixLen / 16 + 1) : 0);
+    const long long most = (long long)kSMs * (perSm / p.teamSize) * kOver, want = (steps + 1) / 2;
+    p.teams = (int)(want < 1 ? 1 : want < most ? want : most);
+    p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
     if (p.tensor) {
         const int tileRows = d->headDim != 256 && rows > 128 ? 256 : 128;
         const int tokens = d->headDim == 256 ? 64 : 128;
@@ -155,7 +181,7 @@ Layout make_layout(const Plan& p, int D)
     w.segO = w.partL + up(p.partRows * 4);
     w.segL = w.segO + up(p.slots * p.pitch * D * 4);
     w.offsets = w.segL + up(p.slots * p.pitch * 4);
-    w.size = w.offsets + up((p.units + 2) * 8);
+    w.size = w.offsets + up((p.units + 4) * 8);
     return w;
 }
 
@@ -174,9 +200,9 @@ int launch_stream(const Args& a, const Plan& p, cudaStream_t st)
 {
     constexpr auto kern = ropekv_attn::stream_kernel<D, FMT, NT>;
     using C = StreamConfig<D, FMT, NT>;
-    if (!raise_smem<kern>(C::kSmem))
+    if (!raise_smem<kern>(C::smem(C::kPerSm)))
         return ROPEKV_ERR_LAUNCH;
-    return launch(kern, p.ctas, C::kWarps * 32, C::kSmem, p.tensor, st, a);
+    return launch(kern, p.teams, p.teamSize * 32, C::smem(p.teamSize), p.tensor, st, a);
 }
 
 template <int D, int FMT>
@@ -203,9 +229,10 @@ int launch_all(const Args& a, const Plan& p, cudaStream_t st)
     // few rows whose items many warps share: all groups of a CTA join one row
     const long long rows = (long long)a.B * a.S * a.Hq;
     constexpr int perCta = 1024 / D;
+    const int tileShift = p.nt == 1 ? 3 : p.nt == 2 ? 4 : 5;
     if (rows < 4LL * kSMs)
-        return launch(ropekv_attn::join_kernel<D, true>, rows, 256, 0, true, st, a, 8 * p.nt);
-    return launch(ropekv_attn::join_kernel<D, false>, (rows + perCta - 1) / perCta, 256, 0, true, st, a, 8 * p.nt);
+        return launch(ropekv_attn::join_kernel<D, true>, rows, 256, 0, true, st, a, tileShift);
+    return launch(ropekv_attn::join_kernel<D, false>, (rows + perCta - 1) / perCta, 256, 0, true, st, a, tileShift);
 }
 
 template <int D>
@@ -218,27 +245,23 @@ int dispatch(const Args& a, const Plan& p, int fmt, cudaStream_t st)
     }
 }
 
-template <int D, int FMT>
-int stream_warps_nt(int nt)
+// Warps of an SM (both 8-bit formats have the same shape).
+template <int D>
+int stream_warps(bool f16, int nt)
 {
     if constexpr (D != 256) {
         if (nt == 4)
-            return StreamConfig<D, FMT, 4>::kWarps;
+            return f16 ? StreamConfig<D, ROPEKV_CACHE_F16, 4>::kPerSm : StreamConfig<D, ROPEKV_CACHE_E4M3, 4>::kPerSm;
     }
-    return nt == 1 ? StreamConfig<D, FMT, 1>::kWarps : StreamConfig<D, FMT, 2>::kWarps;
-}
-
-template <int D>
-int stream_warps_fmt(int fmt, int nt)
-{
-    return fmt == ROPEKV_CACHE_F16 ? stream_warps_nt<D, ROPEKV_CACHE_F16>(nt)
-                                   : stream_warps_nt<D, ROPEKV_CACHE_E4M3>(nt);
+    if (nt == 2)
+        return f16 ? StreamConfig<D, ROPEKV_CACHE_F16, 2>::kPerSm : StreamConfig<D, ROPEKV_CACHE_E4M3, 2>::kPerSm;
+    return f16 ? StreamConfig<D, ROPEKV_CACHE_F16, 1>::kPerSm : StreamConfig<D, ROPEKV_CACHE_E4M3, 1>::kPerSm;
 }
 
 int stream_warps(int D, int fmt, int nt)
 {
-    return D == 64 ? stream_warps_fmt<64>(fmt, nt) : D == 128 ? stream_warps_fmt<128>(fmt, nt)
-                                                              : stream_warps_fmt<256>(fmt, nt);
+    const bool f16 = fmt == ROPEKV_CACHE_F16;
+    return D == 64 ? stream_warps<64>(f16, nt) : D == 128 ? stream_warps<128>(f16, nt) : stream_warps<256>(f16, nt);
 }
 
 }  // namespace
@@ -313,10 +336,13 @@ int paged_attention_shared_prefix(const uint16_t* q, const void* kvCache, const 
     a.tilesPrefix = plan.tilesPrefix;
     a.tilesSeq = plan.tilesSeq;
     a.pitch = plan.pitch;
-    a.warps = plan.warps;
+    a.teams = plan.teams;
+    a.teamSize = plan.teamSize;
+    a.groups = plan.groups;
     a.divTpp = make_divisor(a.tpp);
     a.divG = make_divisor(a.G);
-    a.divHkv = make_divisor(a.Hkv);
+    a.divGroups = make_divisor(a.groups);
+    a.divTeam = make_divisor(a.teamSize);
     a.divS = make_divisor(a.S);
     cudaStream_t st = (cudaStream_t)stream;
     switch (dims->headDim) {

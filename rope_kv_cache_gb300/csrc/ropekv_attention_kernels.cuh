@@ -59,7 +59,7 @@ struct Args {
     float* partL;                // [numParts, Hkv, B*S*G]
     float* segO;                 // [slots, pitch, D]          segments of the streamed tokens
     float* segL;                 // [slots, pitch]
-    long long* offsets;          // [units + 2]: first step of each unit, their sum, steps per warp
+    long long* offsets;          // [units + 4]: first step of each unit, their sum, steps of a share, its divisor
     float scaleLog2;             // smScale * log2(e)
     int32_t B, S, Hq, Hkv, G, numPages, tpp, mpps, P, prefixPages;
     int32_t rowsPrefix;          // B * S * G
@@ -69,8 +69,10 @@ struct Args {
     int32_t tilesPrefix;         // row tiles of the prefix unit (0 without one)
     int32_t tilesSeq;            // row tiles of a sequence
     int32_t pitch;               // rows of a segment's slot
-    int32_t warps;               // warps of the stream grid
-    Divisor divTpp, divG, divHkv, divS;
+    int32_t teams;               // CTAs of the stream grid
+    int32_t teamSize;            // their warps: KV heads that one CTA reads side by side
+    int32_t groups;              // Hkv / teamSize
+    Divisor divTpp, divG, divGroups, divS, divTeam;
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -166,6 +168,15 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Not 0 if a word of V (two halves, four codes) holds an infinity or NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t non_finite(uint32_t w)
+{
+    if (FMT == kF16)
+        return __vcmpeq2(w & 0x7c007c00u, 0x7c007c00u);
+    return FMT == kE4M3 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+}
+
 // Shared-memory position of 16-byte chunk `c` of row `r` in a tile of rows of
 // CPR chunks: eight consecutive rows of one chunk column fall into eight
 // different 16-byte bank groups, as ldmatrix reads them.
@@ -186,16 +197,18 @@ __device__ __forceinline__ int swizzle(int r, int c)
 // transposes per 16 tokens make it the B operand of the second product.
 //
 // Work. A unit is a sequence's own tokens (or the prefix, when few rows share
-// it), an item one row tile and KV head of a unit, a step 16 tokens of an item
+// it). A CTA is a team of warps, one for each of a group of KV heads, so that a
+// page's rows, which hold all heads, are read in runs longer than one head. An
+// item is one row tile and group of heads of a unit, a step 16 tokens of an item
 // (steps begin at multiples of 16 positions). All steps of all items form one
-// sequence, and every warp of a persistent grid takes an equal share of it,
-// whatever the lengths: lengths are on the device, so each CTA sums them first.
-// A warp's share covers the end of an item, whole items, the start of another:
-// its segments. Warps never wait for one another. A warp's ring of cp.async
+// sequence, and every team takes an equal share of it, whatever the lengths:
+// lengths are on the device, so each CTA sums them first. A share covers the end
+// of an item, whole items, the start of another: its segments. The warps of a team
+// walk the same steps but never wait for one another. A warp's ring of cp.async
 // stages runs ahead across segment borders, so the loads do not drain between
 // items; page ids are fetched a step before the copies that need them. Each
-// segment leaves (O / l, m + log2 l) in slot item + warp, which no other segment
-// has, as the next segment in order has a larger item or a larger warp.
+// segment leaves (O / l, m + log2 l) in slots item + team, which no other segment
+// has, as the next segment in order has a larger item or a larger team.
 //
 // m follows the maximum lazily: it moves only when a score exceeds it by more
 // than 8 (2^8 stays far inside FP16 and FP32), so most steps need one vote
@@ -226,13 +239,11 @@ struct StreamConfig {
     static constexpr int kStageBytes = 32 * kRowBytes + 256;
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRows = 8 * NT;
-    // one CTA per SM, its warps limited by shared memory and by registers (accumulators)
-    static constexpr int kBySmem = 210 * 1024 / kWarpBytes;
+    // warps of an SM: limited by shared memory and by registers (accumulators)
+    static constexpr int kBySmem = 212 * 1024 / kWarpBytes;
     static constexpr int kByRegs = NT * D <= 128 ? 16 : 8;
-    static constexpr int kFit = kBySmem < kByRegs ? kBySmem : kByRegs;
-    static constexpr int kWarps = kFit >= 16 ? 16 : kFit >= 8 ? 8 : 4;
-    static constexpr int kOffScan = kWarps * kWarpBytes;
-    static constexpr int kSmem = kOffScan + (kWarps * 32 + 1) * 8 + kWarps * 8;
+    static constexpr int kPerSm = kBySmem < kByRegs ? kBySmem : kByRegs;
+    static constexpr int smem(int team) { return team * kWarpBytes + (team * 32 + 1) * 8 + team * 8; }
 };
 
 // Tokens of unit u: positions [lo, hi).
@@ -253,24 +264,24 @@ __device__ __forceinline__ int unit_steps(int lo, int hi)
 }
 
 template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(StreamConfig<D, FMT, NT>::kWarps * 32, 1)
+__global__ void __launch_bounds__(StreamConfig<D, FMT, NT>::kPerSm * 32, 1)
 stream_kernel(const __grid_constant__ Args a)
 {
     using C = StreamConfig<D, FMT, NT>;
     constexpr int kRowBytes = C::kRowBytes, kChunks = C::kChunks, kRows = C::kRows;
-    constexpr int MT = D / 16, NS = C::kStages, T = C::kWarps * 32;
+    constexpr int MT = D / 16, NS = C::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, T = blockDim.x;
     const int units = a.B + a.prefixUnit;
 
-    // ---- shares: sum of all units' steps, then this warp's range
-    long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);   // [T + 1] exclusive sums
+    // ---- shares: sum of all units' steps, then this team's range
+    long long* scan = reinterpret_cast<long long*>(smem + a.teamSize * C::kWarpBytes);   // [T + 1] exclusive sums
     long long* warpSum = scan + T + 1;
     const int perThread = (units + T - 1) / T;
     auto weight = [&](int u) -> long long {
         int lo, hi;
         unit_range(a, u, lo, hi);
-        return (long long)unit_steps(lo, hi) * ((u < a.prefixUnit ? a.tilesPrefix : a.tilesSeq) * (long long)a.Hkv);
+        return (long long)unit_steps(lo, hi) * ((u < a.prefixUnit ? a.tilesPrefix : a.tilesSeq) * (long long)a.groups);
     };
     const int u0 = min(units, (int)threadIdx.x * perThread), u1 = min(units, u0 + perThread);
     long long mine = 0;
@@ -287,12 +298,12 @@ stream_kernel(const __grid_constant__ Args a)
         warpSum[warp] = sum;
     __syncthreads();
     long long before = 0, total = 0;
-    for (int x = 0; x < C::kWarps; ++x) {
+    for (int x = 0; x < a.teamSize; ++x) {
         before += x < warp ? warpSum[x] : 0;
         total += warpSum[x];
     }
     scan[threadIdx.x] = before + sum - mine;
-    const long long share = max(2LL, (total + a.warps - 1) / a.warps);
+    const long long share = max(2LL, (total + a.teams - 1) / a.teams);
     if (blockIdx.x == 0) {
         long long at = before + sum - mine;
         for (int u = u0; u < u1; ++u) {
@@ -302,13 +313,17 @@ stream_kernel(const __grid_constant__ Args a)
         if (threadIdx.x == 0) {
             a.offsets[units] = total;
             a.offsets[units + 1] = share;
+            if (total < (1LL << 31)) {
+                // multiplier and shift of the division by the share (see Divisor)
+                const int c = share > 1 ? 64 - __clzll(share - 1) : 0;
+                a.offsets[units + 2] = (long long)(((1ULL << (31 + c)) + share - 1) / (unsigned long long)share);
+                a.offsets[units + 3] = 31 + c;
+            }
         }
     }
     __syncthreads();
 
-    // warps next to one another in the sequence of steps sit on different SMs
-    const int w = warp * gridDim.x + blockIdx.x;
-    const long long begin = w * share;
+    const long long begin = blockIdx.x * share;
     const long long count = max(0LL, min(total - begin, share));
 
     uint8_t* ring = smem + warp * C::kWarpBytes;
@@ -321,13 +336,13 @@ stream_kernel(const __grid_constant__ Args a)
     // ---- producer: the step to issue next
     int pu = 0, pSub = 0, pStep = 0, pEnd = 0, pFirst = 0, pLo = 0, pHi = 0, pSubs = 1;
     const int32_t* table = nullptr;
-    int id = -1, pHead = 0;
+    int id = -1, pGroup = 0;
     bool pNew = true;         // first step of a segment
     auto enter_unit = [&]() {
         unit_range(a, pu, pLo, pHi);
         pFirst = pLo >> 4;
         pEnd = pFirst + unit_steps(pLo, pHi);
-        pSubs = (pu < a.prefixUnit ? a.tilesPrefix : a.tilesSeq) * a.Hkv;
+        pSubs = (pu < a.prefixUnit ? a.tilesPrefix : a.tilesSeq) * a.groups;
         table = pu < a.prefixUnit ? a.prefixTable : a.pageTable + (size_t)(pu - a.prefixUnit) * 2 * a.mpps;
     };
     // page id of this lane's token of the step (lanes 0..15: K plane, 16..31: V plane)
@@ -345,6 +360,7 @@ stream_kernel(const __grid_constant__ Args a)
         const int inPage = pos - divide(pos, a.divTpp) * a.tpp;
         const uint32_t row = mapped ? (uint32_t)id * (uint32_t)a.tpp + inPage : 0u;
         const uint32_t base = ringAddr + stage * C::kStageBytes;
+        const int pHead = pGroup * a.teamSize + warp;
         const uint8_t* headBase = a.pool + (size_t)pHead * kRowBytes;
         if (pagesAligned && ok == 0xffff) {
             // 16 consecutive rows of one K page and one V page
@@ -383,7 +399,7 @@ stream_kernel(const __grid_constant__ Args a)
             return;
         pNew = true;
         ++pSub;
-        pHead = pHead + 1 == a.Hkv ? 0 : pHead + 1;
+        pGroup = pGroup + 1 == a.groups ? 0 : pGroup + 1;
         if (pSub == pSubs) {
             pSub = 0;
             do {
@@ -411,7 +427,7 @@ stream_kernel(const __grid_constant__ Args a)
         const long long in = begin - at;
         pSub = (int)(in / n);
         pStep = pFirst + (int)(in - (long long)pSub * n);
-        pHead = pSub - divide(pSub, a.divHkv) * a.Hkv;
+        pGroup = pSub - divide(pSub, a.divGroups) * a.groups;
         fetch_id();
     }
     long long issued = 0;
@@ -458,8 +474,8 @@ stream_kernel(const __grid_constant__ Args a)
         if (meta.x & (1 << 16)) {
             // a segment begins: its rows, Q as B fragments (column n = lane / 4,
             // k = (lane % 4) * 2 + {0, 1} (+8))
-            const int t = divide(meta.w, a.divHkv);
-            head = meta.w - t * a.Hkv;
+            const int t = divide(meta.w, a.divGroups);
+            head = (meta.w - t * a.groups) * a.teamSize + warp;
             row0 = t * kRows;
             rowsOfUnit = prefix ? a.rowsPrefix : a.S * a.G;
             const int b = meta.z - a.prefixUnit;
@@ -601,7 +617,7 @@ stream_kernel(const __grid_constant__ Args a)
         // Where rows see different tokens a weight of 0 can meet an infinity or
         // NaN in V that another row sees: such values are taken out of the tile
         // and added to the rows that do see them.
-        if (a.S > 1 && !prefix && pos16 + 15 > last0) {
+        if (FMT != kInt8 && a.S > 1 && !prefix && pos16 + 15 > last0) {
             auto value = [&](int t, int d) -> float {
                 const uint8_t* p = stagePtr + 16 * kRowBytes +
                     swizzle<kChunks>(t, d * C::kEsize / 16) + (d * C::kEsize) % 16;
@@ -610,10 +626,14 @@ stream_kernel(const __grid_constant__ Args a)
                 const uint32_t two = decode_pair<FMT, 0x10>(*p);
                 return __half2float(__ushort_as_half((unsigned short)(two & 0xffff)));
             };
-            bool bad = false;
-            for (int x = lane; x < 16 * D; x += 32)
-                bad = bad || !(fabsf(value(x / D, x % D)) < INFINITY);
-            if (__any_sync(0xffffffffu, bad)) {
+            uint32_t bad = 0;
+            const uint4* v = reinterpret_cast<const uint4*>(stagePtr + 16 * kRowBytes);
+#pragma unroll
+            for (int x = 0; x < kChunks / 2; ++x) {
+                const uint4 y = v[x * 32 + lane];
+                bad |= non_finite<FMT>(y.x) | non_finite<FMT>(y.y) | non_finite<FMT>(y.z) | non_finite<FMT>(y.w);
+            }
+            if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -676,10 +696,10 @@ stream_kernel(const __grid_constant__ Args a)
         }
 
         if (meta.x & (1 << 17)) {
-            // the segment ends: slot item + warp
-            const long long item = (long long)(prefix ? 0 : a.tilesPrefix) * a.Hkv +
-                (prefix ? 0LL : (long long)(meta.z - a.prefixUnit) * a.tilesSeq * a.Hkv) + meta.w;
-            const size_t slot = (size_t)(item + w) * a.pitch;
+            // the segment ends: slots item + team
+            const long long item = prefix ? meta.w :
+                (a.tilesPrefix + (long long)(meta.z - a.prefixUnit) * a.tilesSeq) * a.groups + meta.w;
+            const size_t slot = (size_t)((item + blockIdx.x) * a.teamSize + warp) * a.pitch;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -725,7 +745,7 @@ stream_kernel(const __grid_constant__ Args a)
 // of D / 4 threads holds a row; SPLIT: the CTA's groups share one row's partials
 // (few rows with many segments each).
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int rowsPerTile)
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int tileShift)
 {
     constexpr int TG = D / 4, kGroups = 256 / TG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -739,6 +759,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const int h = divide(hq, a.divG), g = hq - h * a.G;
     const int b = divide(tok, a.divS), s = tok - b * a.S;
     const bool active = __ldg(a.kvLens + b) - (long long)a.S + s >= a.P;
+    const int units = a.B + a.prefixUnit;
+    const long long offset = a.offsets[b + a.prefixUnit], share = a.offsets[units + 1];
+    const bool small = a.offsets[units] < (1LL << 31);
+    const Divisor divShare = {(uint32_t)a.offsets[units + 2], (uint32_t)a.offsets[units + 3], 0};
 
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -771,23 +795,25 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
         for (int k = first; k < a.numParts; k += stride)
             join4(a.partL + headRow, partStride, a.partO + headRow * D + d, partStride * D, k, a.numParts);
-        const int units = a.B + a.prefixUnit;
-        const long long share = a.offsets[units + 1];
-        auto join_segments = [&](int u, int row, int tiles, long long itemBase) {
-            const long long at = a.offsets[u], all = a.offsets[u + 1] - at;
-            if (all == 0)
+        const int grp = divide(h, a.divTeam), member = h - grp * a.teamSize;
+        auto join_segments = [&](int n, long long at, int row, long long itemBase) {
+            if (n == 0)
                 return;
-            const int t = row / rowsPerTile, sub = t * a.Hkv + h;
-            const long long n = all / ((long long)tiles * a.Hkv);
-            const long long w0 = (at + sub * n) / share, w1 = (at + sub * n + n - 1) / share;
-            const size_t slot = (size_t)(itemBase + sub + w0) * a.pitch + (row - t * rowsPerTile);
+            const int t = row >> tileShift, sub = t * a.groups + grp;
+            at += (long long)sub * n;
+            const long long w0 = small ? divide((int)at, divShare) : at / share;
+            const long long w1 = small ? divide((int)at + n - 1, divShare) : (at + n - 1) / share;
+            const size_t slot = (size_t)((itemBase + sub + w0) * a.teamSize + member) * a.pitch + (row - (t << tileShift));
+            const size_t stepL = (size_t)a.teamSize * a.pitch;
             for (long long k = first; k < w1 - w0 + 1; k += stride)
-                join4(a.segL + slot, a.pitch, a.segO + slot * D + d, (size_t)a.pitch * D, k, w1 - w0 + 1);
+                join4(a.segL + slot, stepL, a.segO + slot * D + d, stepL * D, k, w1 - w0 + 1);
         };
         if (a.prefixUnit)
-            join_segments(0, tok * a.G + g, a.tilesPrefix, 0);
-        join_segments(b + a.prefixUnit, s * a.G + g, a.tilesSeq,
-                      ((long long)a.tilesPrefix + (long long)b * a.tilesSeq) * a.Hkv);
+            join_segments(unit_steps(0, a.P), 0, tok * a.G + g, 0);
+        int lo, hi;
+        unit_range(a, b + a.prefixUnit, lo, hi);
+        join_segments(unit_steps(lo, hi), offset, s * a.G + g,
+                      (a.tilesPrefix + (long long)b * a.tilesSeq) * a.groups);
     }
     if (SPLIT) {
         __shared__ float sm[kGroups], sl[kGroups];
