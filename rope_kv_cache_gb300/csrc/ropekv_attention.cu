@@ -138,7 +138,10 @@ Plan make_plan(const ropekv_attention_dims* d)
     p.pitch = (int)(longest < 8 * p.nt ? longest : 8 * p.nt);
     p.units = d->batch + p.tilesPrefix;
     const int perSm = stream_warps(d->headDim, d->cacheFormat, p.nt);
-    p.teamSize = team_size(d->numKVHeads, perSm);
+#ifndef TEAMDIV
+#define TEAMDIV 1
+#endif
+    p.teamSize = team_size(d->numKVHeads, perSm / TEAMDIV);
     p.groups = d->numKVHeads / p.teamSize;
     // the table's capacity bounds the steps; at least two of them make a share
     const long long own = (long long)d->maxPagesPerSeq * d->tokensPerPage - d->prefixLen;
@@ -228,7 +231,7 @@ int launch_all(const Args& a, const Plan& p, cudaStream_t st)
         return rc;
     // few rows whose items many warps share: all groups of a CTA join one row
     const long long rows = (long long)a.B * a.S * a.Hq;
-    constexpr int perCta = 1024 / D;
+    constexpr int perCta = 2048 / D;
     const int tileShift = p.nt == 1 ? 3 : p.nt == 2 ? 4 : 5;
     if (rows < 4LL * kSMs)
         return launch(ropekv_attn::join_kernel<D, true>, rows, 256, 0, true, st, a, tileShift);

@@ -94,9 +94,22 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok)
                  :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 
-__device__ __forceinline__ void copy16_full(uint32_t dst, const void* src)
+// Whole copies of data that is read once, evict-first in L2.
+__device__ __forceinline__ uint64_t stream_policy()
 {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void copy16_full(uint32_t dst, const void* src, uint64_t policy)
+{
+#ifdef NOHINT
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+#else
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(src), "l"(policy) : "memory");
+#endif
 }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok)
@@ -151,21 +164,29 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two 8-bit codes (bytes `lo` and `hi` of w) as two FP16 values; both formats'
-// codes are exact in FP16. INT8: byte ^ 0x80 is code + 128 unsigned; as the low
-// mantissa byte of 1024 (0x6400) it reads 1024 + 128 + code.
-template <int FMT, int SEL>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w)
+// The four 8-bit codes of a word as two pairs of FP16 values: bytes (0, 1) and
+// (2, 3), or with SWAP bytes (0, 2) and (1, 3). Both formats' codes are exact in
+// FP16. INT8: byte ^ 0x80 is code + 128 unsigned; as the low mantissa byte of 1024
+// (0x6400) it reads 1024 + 128 + code.
+template <int FMT, bool SWAP>
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t& lo, uint32_t& hi)
 {
     if (FMT == kE4M3) {
-        const uint32_t two = __byte_perm(w, 0, 0x4400 | SEL);
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffff), __NV_E4M3);
-        return (uint32_t)h.x | ((uint32_t)h.y << 16);
+        if (SWAP)
+            w = __byte_perm(w, 0, 0x3120);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+        return;
     }
-    const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u,
-                                   0x4040 | (SEL & 0xf) | ((SEL & 0xf0) << 4));
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&h);
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, SWAP ? 0x4240 : 0x4140);
+    const uint32_t b = __byte_perm(w, 0x64646464u, SWAP ? 0x4341 : 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // Not 0 if a word of V (two halves, four codes) holds an infinity or NaN.
@@ -330,6 +351,7 @@ stream_kernel(const __grid_constant__ Args a)
     const uint32_t ringAddr = smem_u32(ring);
     const size_t rowStride = (size_t)a.Hkv * kRowBytes;
     const bool pagesAligned = a.tpp % 16 == 0;
+    const uint64_t policy = stream_policy();
     // where this lane copies from inside 16 consecutive rows, and to
     const size_t laneSrc = (size_t)(lane / kChunks) * rowStride + (lane % kChunks) * 16;
 
@@ -370,7 +392,7 @@ stream_kernel(const __grid_constant__ Args a)
 #pragma unroll
                 for (int i = 0; i < kChunks / 2; ++i) {
                     const int r = i * (32 / kChunks) + lane / kChunks;
-                    copy16_full(base + p * 16 * kRowBytes + swizzle<kChunks>(r, lane % kChunks), src);
+                    copy16_full(base + p * 16 * kRowBytes + swizzle<kChunks>(r, lane % kChunks), src, policy);
                     src += (32 / kChunks) * rowStride;
                 }
             }
@@ -521,8 +543,9 @@ stream_kernel(const __grid_constant__ Args a)
                 ldmatrix4(x, kBase + swizzle<kChunks>(lane & 15, kk + (lane >> 4)));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t k4[4] = {decode_pair<FMT, 0x10>(x[2 * u]), decode_pair<FMT, 0x10>(x[2 * u + 1]),
-                                            decode_pair<FMT, 0x32>(x[2 * u]), decode_pair<FMT, 0x32>(x[2 * u + 1])};
+                    uint32_t k4[4];
+                    decode_word<FMT, false>(x[2 * u], k4[0], k4[2]);
+                    decode_word<FMT, false>(x[2 * u + 1], k4[1], k4[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma16816(s[nt], k4, qf[nt][kk + u]);
@@ -623,7 +646,8 @@ stream_kernel(const __grid_constant__ Args a)
                     swizzle<kChunks>(t, d * C::kEsize / 16) + (d * C::kEsize) % 16;
                 if (FMT == kF16)
                     return __half2float(*reinterpret_cast<const __half*>(p));
-                const uint32_t two = decode_pair<FMT, 0x10>(*p);
+                uint32_t two, other;
+                decode_word<FMT, false>(*p, two, other);
                 return __half2float(__ushort_as_half((unsigned short)(two & 0xffff)));
             };
             uint32_t bad = 0;
@@ -686,8 +710,9 @@ stream_kernel(const __grid_constant__ Args a)
                                                             mt + (lane >> 4)));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t v4[4] = {decode_pair<FMT, 0x20>(x[2 * u]), decode_pair<FMT, 0x31>(x[2 * u]),
-                                            decode_pair<FMT, 0x20>(x[2 * u + 1]), decode_pair<FMT, 0x31>(x[2 * u + 1])};
+                    uint32_t v4[4];
+                    decode_word<FMT, true>(x[2 * u], v4[0], v4[1]);
+                    decode_word<FMT, true>(x[2 * u + 1], v4[2], v4[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma16816(acc[nt][mt + u], v4, pf[nt]);
@@ -742,15 +767,15 @@ stream_kernel(const __grid_constant__ Args a)
 //
 // Joins the partials of every output row: the prefix's (numParts ranges, or the
 // segments of the prefix unit) and the row's own segments, in that order. A group
-// of D / 4 threads holds a row; SPLIT: the CTA's groups share one row's partials
+// of D / 8 threads holds a row; SPLIT: the CTA's groups share one row's partials
 // (few rows with many segments each).
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int tileShift)
 {
-    constexpr int TG = D / 4, kGroups = 256 / TG;
+    constexpr int TG = D / 8, kGroups = 256 / TG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int group = threadIdx.x / TG, d = threadIdx.x % TG * 4;
+    const int group = threadIdx.x / TG, d = threadIdx.x % TG * 8;
     const int hv = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * kGroups + group;   // (token, q head)
     const int rows = a.B * a.S * a.Hq;
     if (!SPLIT && hv >= rows)
@@ -765,28 +790,42 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const Divisor divShare = {(uint32_t)a.offsets[units + 2], (uint32_t)a.offsets[units + 3], 0};
 
     float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float o[8] = {};
     // four partials at a time: their loads are in flight together
-    auto join4 = [&](const float* L, size_t strideL, const float* O, size_t strideO, long long k, long long n) {
+    auto join4 = [&](const float* L, size_t strideL, const float* O, size_t strideO, int n) {
         float x[4];
-        float4 v[4];
+        float4 v[4][2];
+        float top = m;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool in = k + j < n;
-            x[j] = in ? L[(k + j) * strideL] : -INFINITY;
-            v[j] = in ? *reinterpret_cast<const float4*>(O + (k + j) * strideO) : make_float4(0, 0, 0, 0);
+            x[j] = -INFINITY;
+            v[j][0] = v[j][1] = make_float4(0, 0, 0, 0);
+            if (j < n) {
+                x[j] = *L;
+                v[j][0] = *reinterpret_cast<const float4*>(O);
+                v[j][1] = *reinterpret_cast<const float4*>(O + 4);
+            }
+            L += strideL;
+            O += strideO;
         }
 #pragma unroll
+        for (int j = 0; j < 4; ++j)
+            top = fmaxf(top, x[j]);
+        const float mm = top == -INFINITY ? 0.0f : top;
+        const float f = exp2_fast(m - mm);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            o[k] *= f;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float top = fmaxf(m, x[j]);
-            const float mm = top == -INFINITY ? 0.0f : top;
-            const float f = exp2_fast(m - mm), w = exp2_fast(x[j] - mm);
-            m = top;
-            l = l * f + w;
-            o.x = o.x * f + w * v[j].x;
-            o.y = o.y * f + w * v[j].y;
-            o.z = o.z * f + w * v[j].z;
-            o.w = o.w * f + w * v[j].w;
+            const float w = exp2_fast(x[j] - mm);
+            const float* y = reinterpret_cast<const float*>(v[j]);
+            l += w;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                o[k] += w * y[k];
         }
     };
     if (active) {
@@ -794,7 +833,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         const size_t headRow = (size_t)h * a.rowsPrefix + (size_t)tok * a.G + g;
         const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
         for (int k = first; k < a.numParts; k += stride)
-            join4(a.partL + headRow, partStride, a.partO + headRow * D + d, partStride * D, k, a.numParts);
+            join4(a.partL + k * partStride + headRow, partStride, a.partO + (k * partStride + headRow) * D + d,
+                  partStride * D, a.numParts - k);
         const int grp = divide(h, a.divTeam), member = h - grp * a.teamSize;
         auto join_segments = [&](int n, long long at, int row, long long itemBase) {
             if (n == 0)
@@ -805,8 +845,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
             const long long w1 = small ? divide((int)at + n - 1, divShare) : (at + n - 1) / share;
             const size_t slot = (size_t)((itemBase + sub + w0) * a.teamSize + member) * a.pitch + (row - (t << tileShift));
             const size_t stepL = (size_t)a.teamSize * a.pitch;
-            for (long long k = first; k < w1 - w0 + 1; k += stride)
-                join4(a.segL + slot, stepL, a.segO + slot * D + d, stepL * D, k, w1 - w0 + 1);
+            const int segments = (int)(w1 - w0) + 1;
+            for (int k = first; k < segments; k += stride)
+                join4(a.segL + slot + k * stepL, stepL, a.segO + (slot + k * stepL) * D + d, stepL * D, segments - k);
         };
         if (a.prefixUnit)
             join_segments(unit_steps(0, a.P), 0, tok * a.G + g, 0);
@@ -817,12 +858,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     }
     if (SPLIT) {
         __shared__ float sm[kGroups], sl[kGroups];
-        __shared__ float4 so[256];
+        __shared__ float so[kGroups][D];
         if (d == 0) {
             sm[group] = m;
             sl[group] = l;
         }
-        so[threadIdx.x] = o;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            so[group][d + k] = o[k];
         __syncthreads();
         if (group > 0)
             return;
@@ -830,18 +873,24 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
             m = fmaxf(m, sm[k]);
         const float mm = m == -INFINITY ? 0.0f : m;
         l = 0.0f;
-        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = 0; k < kGroups; ++k) {
-            const float w = exp2_fast(sm[k] - mm);
-            const float4 v = so[k * TG + threadIdx.x];
-            l += w * sl[k];
-            o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            o[k] = 0.0f;
+        for (int x = 0; x < kGroups; ++x) {
+            const float w = exp2_fast(sm[x] - mm);
+            l += w * sl[x];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                o[k] += w * so[x][d + k];
         }
     }
     const bool none = l == 0.0f;
     const float inv = none ? 0.0f : 1.0f / l;
-    *reinterpret_cast<uint2*>(a.out + (size_t)hv * D + d) =
-        none ? make_uint2(0, 0) : make_uint2(half2_bits(o.x * inv, o.y * inv), half2_bits(o.z * inv, o.w * inv));
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (!none)
+        y = make_uint4(half2_bits(o[0] * inv, o[1] * inv), half2_bits(o[2] * inv, o[3] * inv),
+                       half2_bits(o[4] * inv, o[5] * inv), half2_bits(o[6] * inv, o[7] * inv));
+    *reinterpret_cast<uint4*>(a.out + (size_t)hv * D + d) = y;
     if (d == 0 && a.lse != nullptr)
         a.lse[hv] = none ? -INFINITY : kLn2 * (m + log2f(l));
 }

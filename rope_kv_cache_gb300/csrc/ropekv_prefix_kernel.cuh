@@ -469,8 +469,9 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = ok ? decode_pair<FMT, 0x10>(w[k]) ^ sign : 0u;
-                        o[2 * k + 1] = ok ? decode_pair<FMT, 0x32>(w[k]) ^ sign : 0u;
+                        decode_word<FMT, false>(w[k], o[2 * k], o[2 * k + 1]);
+                        o[2 * k] = ok ? o[2 * k] ^ sign : 0u;
+                        o[2 * k + 1] = ok ? o[2 * k + 1] ^ sign : 0u;
                     }
                     *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
