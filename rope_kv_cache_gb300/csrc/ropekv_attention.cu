@@ -47,9 +47,11 @@ int check_dims(const ropekv_attention_dims* d)
     return ROPEKV_OK;
 }
 
-// A kernel's dynamic shared memory limit is raised once per device.
+// A kernel's dynamic shared memory limit is raised once per device. `regs`: the
+// registers per thread that its register split counts on (0: none); a kernel
+// compiled to another number must not run, its warps would wait for them.
 template <auto Kern>
-bool raise_smem(int bytes)
+bool raise_smem(int bytes, int regs = 0)
 {
     static std::atomic<unsigned long long> raised{0};
     int dev = 0;
@@ -58,6 +60,9 @@ bool raise_smem(int bytes)
     const unsigned long long bit = (dev >= 0 && dev < 64) ? 1ULL << dev : 0;
     if (bit && (raised.load(std::memory_order_relaxed) & bit))
         return true;
+    cudaFuncAttributes attr;
+    if (regs > 0 && (cudaFuncGetAttributes(&attr, Kern) != cudaSuccess || attr.numRegs != regs))
+        return false;
     if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return false;
     raised.fetch_or(bit, std::memory_order_relaxed);
@@ -81,12 +86,6 @@ int launch(Kern kern, long long grid, int threads, int smem, bool dependent, cud
     cfg.numAttrs = dependent ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
-
-// CTAs of the stream grid for each that fits on the GPU.
-#ifndef ROPEKV_OVER
-#define ROPEKV_OVER 1
-#endif
-constexpr int kOver = ROPEKV_OVER;
 
 // How a call is cut into launches, from its sizes alone.
 struct Plan {
@@ -138,17 +137,14 @@ Plan make_plan(const ropekv_attention_dims* d)
     p.pitch = (int)(longest < 8 * p.nt ? longest : 8 * p.nt);
     p.units = d->batch + p.tilesPrefix;
     const int perSm = stream_warps(d->headDim, d->cacheFormat, p.nt);
-#ifndef TEAMDIV
-#define TEAMDIV 1
-#endif
-    p.teamSize = team_size(d->numKVHeads, perSm / TEAMDIV);
+    p.teamSize = team_size(d->numKVHeads, perSm);
     p.groups = d->numKVHeads / p.teamSize;
     // the table's capacity bounds the steps; at least two of them make a share
     const long long own = (long long)d->maxPagesPerSeq * d->tokensPerPage - d->prefixLen;
     const long long items = (long long)d->batch * p.tilesSeq * p.groups;
     const long long steps = items * (own > 0 ? own / 16 + 2 : 0) +
                             (p.tilesPrefix ? (long long)p.groups * (d->prefixLen / 16 + 1) : 0);
-    const long long most = (long long)kSMs * (perSm / p.teamSize) * kOver, want = (steps + 1) / 2;
+    const long long most = (long long)kSMs * (perSm / p.teamSize), want = (steps + 1) / 2;
     p.teams = (int)(want < 1 ? 1 : want < most ? want : most);
     p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
     if (p.tensor) {
@@ -193,7 +189,7 @@ int launch_prefix(const Args& a, const Plan& p, cudaStream_t st)
 {
     constexpr auto kern = ropekv_attn::prefix_kernel<D, FMT, MT>;
     using C = PrefixConfig<D, FMT, MT>;
-    if (!raise_smem<kern>(C::kSmem))
+    if (!raise_smem<kern>(C::kSmem, C::kSplit ? C::kLaunchRegs : 0))
         return ROPEKV_ERR_LAUNCH;
     return launch(kern, (long long)p.prefixTiles * a.Hkv * p.parts, C::kThreads, C::kSmem, false, st, a);
 }

@@ -88,6 +88,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p)
 }
 
 // 16-byte (4-byte) asynchronous copy; zeros where !ok (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -104,12 +109,8 @@ __device__ __forceinline__ uint64_t stream_policy()
 
 __device__ __forceinline__ void copy16_full(uint32_t dst, const void* src, uint64_t policy)
 {
-#ifdef NOHINT
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-#else
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;"
                  :: "r"(dst), "l"(src), "l"(policy) : "memory");
-#endif
 }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok)
@@ -127,6 +128,11 @@ template <int N>
 __device__ __forceinline__ void copy_wait()
 {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+__device__ __forceinline__ void copy_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t r[4], uint32_t addr)

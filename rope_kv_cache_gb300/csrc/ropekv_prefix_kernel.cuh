@@ -12,9 +12,11 @@
 //   warp 8            issues tcgen05.mma from one thread: S from shared memory
 //                     (both operands K-major), O with P from TMEM and V from
 //                     shared memory (N-major: V is stored as it lies in the cache)
-//   warps 9-11        fetch pages: a ring of tiles K0, V0, K1, V1, ... in shared
+//   warps 9-          fetch pages: a ring of tiles K0, V0, K1, V1, ... in shared
 //                     memory, 128-byte swizzled rows of 64 dims. FP16 rows come by
-//                     cp.async; 8-bit rows are decoded to FP16 (exact) on the way
+//                     cp.async (three warps); 8-bit rows are decoded to FP16 (exact)
+//                     on the way, which takes seven: 512 threads, whose registers
+//                     are split 168 for the softmax and 88 for the others
 //
 // Items i = 0, 1, ... alternate between two TMEM slots for S. With two row tiles
 // item i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i: either way
@@ -45,7 +47,15 @@ struct PrefixConfig {
     static constexpr int kMeta = 4;                        // tiles whose scales are kept
     static constexpr int kQBytes = MT * 128 * D * 2;
     static constexpr int kGroups = kTile / 32;             // 32 rows of a tile: one warp's copy
-    static constexpr int kThreads = 384;
+    // 8-bit rows are decoded by seven warps, FP16 rows only copied, by three
+    static constexpr int kFetchers = FMT == kF16 ? 3 : 7;
+    static constexpr int kThreads = (9 + kFetchers) * 32;
+    // registers move from the fetching warps to the softmax (a row of 128 scores)
+    static constexpr bool kSplit = kThreads == 512 && kTile == 128;
+    static constexpr int kLaunchRegs = 128;
+    // arrivals that complete a tile: per group of rows one of each lane's copies and one of
+    // the warp (FP16), or the warp's alone
+    static constexpr int kArrivals = kGroups * (FMT == kF16 ? 33 : 1);
     // TMEM columns: S slots, then O of each row tile
     static constexpr int kColO = 2 * kTile;
     static constexpr int kCols = 512;
@@ -218,7 +228,7 @@ __device__ __forceinline__ uint32_t tile_pos(int rows, int r, int c)
 }
 
 template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_kernel(const __grid_constant__ Args a)
 {
     using C = PrefixConfig<D, FMT, MT>;
     constexpr int TN = C::kTile, NS = C::kStages, GP = C::kGroups;
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(kvFull + 8 * i, GP);
+            mbar_init(kvFull + 8 * i, C::kArrivals);
             mbar_init(kvEmpty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -284,6 +294,10 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
     const uint32_t tmem = *tmemSlot;
     const int items = MT * J;
 
+    // 256 x 168 + 256 x 88 registers is what a launch of 512 x 128 has
+    if (warp >= 8) {
+        if (C::kSplit)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
         // ------------------------------------------------------- MMA issue
         if (lane == 0) {
@@ -293,6 +307,8 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                 const int st = (2 * j) % NS;
                 if (tile == 0)
                     mbar_wait(kvFull + 8 * st, ((2 * j) / NS) & 1, failed);
+                if (FMT == kF16)
+                    fence_async_smem();  // the copies landed in the generic proxy
                 tmem_fence_after();
                 const uint32_t qa = base + tile * (128 * D * 2);
                 const uint32_t ka = base + C::kOffRing + st * C::kTileBytes;
@@ -312,6 +328,8 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                 mbar_wait(pFull + 8 * (i & 1), (i >> 1) & 1, failed);
                 if (tile == 0)
                     mbar_wait(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed);
+                if (FMT == kF16)
+                    fence_async_smem();
                 tmem_fence_after();
                 const uint32_t va = base + C::kOffRing + st * C::kTileBytes;
 #pragma unroll
@@ -332,7 +350,7 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
                     issue_s(i + 2);
             }
         }
-    } else if (warp > 8) {
+    } else {
         // ------------------------------------------------------- page fetch
         const int me = warp - 9;
         const int groups = 2 * J * GP;
@@ -340,6 +358,8 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
         const uint8_t* headBase = a.pool + (size_t)h * D * kEsize;
         constexpr int kVecs = D * kEsize / 16;         // 16-byte vectors of a row
         constexpr int kPerLane = kVecs;                // 32 rows of kVecs vectors over 32 lanes
+        constexpr int kStep = C::kFetchers;
+        constexpr int kDepth = kVecs > 4 ? 1 : 2;      // 8-bit: groups of a warp in flight
 
         int idK = -1, idV = -1;                        // page ids of this lane's row of a group
         auto fetch_ids = [&](int u) {
@@ -376,112 +396,124 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
             if (lane == 0)
                 reinterpret_cast<uint32_t*>(smem + C::kOffMask)[slot * 4 + g] = mask;
         };
-        auto wait_empty = [&](int u) {
-            const int t = u / GP;
-            if (t >= NS)
-                mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
-            __syncwarp();
-        };
-        auto publish = [&](int u) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(kvFull + 8 * ((u / GP) % NS));
-        };
-
         fetch_ids(me);
         if (FMT == kF16) {
-            int pending = -1;
-            for (int u = me; u < groups; u += 3) {
+            // the copies arrive at the tile's barrier by themselves when they land
+            for (int u = me; u < groups; u += kStep) {
                 uint32_t mask;
                 const uint32_t row = locate(u, mask);
-                fetch_ids(u + 3);
-                wait_empty(u);
-                const uint32_t dst = base + C::kOffRing + ((u / GP) % NS) * C::kTileBytes;
+                fetch_ids(u + kStep);
+                const int t = u / GP;
+                if (t >= NS)
+                    mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
+                __syncwarp();
+                const uint32_t dst = base + C::kOffRing + (t % NS) * C::kTileBytes;
                 const int r0 = (u % GP) * 32;
+                if (mask == 0xffffffffu) {
 #pragma unroll
-                for (int i = 0; i < kPerLane; ++i) {
-                    const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
-                    const uint32_t src = __shfl_sync(0xffffffffu, row, r);
-                    copy16(dst + tile_pos(TN, r0 + r, c), headBase + (size_t)src * rowStride + c * 16,
-                           (mask >> r) & 1);
+                    for (int i = 0; i < kPerLane; ++i) {
+                        const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
+                        const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                        copy16(dst + tile_pos(TN, r0 + r, c), headBase + (size_t)src * rowStride + c * 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i) {
+                        const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
+                        const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                        copy16(dst + tile_pos(TN, r0 + r, c), headBase + (size_t)src * rowStride + c * 16,
+                               (mask >> r) & 1);
+                    }
                 }
-                copy_commit();
-                if (!((u / GP) & 1))
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];"
+                             :: "r"(kvFull + 8 * (t % NS)) : "memory");
+                if (!(t & 1))
                     write_meta(u, mask, 0.0f, 0.0f);
-                if (pending >= 0) {
-                    copy_wait<1>();
-                    publish(pending);
-                }
-                pending = u;
+                if (lane == 0)
+                    mbar_arrive(kvFull + 8 * (t % NS));
             }
-            copy_wait<0>();
-            if (pending >= 0)
-                publish(pending);
+            copy_wait_all();
         } else {
-            uint4 buf[kPerLane];
-            float ks = 0.0f, vs = 0.0f;
-            uint32_t mask = 0;
-            auto load = [&](int u) {
-                const uint32_t row = locate(u, mask);
-                ks = vs = 0.0f;
-                if ((mask >> lane) & 1) {
+            // registers of kDepth groups in flight
+            auto publish = [&](int u) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(kvFull + 8 * ((u / GP) % NS));
+            };
+            uint4 buf[kDepth][kPerLane];
+            float ks[kDepth], vs[kDepth];
+            uint32_t mask[kDepth];
+            auto load = [&](int u, int k) {
+                const uint32_t row = locate(u, mask[k]);
+                ks[k] = vs[k] = 0.0f;
+                if ((mask[k] >> lane) & 1) {
                     const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
                     const int inPage = pos - divide(pos, a.divTpp) * a.tpp;
-                    ks = __ldg(a.scales + ((size_t)idK * a.Hkv + h) * a.tpp + inPage);
-                    vs = __ldg(a.scales + ((size_t)idV * a.Hkv + h) * a.tpp + inPage);
+                    ks[k] = __ldg(a.scales + ((size_t)idK * a.Hkv + h) * a.tpp + inPage);
+                    vs[k] = __ldg(a.scales + ((size_t)idV * a.Hkv + h) * a.tpp + inPage);
                 }
 #pragma unroll
                 for (int i = 0; i < kPerLane; ++i) {
                     const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
                     const uint32_t src = __shfl_sync(0xffffffffu, row, r);
-                    buf[i] = make_uint4(0, 0, 0, 0);
-                    if ((mask >> r) & 1)
-                        buf[i] = __ldg(reinterpret_cast<const uint4*>(headBase + (size_t)src * rowStride + c * 16));
+                    buf[k][i] = make_uint4(0, 0, 0, 0);
+                    if ((mask[k] >> r) & 1)
+                        buf[k][i] = __ldg(reinterpret_cast<const uint4*>(headBase + (size_t)src * rowStride + c * 16));
                 }
+                fetch_ids(u + kStep);
             };
-            if (me < groups)
-                load(me);
-            fetch_ids(me + 3);
-            for (int u = me; u < groups; u += 3) {
-                uint4 cur[kPerLane];
 #pragma unroll
-                for (int i = 0; i < kPerLane; ++i)
-                    cur[i] = buf[i];
-                const uint32_t curMask = mask;
-                const float curK = ks, curV = vs;
-                // V rows whose scale is 0 or negative
-                const bool isV = (u / GP) & 1;
-                const uint32_t dead = isV ? __ballot_sync(0xffffffffu, curV == 0.0f) : ~curMask;
-                const uint32_t flip = isV ? __ballot_sync(0xffffffffu, curV < 0.0f) : 0u;
-                if (u + 3 < groups)
-                    load(u + 3);
-                fetch_ids(u + 6);
-                wait_empty(u);
-                uint8_t* dst = smem + C::kOffRing + ((u / GP) % NS) * C::kTileBytes;
-                const int r0 = (u % GP) * 32;
+            for (int k = 0; k < kDepth; ++k)
+                if (me + kStep * k < groups)
+                    load(me + kStep * k, k);
+            for (int v = me; v < groups; v += kStep * kDepth) {
 #pragma unroll
-                for (int i = 0; i < kPerLane; ++i) {
-                    const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
-                    const bool ok = !((dead >> r) & 1);   // else zeros: unmapped tokens among them
-                    const uint32_t sign = (flip >> r) & 1 ? 0x80008000u : 0u;
-                    const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-                    uint32_t o[8];
+                for (int k = 0; k < kDepth; ++k) {
+                    const int u = v + kStep * k;
+                    if (u >= groups)
+                        break;
+                    const int t = u / GP;
+                    if (t >= NS)
+                        mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
+                    __syncwarp();
+                    uint8_t* dst = smem + C::kOffRing + (t % NS) * C::kTileBytes;
+                    const int r0 = (u % GP) * 32;
+                    // zero rows: unmapped tokens and V rows with scale 0; V rows with a negative scale
+                    const uint32_t dead = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] == 0.0f) : ~mask[k];
+                    const uint32_t flip = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] < 0.0f) : 0u;
+                    const bool plain = (dead | flip) == 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        decode_word<FMT, false>(w[k], o[2 * k], o[2 * k + 1]);
-                        o[2 * k] = ok ? o[2 * k] ^ sign : 0u;
-                        o[2 * k + 1] = ok ? o[2 * k + 1] ^ sign : 0u;
+                    for (int i = 0; i < kPerLane; ++i) {
+                        const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
+                        const uint32_t w[4] = {buf[k][i].x, buf[k][i].y, buf[k][i].z, buf[k][i].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            decode_word<FMT, false>(w[x], o[2 * x], o[2 * x + 1]);
+                        if (!plain) {
+                            const uint32_t keep = (dead >> r) & 1 ? 0u : 0xffffffffu;
+                            const uint32_t sign = (flip >> r) & 1 ? 0x80008000u : 0u;
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                o[x] = (o[x] ^ sign) & keep;
+                        }
+                        *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    if (!(t & 1))
+                        write_meta(u, mask[k], ks[k], vs[k]);
+                    publish(u);
+                    if (u + kStep * kDepth < groups)
+                        load(u + kStep * kDepth, k);
                 }
-                if (!((u / GP) & 1))
-                    write_meta(u, curMask, curK, curV);
-                publish(u);
             }
         }
-    } else if (warp < 4 * MT) {
+    }
+    } else {
+        if (C::kSplit)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if (warp < 4 * MT) {
         // ----------------------------------------------------------- softmax
         const int tile = warp >> 2;
         const uint32_t laneBase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -636,6 +668,7 @@ __global__ void __launch_bounds__(384, 1) prefix_kernel(const __grid_constant__ 
         if (live)
             a.partL[r] = none ? -INFINITY + bad : M + log2f(l) + bad;
         tmem_fence_before();
+    }
     }
     __syncthreads();
     if (warp == 8) {
