@@ -1,17 +1,19 @@
 """Build libropekv.so (the C ABI and its sm_103a kernels) in-tree with nvcc,
-libropekv_serving.so (the serving operators around the paged cache), and
-libropekv_floor.so, the copy kernel the benchmark times as the floor of a
-decode-sized launch.
+libropekv_serving.so (the serving operators around the paged cache) with
+ropekv_bind.so, its Python module for torch tensors, and libropekv_floor.so, the
+copy kernel the benchmark times as the floor of a decode-sized launch.
 
 Each library is compiled for sm_103a only and linked against the static CUDA
-runtime, so it loads without any other file from this package; all translation
-units compile in parallel. Output: ``rope_kv_cache_gb300/lib/`` (git-ignored).
+runtime, so it loads without any other file from this package (the Python module
+needs libropekv_serving.so beside it); all translation units compile in parallel.
+Output: ``rope_kv_cache_gb300/lib/`` (git-ignored).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,6 +32,9 @@ SERVING_SOURCES = [os.path.join(CSRC, "ropekv_serving.cu"),
 SERVING_DEPS = SERVING_SOURCES + [os.path.join(CSRC, n) for n in (
     "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh", "ropekv_prefix_kernel.cuh")] + [
     os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
+BIND_PATH = os.path.join(LIB_DIR, "ropekv_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "ropekv_bind.cpp")
+BIND_DEPS = [BIND_SOURCE] + [os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -46,6 +51,25 @@ def nvcc_command(out: str, extra=(), sources=None) -> list:
             "-I", INCLUDE, "-I", CSRC, *extra, "-o", out, *(sources or SOURCES)]
 
 
+def bind_commands(out: str, obj: str) -> tuple:
+    """Compile and link commands of the Python module."""
+    import torch  # headers and libraries of the installed torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    lib = os.path.join(root, "lib")
+    compile_ = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+                "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda, "include"),
+                "-isystem", sysconfig.get_paths()["include"], "-c", "-o", obj, BIND_SOURCE]
+    link = [os.environ.get("CXX", "g++"), "-shared", "-o", out, obj, "-L", LIB_DIR, "-lropekv_serving",
+            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    return compile_, link
+
+
 def _stale(lib: str, deps) -> bool:
     return not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(p) for p in deps)
 
@@ -55,24 +79,29 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     path of libropekv.so."""
     os.makedirs(LIB_DIR, exist_ok=True)
     extra = ("-Xptxas", "-v") if verbose else ()
-    jobs = []   # (compilers, their objects (none: the library itself), output, library)
+    jobs = []   # (compilers, their objects, link command (None: nothing to link), output, library)
     for lib, sources, deps in ((LIB_PATH, SOURCES, DEPS),
                                (FLOOR_LIB_PATH, FLOOR_SOURCES, FLOOR_DEPS),
                                (SERVING_LIB_PATH, SERVING_SOURCES, SERVING_DEPS)):
         if force or _stale(lib, deps):
             tmp = lib + f".{os.getpid()}.tmp"
             if len(sources) == 1:
-                jobs.append(([subprocess.Popen(nvcc_command(tmp, extra, sources))], [], tmp, lib))
+                jobs.append(([subprocess.Popen(nvcc_command(tmp, extra, sources))], [], None, tmp, lib))
             else:
                 objs = [f"{tmp}.{i}.o" for i in range(len(sources))]
-                jobs.append(([subprocess.Popen([a for a in nvcc_command(o, (*extra, "-c"), [src])
-                                                if a != "-shared"])
-                              for o, src in zip(objs, sources)], objs, tmp, lib))
+                procs = [subprocess.Popen([a for a in nvcc_command(o, (*extra, "-c"), [src])
+                                           if a != "-shared"]) for o, src in zip(objs, sources)]
+                jobs.append((procs, objs, nvcc_command(tmp, (), objs), tmp, lib))
+    if force or _stale(BIND_PATH, BIND_DEPS):
+        # after the library that it links with
+        tmp = BIND_PATH + f".{os.getpid()}.tmp"
+        compile_, link = bind_commands(tmp, tmp + ".o")
+        jobs.append(([subprocess.Popen(compile_)], [tmp + ".o"], link, tmp, BIND_PATH))
     failed = []
-    for procs, objs, tmp, lib in jobs:
+    for procs, objs, link, tmp, lib in jobs:
         ok = all([p.wait() == 0 for p in procs])
-        if ok and objs:
-            ok = subprocess.run(nvcc_command(tmp, (), objs)).returncode == 0
+        if ok and link:
+            ok = subprocess.run(link).returncode == 0
         for o in objs:
             if os.path.exists(o):
                 os.remove(o)
@@ -81,7 +110,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         else:
             failed.append(os.path.basename(lib))
     if failed:
-        raise RuntimeError(f"nvcc failed for {', '.join(failed)}")
+        raise RuntimeError(f"the compiler failed for {', '.join(failed)}")
     return LIB_PATH
 
 
