@@ -65,7 +65,7 @@ struct PrefixConfig {
     static constexpr int kOffRv = kOffVs + kMeta * kTile * 4;
     static constexpr int kOffMask = kOffRv + kMeta * kTile * 4;
     static constexpr int kOffBar = kOffMask + kMeta * 16;
-    static constexpr int kUsed = kOffBar + (2 * kStages + 6) * 8 + 16;
+    static constexpr int kUsed = kOffBar + (2 * kStages + 7) * 8 + 16;
     // one CTA per SM (each takes all of TMEM)
     static constexpr int kSmem = (kUsed > 120 * 1024 ? kUsed : 120 * 1024) + 1024;
 };
@@ -243,9 +243,9 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
 
     const uint32_t bars = base + C::kOffBar;
     const uint32_t kvFull = bars, kvEmpty = bars + NS * 8, sFull = bars + 2 * NS * 8,
-                   pFull = sFull + 16, oDone = pFull + 16;
-    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffBar + (2 * NS + 6) * 8);
-    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + (2 * NS + 6) * 8 + 8);
+                   pFull = sFull + 16, oDone = pFull + 16, qFull = oDone + 16;
+    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffBar + (2 * NS + 7) * 8);
+    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + (2 * NS + 7) * 8 + 8);
 
     // blockIdx.x = (row tile * Hkv + head) * parts + part
     const int part = blockIdx.x % a.numParts;
@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             mbar_init(pFull + 8 * i, 128);
             mbar_init(oDone + 8 * i, 1);
         }
+        mbar_init(qFull, MT * 128);
         *failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -275,19 +276,6 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                      :: "r"(smem_u32(tmemSlot)), "n"(C::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // Q, zeros past the last row
-    for (int i = threadIdx.x; i < MT * 128 * (D / 8); i += C::kThreads) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        const int row = row0 + r;
-        const bool ok = row < a.rowsPrefix;
-        const size_t tok = ok ? divide(row, a.divG) : 0;
-        const int g = ok ? row - (int)tok * a.G : 0;
-        copy16(base + (r >> 7) * (128 * D * 2) + tile_pos(128, r & 127, c),
-               a.q + (tok * a.Hq + h * a.G + g) * D + c * 8, ok);
-    }
-    copy_commit();
-    copy_wait<0>();
-    fence_async_smem();
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -307,7 +295,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 const int st = (2 * j) % NS;
                 if (tile == 0)
                     mbar_wait(kvFull + 8 * st, ((2 * j) / NS) & 1, failed);
-                if (FMT == kF16)
+                if (FMT == kF16 || i == 0)
                     fence_async_smem();  // the copies landed in the generic proxy
                 tmem_fence_after();
                 const uint32_t qa = base + tile * (128 * D * 2);
@@ -340,8 +328,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 if (tile == MT - 1 && 2 * j + 1 + NS < 2 * J)
                     mma_commit(kvEmpty + 8 * st);
             };
-            if (items > 0)
+            if (items > 0) {
+                mbar_wait(qFull, 0, failed);
                 issue_s(0);
+            }
             if (items > 1)
                 issue_s(1);
             for (int i = 0; i < items; ++i) {
@@ -358,11 +348,13 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         const uint8_t* headBase = a.pool + (size_t)h * D * kEsize;
         constexpr int kVecs = D * kEsize / 16;         // 16-byte vectors of a row
         constexpr int kPerLane = kVecs;                // 32 rows of kVecs vectors over 32 lanes
-        constexpr int kStep = C::kFetchers;
         constexpr int kDepth = kVecs > 4 ? 1 : 2;      // 8-bit: groups of a warp in flight
 
-        int idK = -1, idV = -1;                        // page ids of this lane's row of a group
-        auto fetch_ids = [&](int u) {
+        // page ids of this lane's row of the next kIds groups: an id is a round trip to L2
+        // ahead of the copies that need it
+        constexpr int kIds = 4;
+        int idsK[kIds], idsV[kIds];
+        auto fetch_ids = [&](int u, int& idK, int& idV) {
             idK = idV = -1;
             const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
             if (u < groups && pos < a.P) {
@@ -371,9 +363,8 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 idV = __ldg(a.prefixTable + a.prefixPages + lp);
             }
         };
-        // Row of the pool for this lane's token and the mask of mapped tokens; for K
-        // groups also the token's scales.
-        auto locate = [&](int u, uint32_t& mask) -> uint32_t {
+        // Row of the pool for this lane's token and the mask of mapped tokens
+        auto locate = [&](int u, int idK, int idV, uint32_t& mask) -> uint32_t {
             const int t = u / GP, g = u % GP;
             const int pos = (tile0 + (t >> 1)) * TN + g * 32 + lane;
             const bool ok = idK >= 0 && idK < a.numPages && idV >= a.numPages &&
@@ -396,13 +387,21 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             if (lane == 0)
                 reinterpret_cast<uint32_t*>(smem + C::kOffMask)[slot * 4 + g] = mask;
         };
-        fetch_ids(me);
+        constexpr int kStep = C::kFetchers;
+#pragma unroll
+        for (int x = 0; x < kIds; ++x)
+            fetch_ids(me + kStep * x, idsK[x], idsV[x]);
         if (FMT == kF16) {
             // the copies arrive at the tile's barrier by themselves when they land
-            for (int u = me; u < groups; u += kStep) {
+            for (int v = me; v < groups; v += kStep * kIds) {
+#pragma unroll
+            for (int x = 0; x < kIds; ++x) {
+                const int u = v + kStep * x;
+                if (u >= groups)
+                    break;
                 uint32_t mask;
-                const uint32_t row = locate(u, mask);
-                fetch_ids(u + kStep);
+                const uint32_t row = locate(u, idsK[x], idsV[x], mask);
+                fetch_ids(u + kStep * kIds, idsK[x], idsV[x]);
                 const int t = u / GP;
                 if (t >= NS)
                     mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
@@ -432,6 +431,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 if (lane == 0)
                     mbar_arrive(kvFull + 8 * (t % NS));
             }
+            }
             copy_wait_all();
         } else {
             // registers of kDepth groups in flight
@@ -444,8 +444,8 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             uint4 buf[kDepth][kPerLane];
             float ks[kDepth], vs[kDepth];
             uint32_t mask[kDepth];
-            auto load = [&](int u, int k) {
-                const uint32_t row = locate(u, mask[k]);
+            auto load = [&](int u, int k, int& idK, int& idV) {
+                const uint32_t row = locate(u, idK, idV, mask[k]);
                 ks[k] = vs[k] = 0.0f;
                 if ((mask[k] >> lane) & 1) {
                     const int pos = (tile0 + (u / GP >> 1)) * TN + (u % GP) * 32 + lane;
@@ -461,16 +461,16 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                     if ((mask[k] >> r) & 1)
                         buf[k][i] = __ldg(reinterpret_cast<const uint4*>(headBase + (size_t)src * rowStride + c * 16));
                 }
-                fetch_ids(u + kStep);
+                fetch_ids(u + kStep * kIds, idK, idV);
             };
 #pragma unroll
             for (int k = 0; k < kDepth; ++k)
                 if (me + kStep * k < groups)
-                    load(me + kStep * k, k);
-            for (int v = me; v < groups; v += kStep * kDepth) {
+                    load(me + kStep * k, k, idsK[k], idsV[k]);
+            for (int v = me; v < groups; v += kStep * kIds) {
 #pragma unroll
-                for (int k = 0; k < kDepth; ++k) {
-                    const int u = v + kStep * k;
+                for (int y = 0; y < kIds; ++y) {
+                    const int u = v + kStep * y, k = y % kDepth, ahead = (y + kDepth) % kIds;
                     if (u >= groups)
                         break;
                     const int t = u / GP;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                         write_meta(u, mask[k], ks[k], vs[k]);
                     publish(u);
                     if (u + kStep * kDepth < groups)
-                        load(u + kStep * kDepth, k);
+                        load(u + kStep * kDepth, k, idsK[ahead], idsV[ahead]);
                 }
             }
         }
@@ -515,6 +515,17 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     if (warp < 4 * MT) {
         // ----------------------------------------------------------- softmax
+        // first of all Q, zeros past the last row, while the first pages come
+        for (int i = threadIdx.x; i < MT * 128 * (D / 8); i += MT * 128) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            const int row = row0 + r;
+            const bool ok = row < a.rowsPrefix;
+            const size_t tok = ok ? divide(row, a.divG) : 0;
+            const int g = ok ? row - (int)tok * a.G : 0;
+            copy16(base + (r >> 7) * (128 * D * 2) + tile_pos(128, r & 127, c),
+                   a.q + (tok * a.Hq + h * a.G + g) * D + c * 8, ok);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(qFull) : "memory");
         const int tile = warp >> 2;
         const uint32_t laneBase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t oAddr = laneBase + C::kColO + tile * D;
@@ -634,6 +645,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             tmem_fence_before();
             mbar_arrive(pFull + 8 * slot);
         }
+        copy_wait_all();   // Q, should no product have waited for it
         // the last products of this row tile
         if (J > 0) {
             const int last = MT == 2 ? 2 * (J - 1) + tile : J - 1;
@@ -645,10 +657,14 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         tmem_fence_after();
         const int row = row0 + (int)threadIdx.x;       // threads 0..127: tile 0, 128..255: tile 1
         const bool live = row < a.rowsPrefix;
-        const size_t r = ((size_t)part * a.Hkv + h) * a.rowsPrefix + (live ? row : 0);
+        const size_t r = ((size_t)part * a.Hkv + h) * a.rowsPrefix + row;
         const bool none = J == 0 || l == 0.0f;
         const float inv = none ? 0.0f : 1.0f / l;
         const float bad = *failed ? __int_as_float(0x7fc00000) : 0.0f;
+        // 32 columns at a time through shared memory (this tile's Q: its products have
+        // finished), so that eight lanes write 128 bytes of one row
+        float* mine = reinterpret_cast<float*>(smem + tile * (128 * D * 2)) + (warp & 3) * (32 * 32);
+        const int warpRow = row - lane;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
             float o[32];
@@ -657,13 +673,20 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 tmem_wait_load();
                 pin32(o);
             }
-            if (live) {
 #pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                    *reinterpret_cast<float4*>(a.partO + r * D + k + x) =
-                        none ? make_float4(bad, bad, bad, bad)
-                             : make_float4(o[x] * inv + bad, o[x + 1] * inv + bad, o[x + 2] * inv + bad, o[x + 3] * inv + bad);
+            for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<float4*>(mine + lane * 32 + (((x >> 2) ^ (lane & 7)) << 2)) =
+                    none ? make_float4(bad, bad, bad, bad)
+                         : make_float4(o[x] * inv + bad, o[x + 1] * inv + bad, o[x + 2] * inv + bad, o[x + 3] * inv + bad);
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int n = x * 4 + (lane >> 3);
+                if (warpRow + n < a.rowsPrefix)
+                    *reinterpret_cast<float4*>(a.partO + (r - lane + n) * D + k + (lane & 7) * 4) =
+                        *reinterpret_cast<const float4*>(mine + n * 32 + (((lane & 7) ^ (n & 7)) << 2));
             }
+            __syncwarp();
         }
         if (live)
             a.partL[r] = none ? -INFINITY + bad : M + log2f(l) + bad;
