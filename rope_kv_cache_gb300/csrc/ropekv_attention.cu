@@ -47,11 +47,9 @@ int check_dims(const ropekv_attention_dims* d)
     return ROPEKV_OK;
 }
 
-// A kernel's dynamic shared memory limit is raised once per device. `regs`: the
-// registers per thread that its register split counts on (0: none); a kernel
-// compiled to another number must not run, its warps would wait for them.
+// A kernel's dynamic shared memory limit is raised once per device.
 template <auto Kern>
-bool raise_smem(int bytes, int regs = 0)
+bool raise_smem(int bytes)
 {
     static std::atomic<unsigned long long> raised{0};
     int dev = 0;
@@ -60,9 +58,6 @@ bool raise_smem(int bytes, int regs = 0)
     const unsigned long long bit = (dev >= 0 && dev < 64) ? 1ULL << dev : 0;
     if (bit && (raised.load(std::memory_order_relaxed) & bit))
         return true;
-    cudaFuncAttributes attr;
-    if (regs > 0 && (cudaFuncGetAttributes(&attr, Kern) != cudaSuccess || attr.numRegs != regs))
-        return false;
     if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return false;
     raised.fetch_or(bit, std::memory_order_relaxed);
@@ -87,6 +82,10 @@ int launch(Kern kern, long long grid, int threads, int smem, bool dependent, cud
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
 
+#ifndef START
+#define START 8.0
+#define PARTC 0.5
+#endif
 // How a call is cut into launches, from its sizes alone.
 struct Plan {
     int nt;             // row tiles of the stream kernel: 8, 16 or 32 rows
@@ -149,14 +148,13 @@ Plan make_plan(const ropekv_attention_dims* d)
     p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
     if (p.tensor) {
         const int tileRows = d->headDim != 256 && rows > 128 ? 256 : 128;
-        const int tokens = d->headDim == 256 ? 64 : 128;
         p.prefixTiles = (int)((rows + tileRows - 1) / tileRows);
         const long long units = (long long)p.prefixTiles * d->numKVHeads;
-        const long long kv = ((long long)d->prefixLen + tokens - 1) / tokens;
+        const long long kv = ((long long)d->prefixLen + 63) / 64;
         double best = 1e30;
         for (int k = 1; k <= ropekv_attn::kMaxParts && k <= kv; ++k) {
             const double waves = (double)((units * k + kSMs - 1) / kSMs);
-            const double cost = waves * ((double)((kv + k - 1) / k) + 3.0) + 0.25 * k;
+            const double cost = waves * ((double)((kv + k - 1) / k) + START) + PARTC * k;
             if (cost < best) {
                 best = cost;
                 p.parts = k;
@@ -189,7 +187,7 @@ int launch_prefix(const Args& a, const Plan& p, cudaStream_t st)
 {
     constexpr auto kern = ropekv_attn::prefix_kernel<D, FMT, MT>;
     using C = PrefixConfig<D, FMT, MT>;
-    if (!raise_smem<kern>(C::kSmem, C::kSplit ? C::kLaunchRegs : 0))
+    if (!raise_smem<kern>(C::kSmem))
         return ROPEKV_ERR_LAUNCH;
     return launch(kern, (long long)p.prefixTiles * a.Hkv * p.parts, C::kThreads, C::kSmem, false, st, a);
 }

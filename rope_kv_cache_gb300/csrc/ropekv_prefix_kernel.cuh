@@ -12,17 +12,17 @@
 //   warp 8            issues tcgen05.mma from one thread: S from shared memory
 //                     (both operands K-major), O with P from TMEM and V from
 //                     shared memory (N-major: V is stored as it lies in the cache)
-//   warps 9-          fetch pages: a ring of tiles K0, V0, K1, V1, ... in shared
-//                     memory, 128-byte swizzled rows of 64 dims. FP16 rows come by
-//                     cp.async (three warps); 8-bit rows are decoded to FP16 (exact)
-//                     on the way, which takes seven: 512 threads, whose registers
-//                     are split 168 for the softmax and 88 for the others
+//   warps 9-15        fetch pages: a ring of tiles K0, V0, K1, V1, ... of 64 tokens in
+//                     shared memory, 128-byte swizzled rows of 64 dims. FP16 rows
+//                     come by cp.async, 8-bit rows are decoded to FP16 (exact) on the way
 //
-// Items i = 0, 1, ... alternate between two TMEM slots for S. With two row tiles
-// item i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i: either way
-// the tensor cores work on one slot while the softmax works on the other. The
-// issue order S(0) S(1) [O(i) S(i + 2)]... makes each S overwrite its slot only
-// after the P in it was read.
+// Items i = 0, 1, ... take the SL TMEM slots for S in turn. With two row tiles item
+// i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i. The issue order
+// S(0) .. S(SL-1) [O(i) S(i + SL)]... makes each S overwrite its slot only after
+// the P in it was read, and keeps the next scores of a row tile ready while its
+// softmax works: with a single slot per row tile (128 tokens wide) the chain
+// product - softmax - product of one tile, 2500 cycles of latencies even without
+// any arithmetic, set the pace.
 //
 // M moves only when a row's scores exceed it by more than 8, in which case the
 // row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: with ks and vs
@@ -31,8 +31,9 @@
 // (A V row with scale 0 is fetched as zeros with vs = 1, one with a negative scale
 // as its negative.)
 //
-// Every wait on an mbarrier is bounded; a wait that runs out makes the CTA stop
-// waiting and write NaN.
+// Every wait on an mbarrier is bounded. One that runs out ends its role's loop and,
+// through a flag, those of the others, and the CTA writes NaN; no role goes on past
+// a wait that was not satisfied, so no barrier gets an arrival too many.
 #pragma once
 
 #include "ropekv_attention_kernels.cuh"
@@ -41,31 +42,30 @@ namespace ropekv_attn {
 
 template <int D, int FMT, int MT>
 struct PrefixConfig {
-    static constexpr int kTile = D == 256 ? 64 : 128;      // tokens of a K/V tile
+    static constexpr int kTile = 64;                       // tokens of a K/V tile
+    static constexpr int kSlots = D == 256 ? 2 : 4;        // of S in TMEM
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = 4;
-    static constexpr int kMeta = 4;                        // tiles whose scales are kept
+    // a ring as wide as the products look ahead: V of item i to K of item i + kSlots
+    static constexpr int kStages = 2 * kSlots;
+    static constexpr int kMeta = 8;                        // tiles whose scales are kept
     static constexpr int kQBytes = MT * 128 * D * 2;
     static constexpr int kGroups = kTile / 32;             // 32 rows of a tile: one warp's copy
-    // 8-bit rows are decoded by seven warps, FP16 rows only copied, by three
-    static constexpr int kFetchers = FMT == kF16 ? 3 : 7;
+    static constexpr int kFetchers = 7;
     static constexpr int kThreads = (9 + kFetchers) * 32;
-    // registers move from the fetching warps to the softmax (a row of 128 scores)
-    static constexpr bool kSplit = kThreads == 512 && kTile == 128;
-    static constexpr int kLaunchRegs = 128;
     // arrivals that complete a tile: per group of rows one of each lane's copies and one of
     // the warp (FP16), or the warp's alone
     static constexpr int kArrivals = kGroups * (FMT == kF16 ? 33 : 1);
     // TMEM columns: S slots, then O of each row tile
-    static constexpr int kColO = 2 * kTile;
+    static constexpr int kColO = kSlots * kTile;
     static constexpr int kCols = 512;
+    static constexpr int kBars = 3 * kStages + 3 * kSlots + 1;
     static constexpr int kOffRing = kQBytes;
     static constexpr int kOffKs = kOffRing + kStages * kTileBytes;
     static constexpr int kOffVs = kOffKs + kMeta * kTile * 4;
     static constexpr int kOffRv = kOffVs + kMeta * kTile * 4;
     static constexpr int kOffMask = kOffRv + kMeta * kTile * 4;
     static constexpr int kOffBar = kOffMask + kMeta * 16;
-    static constexpr int kUsed = kOffBar + (2 * kStages + 7) * 8 + 16;
+    static constexpr int kUsed = kOffBar + kBars * 8 + 16;
     // one CTA per SM (each takes all of TMEM)
     static constexpr int kSmem = (kUsed > 120 * 1024 ? kUsed : 120 * 1024) + 1024;
 };
@@ -90,18 +90,25 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, int parity)
     return done != 0;
 }
 
-// Bounded wait: gives up (for the whole CTA) after some seconds at most.
-__device__ __forceinline__ void mbar_wait(uint32_t bar, int parity, volatile int* failed)
+// Bounded wait, of a second at most; false, for the whole CTA, if it runs out.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int* failed)
 {
     if (mbar_try(bar, parity))
-        return;
+        return true;
     for (int i = 0; i < (1 << 20); ++i) {
         if (mbar_try(bar, parity))
-            return;
+            return true;
         if ((i & 255) == 255 && *failed)
-            return;
+            return false;
     }
     *failed = 1;
+    return false;
+}
+
+// The same by a whole warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, int parity, volatile int* failed)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, failed));
 }
 
 __device__ __forceinline__ void fence_async_smem()
@@ -231,7 +238,7 @@ template <int D, int FMT, int MT>
 __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_kernel(const __grid_constant__ Args a)
 {
     using C = PrefixConfig<D, FMT, MT>;
-    constexpr int TN = C::kTile, NS = C::kStages, GP = C::kGroups;
+    constexpr int TN = C::kTile, NS = C::kStages, GP = C::kGroups, SL = C::kSlots;
     constexpr int kEsize = FMT == kF16 ? 2 : 1;
     extern __shared__ uint8_t smemRaw[];
     const uint32_t rawAddr = smem_u32(smemRaw);
@@ -242,10 +249,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const uint32_t bars = base + C::kOffBar;
-    const uint32_t kvFull = bars, kvEmpty = bars + NS * 8, sFull = bars + 2 * NS * 8,
-                   pFull = sFull + 16, oDone = pFull + 16, qFull = oDone + 16;
-    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffBar + (2 * NS + 7) * 8);
-    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + (2 * NS + 7) * 8 + 8);
+    const uint32_t kvFull = bars, kvEmpty = bars + NS * 8, sFull = bars + 3 * NS * 8,
+                   pFull = sFull + SL * 8, oDone = pFull + SL * 8, qFull = oDone + SL * 8;
+    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffBar + C::kBars * 8);
+    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + C::kBars * 8 + 8);
 
     // blockIdx.x = (row tile * Hkv + head) * parts + part
     const int part = blockIdx.x % a.numParts;
@@ -261,8 +268,9 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         for (int i = 0; i < NS; ++i) {
             mbar_init(kvFull + 8 * i, C::kArrivals);
             mbar_init(kvEmpty + 8 * i, 1);
+            mbar_init(kvEmpty + 8 * (NS + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SL; ++i) {
             mbar_init(sFull + 8 * i, 1);
             mbar_init(pFull + 8 * i, 128);
             mbar_init(oDone + 8 * i, 1);
@@ -282,19 +290,15 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
     const uint32_t tmem = *tmemSlot;
     const int items = MT * J;
 
-    // 256 x 168 + 256 x 88 registers is what a launch of 512 x 128 has
-    if (warp >= 8) {
-        if (C::kSplit)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
         // ------------------------------------------------------- MMA issue
         if (lane == 0) {
             constexpr uint32_t descS = mma_desc(TN, false), descO = mma_desc(D, true);
-            auto issue_s = [&](int i) {
+            auto issue_s = [&](int i) -> bool {
                 const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
                 const int st = (2 * j) % NS;
-                if (tile == 0)
-                    mbar_wait(kvFull + 8 * st, ((2 * j) / NS) & 1, failed);
+                if (tile == 0 && !mbar_wait(kvFull + 8 * st, ((2 * j) / NS) & 1, failed))
+                    return false;
                 if (FMT == kF16 || i == 0)
                     fence_async_smem();  // the copies landed in the generic proxy
                 tmem_fence_after();
@@ -302,45 +306,41 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 const uint32_t ka = base + C::kOffRing + st * C::kTileBytes;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + (i & 1) * TN,
+                    mma_ss(tmem + (i % SL) * TN,
                            matrix_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
                            matrix_desc(ka + (k >> 2) * (TN * 128) + (k & 3) * 32, 16, 1024),
                            descS, k > 0);
-                mma_commit(sFull + 8 * (i & 1));
+                mma_commit(sFull + 8 * (i % SL));
                 if (tile == MT - 1 && 2 * j + NS < 2 * J)  // the stage will be filled again
-                    mma_commit(kvEmpty + 8 * st);
+                    mma_commit(kvEmpty + 8 * (2 * j % (2 * NS)));
+                return true;
             };
-            auto issue_o = [&](int i) {
+            auto issue_o = [&](int i) -> bool {
                 const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
                 const int st = (2 * j + 1) % NS;
-                mbar_wait(pFull + 8 * (i & 1), (i >> 1) & 1, failed);
-                if (tile == 0)
-                    mbar_wait(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed);
+                if (!mbar_wait(pFull + 8 * (i % SL), (i / SL) & 1, failed) ||
+                    (tile == 0 && !mbar_wait(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed)))
+                    return false;
                 if (FMT == kF16)
                     fence_async_smem();
                 tmem_fence_after();
                 const uint32_t va = base + C::kOffRing + st * C::kTileBytes;
 #pragma unroll
                 for (int k = 0; k < TN / 16; ++k)
-                    mma_ts(tmem + C::kColO + tile * D, tmem + (i & 1) * TN + k * 8,
+                    mma_ts(tmem + C::kColO + tile * D, tmem + (i % SL) * TN + k * 8,
                            matrix_desc(va + k * 2048, TN * 128, 1024), descO, j > 0 || k > 0);
-                mma_commit(oDone + 8 * (i & 1));
+                mma_commit(oDone + 8 * (i % SL));
                 if (tile == MT - 1 && 2 * j + 1 + NS < 2 * J)
-                    mma_commit(kvEmpty + 8 * st);
+                    mma_commit(kvEmpty + 8 * ((2 * j + 1) % (2 * NS)));
+                return true;
             };
-            if (items > 0) {
-                mbar_wait(qFull, 0, failed);
-                issue_s(0);
-            }
-            if (items > 1)
-                issue_s(1);
-            for (int i = 0; i < items; ++i) {
-                issue_o(i);
-                if (i + 2 < items)
-                    issue_s(i + 2);
-            }
+            bool ok = items > 0 && mbar_wait(qFull, 0, failed);
+            for (int i = 0; ok && i < SL && i < items; ++i)
+                ok = issue_s(i);
+            for (int i = 0; ok && i < items; ++i)
+                ok = issue_o(i) && (i + SL >= items || issue_s(i + SL));
         }
-    } else {
+    } else if (warp > 8) {
         // ------------------------------------------------------- page fetch
         const int me = warp - 9;
         const int groups = 2 * J * GP;
@@ -373,6 +373,16 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             const int inPage = pos - divide(pos, a.divTpp) * a.tpp;
             return ok ? (uint32_t)((t & 1) ? idV : idK) * (uint32_t)a.tpp + inPage : 0u;
         };
+        // Waits until tile t - NS, which had tile t's stage, is consumed. Barriers of two
+        // laps of the ring: a barrier's parity tells only its last two phases apart, and a
+        // warp does not visit every tile. With barrier (t - NS) % 2 NS the phase before the
+        // one waited for is tile t - 3 NS, which is consumed: the warp waited for one of
+        // the tiles from t - 4 - NS on, and products are taken less than NS tiles out of
+        // order. The phase after is tile t + NS, for which tile t would be needed.
+        auto stage_free = [&](int t) -> bool {
+            const int old = t - NS;
+            return old < 0 || mbar_wait_warp(kvEmpty + 8 * (old % (2 * NS)), (old / (2 * NS)) & 1, failed);
+        };
         // what the softmax needs of a K group's tokens: the mask and (8-bit) the K scale
         // times c, log2 and reciprocal of the V scale's magnitude
         auto write_meta = [&](int u, uint32_t mask, float ks, float vs) {
@@ -403,9 +413,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 const uint32_t row = locate(u, idsK[x], idsV[x], mask);
                 fetch_ids(u + kStep * kIds, idsK[x], idsV[x]);
                 const int t = u / GP;
-                if (t >= NS)
-                    mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
-                __syncwarp();
+                if (!stage_free(t)) {
+                    v = groups;
+                    break;
+                }
                 const uint32_t dst = base + C::kOffRing + (t % NS) * C::kTileBytes;
                 const int r0 = (u % GP) * 32;
                 if (mask == 0xffffffffu) {
@@ -474,9 +485,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                     if (u >= groups)
                         break;
                     const int t = u / GP;
-                    if (t >= NS)
-                        mbar_wait(kvEmpty + 8 * (t % NS), (t / NS - 1) & 1, failed);
-                    __syncwarp();
+                    if (!stage_free(t)) {
+                        v = groups;
+                        break;
+                    }
                     uint8_t* dst = smem + C::kOffRing + (t % NS) * C::kTileBytes;
                     const int r0 = (u % GP) * 32;
                     // zero rows: unmapped tokens and V rows with scale 0; V rows with a negative scale
@@ -509,11 +521,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 }
             }
         }
-    }
-    } else {
-        if (C::kSplit)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    if (warp < 4 * MT) {
+    } else if (warp < 4 * MT) {
         // ----------------------------------------------------------- softmax
         // first of all Q, zeros past the last row, while the first pages come
         for (int i = threadIdx.x; i < MT * 128 * (D / 8); i += MT * 128) {
@@ -534,10 +542,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         const float scale = fmaxf(fabsf(a.scaleLog2), 1e-30f);
         for (int j = 0; j < J; ++j) {
             const int i = MT == 2 ? 2 * j + tile : j;
-            const int slot = i & 1;
+            const int slot = i % SL;
             const uint32_t sAddr = laneBase + slot * TN;
-            mbar_wait(sFull + 8 * slot, (i >> 1) & 1, failed);
-            __syncwarp();
+            if (!mbar_wait_warp(sFull + 8 * slot, (i / SL) & 1, failed))
+                break;
             tmem_fence_after();
             float s[TN];
 #pragma unroll
@@ -593,11 +601,9 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 l *= f;
                 if (j > 0) {
                     // O of this row tile is at rest: its last product has finished
-                    if (MT == 1)
-                        mbar_wait(oDone + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, failed);
-                    else
-                        mbar_wait(oDone + 8 * slot, ((i >> 1) - 1) & 1, failed);
-                    __syncwarp();
+                    const int before = i - MT;
+                    if (!mbar_wait_warp(oDone + 8 * (before % SL), (before / SL) & 1, failed))
+                        break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < D; k += 32) {
@@ -649,11 +655,8 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         // the last products of this row tile
         if (J > 0) {
             const int last = MT == 2 ? 2 * (J - 1) + tile : J - 1;
-            if (MT == 1 && last > 0)
-                mbar_wait(oDone + 8 * ((last - 1) & 1), ((last - 1) >> 1) & 1, failed);
-            mbar_wait(oDone + 8 * (last & 1), (last >> 1) & 1, failed);
+            mbar_wait_warp(oDone + 8 * (last % SL), (last / SL) & 1, failed);
         }
-        __syncwarp();
         tmem_fence_after();
         const int row = row0 + (int)threadIdx.x;       // threads 0..127: tile 0, 128..255: tile 1
         const bool live = row < a.rowsPrefix;
@@ -691,7 +694,6 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         if (live)
             a.partL[r] = none ? -INFINITY + bad : M + log2f(l) + bad;
         tmem_fence_before();
-    }
     }
     __syncthreads();
     if (warp == 8) {
