@@ -214,11 +214,28 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1)
         : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
 }
 
-// Shared-memory matrix descriptor: 128-byte swizzle, offsets in bytes.
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t leading, uint32_t stride)
+// Shared-memory matrix descriptor, 128-byte swizzle: the upper word holds the
+// stride of 1024 bytes between groups of eight rows, the version and the swizzle;
+// the lower word the address and the leading offset, both in units of 16 bytes.
+// Operands further on in the same tile differ by an addition to the lower word.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading)
 {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(leading >> 4) << 16) |
-           ((uint64_t)(stride >> 4) << 32) | (1ULL << 46) | (2ULL << 61);
+    return (addr >> 4) | ((leading >> 4) << 16);
+}
+
+__device__ __forceinline__ uint64_t desc(uint32_t low)
+{
+    return ((uint64_t)kDescHigh << 32) | low;
+}
+
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Instruction descriptor: FP16 x FP16 -> FP32, M = 128.
@@ -292,54 +309,61 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
 
     if (warp == 8) {
         // ------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t descS = mma_desc(TN, false), descO = mma_desc(D, true);
-            auto issue_s = [&](int i) -> bool {
-                const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
-                const int st = (2 * j) % NS;
-                if (tile == 0 && !mbar_wait(kvFull + 8 * st, ((2 * j) / NS) & 1, failed))
-                    return false;
-                if (FMT == kF16 || i == 0)
+        // The whole warp walks the loop, so that addresses and descriptors stay in uniform
+        // registers; one elected lane issues (from a lone lane's registers every product
+        // cost 55 cycles to issue, about what it takes to run).
+        constexpr uint32_t descS = mma_desc(TN, false), descO = mma_desc(D, true);
+        auto issue_s = [&](int i) -> bool {
+            const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
+            const int st = (2 * j) % NS;
+            if (tile == 0 && !mbar_wait_warp(kvFull + 8 * st, ((2 * j) / NS) & 1, failed))
+                return false;
+            if (elect_one()) {
+                if ((FMT == kF16 && tile == 0) || i == 0)
                     fence_async_smem();  // the copies landed in the generic proxy
                 tmem_fence_after();
-                const uint32_t qa = base + tile * (128 * D * 2);
-                const uint32_t ka = base + C::kOffRing + st * C::kTileBytes;
+                const uint32_t qd = desc_low(base + tile * (128 * D * 2), 16);
+                const uint32_t kd = desc_low(base + C::kOffRing + st * C::kTileBytes, 16);
+                const uint32_t to = tmem + (i % SL) * TN;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + (i % SL) * TN,
-                           matrix_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                           matrix_desc(ka + (k >> 2) * (TN * 128) + (k & 3) * 32, 16, 1024),
-                           descS, k > 0);
+                    mma_ss(to, desc(qd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16),
+                           desc(kd + ((k >> 2) * (TN * 128) + (k & 3) * 32) / 16), descS, k > 0);
                 mma_commit(sFull + 8 * (i % SL));
                 if (tile == MT - 1 && 2 * j + NS < 2 * J)  // the stage will be filled again
                     mma_commit(kvEmpty + 8 * (2 * j % (2 * NS)));
-                return true;
-            };
-            auto issue_o = [&](int i) -> bool {
-                const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
-                const int st = (2 * j + 1) % NS;
-                if (!mbar_wait(pFull + 8 * (i % SL), (i / SL) & 1, failed) ||
-                    (tile == 0 && !mbar_wait(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed)))
-                    return false;
-                if (FMT == kF16)
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_o = [&](int i) -> bool {
+            const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
+            const int st = (2 * j + 1) % NS;
+            if (tile == 0 && !mbar_wait_warp(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed))
+                return false;
+            if (!mbar_wait_warp(pFull + 8 * (i % SL), (i / SL) & 1, failed))
+                return false;
+            if (elect_one()) {
+                if (FMT == kF16 && tile == 0)
                     fence_async_smem();
                 tmem_fence_after();
-                const uint32_t va = base + C::kOffRing + st * C::kTileBytes;
+                const uint32_t vd = desc_low(base + C::kOffRing + st * C::kTileBytes, TN * 128);
+                const uint32_t to = tmem + C::kColO + tile * D, from = tmem + (i % SL) * TN;
 #pragma unroll
                 for (int k = 0; k < TN / 16; ++k)
-                    mma_ts(tmem + C::kColO + tile * D, tmem + (i % SL) * TN + k * 8,
-                           matrix_desc(va + k * 2048, TN * 128, 1024), descO, j > 0 || k > 0);
+                    mma_ts(to, from + k * 8, desc(vd + k * (2048 / 16)), descO, j > 0 || k > 0);
                 mma_commit(oDone + 8 * (i % SL));
                 if (tile == MT - 1 && 2 * j + 1 + NS < 2 * J)
                     mma_commit(kvEmpty + 8 * ((2 * j + 1) % (2 * NS)));
-                return true;
-            };
-            bool ok = items > 0 && mbar_wait(qFull, 0, failed);
-            for (int i = 0; ok && i < SL && i < items; ++i)
-                ok = issue_s(i);
-            for (int i = 0; ok && i < items; ++i)
-                ok = issue_o(i) && (i + SL >= items || issue_s(i + SL));
-        }
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = items > 0 && mbar_wait_warp(qFull, 0, failed);
+        for (int i = 0; ok && i < SL && i < items; ++i)
+            ok = issue_s(i);
+        for (int i = 0; ok && i < items; ++i)
+            ok = issue_o(i) && (i + SL >= items || issue_s(i + SL));
     } else if (warp > 8) {
         // ------------------------------------------------------- page fetch
         const int me = warp - 9;
@@ -585,12 +609,13 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             // FP16: s is unscaled until the exponential takes c s - M
             float top4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int k = 4; k < TN; k += 4) {
-                top4[0] = fmaxf(top4[0], s[k]);
-                top4[1] = fmaxf(top4[1], s[k + 1]);
-                top4[2] = fmaxf(top4[2], s[k + 2]);
-                top4[3] = fmaxf(top4[3], s[k + 3]);
-            }
+            for (int k = 4; k + 8 <= TN; k += 8)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    top4[x] = fmaxf(fmaxf(top4[x], s[k + 2 * x]), s[k + 2 * x + 1]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                top4[x] = fmaxf(top4[x], s[TN - 4 + x]);
             float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             if (FMT == kF16)
                 top = top == -INFINITY ? top : top * scale;
