@@ -9,20 +9,20 @@
 //   warps 0-3 (and 4-7 with MT = 2)  softmax: a thread owns one row, which is
 //                     one TMEM lane; S comes by tcgen05.ld, P goes back by
 //                     tcgen05.st over the columns of S that it was made from
-//   warp 8            issues tcgen05.mma from one thread: S from shared memory
-//                     (both operands K-major), O with P from TMEM and V from
-//                     shared memory (N-major: V is stored as it lies in the cache)
-//   warps 9-15        fetch pages: a ring of tiles K0, V0, K1, V1, ... of 64 tokens in
+//   warp 8            issues the products S (both operands K-major in shared memory)
+//   warp 9            issues the products O (P in TMEM, V from shared memory, N-major:
+//                     V is stored as it lies in the cache)
+//   warps 10-15       fetch pages: a ring of tiles K0, V0, K1, V1, ... of 64 tokens in
 //                     shared memory, 128-byte swizzled rows of 64 dims. FP16 rows
 //                     come by cp.async, 8-bit rows are decoded to FP16 (exact) on the way
 //
 // Items i = 0, 1, ... take the SL TMEM slots for S in turn. With two row tiles item
-// i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i. The issue order
-// S(0) .. S(SL-1) [O(i) S(i + SL)]... makes each S overwrite its slot only after
-// the P in it was read, and keeps the next scores of a row tile ready while its
-// softmax works: with a single slot per row tile (128 tokens wide) the chain
-// product - softmax - product of one tile, 2500 cycles of latencies even without
-// any arithmetic, set the pace.
+// i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i. S(i + SL) overwrites
+// its slot after O(i) has read the P in it; the slots keep the next scores of a row
+// tile ready while its softmax works. With a single slot per row tile (128 tokens
+// wide) the chain product - softmax - product of one tile, 2500 cycles of latencies
+// even without any arithmetic, set the pace; with one warp issuing both products its
+// waits, fences and commits did (about 100 cycles each, 1150 per item).
 //
 // M moves only when a row's scores exceed it by more than 8, in which case the
 // row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: with ks and vs
@@ -50,8 +50,8 @@ struct PrefixConfig {
     static constexpr int kMeta = 8;                        // tiles whose scales are kept
     static constexpr int kQBytes = MT * 128 * D * 2;
     static constexpr int kGroups = kTile / 32;             // 32 rows of a tile: one warp's copy
-    static constexpr int kFetchers = 7;
-    static constexpr int kThreads = (9 + kFetchers) * 32;
+    static constexpr int kFetchers = 6;
+    static constexpr int kThreads = (10 + kFetchers) * 32;
     // arrivals that complete a tile: per group of rows one of each lane's copies and one of
     // the warp (FP16), or the warp's alone
     static constexpr int kArrivals = kGroups * (FMT == kF16 ? 33 : 1);
@@ -308,17 +308,21 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
     const int items = MT * J;
 
     if (warp == 8) {
-        // ------------------------------------------------------- MMA issue
+        // ------------------------------------------------ products S = Q K^T
         // The whole warp walks the loop, so that addresses and descriptors stay in uniform
         // registers; one elected lane issues (from a lone lane's registers every product
         // cost 55 cycles to issue, about what it takes to run).
-        constexpr uint32_t descS = mma_desc(TN, false), descO = mma_desc(D, true);
-        auto issue_s = [&](int i) -> bool {
+        constexpr uint32_t kind = mma_desc(TN, false);
+        bool ok = items > 0 && mbar_wait_warp(qFull, 0, failed);
+        for (int i = 0; ok && i < items; ++i) {
             const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
-            const int st = (2 * j) % NS;
-            if (tile == 0 && !mbar_wait_warp(kvFull + 8 * st, ((2 * j) / NS) & 1, failed))
-                return false;
-            if (elect_one()) {
+            const int t = 2 * j, st = t % NS;
+            if (tile == 0)
+                ok = mbar_wait_warp(kvFull + 8 * st, (t / NS) & 1, failed);
+            // the slot's P was read by O(i - SL)
+            if (ok && i >= SL)
+                ok = mbar_wait_warp(oDone + 8 * (i % SL), (i / SL - 1) & 1, failed);
+            if (ok && elect_one()) {
                 if ((FMT == kF16 && tile == 0) || i == 0)
                     fence_async_smem();  // the copies landed in the generic proxy
                 tmem_fence_after();
@@ -328,22 +332,24 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     mma_ss(to, desc(qd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16),
-                           desc(kd + ((k >> 2) * (TN * 128) + (k & 3) * 32) / 16), descS, k > 0);
+                           desc(kd + ((k >> 2) * (TN * 128) + (k & 3) * 32) / 16), kind, k > 0);
                 mma_commit(sFull + 8 * (i % SL));
-                if (tile == MT - 1 && 2 * j + NS < 2 * J)  // the stage will be filled again
-                    mma_commit(kvEmpty + 8 * (2 * j % (2 * NS)));
+                if (tile == MT - 1 && t + NS < 2 * J)  // the stage will be filled again
+                    mma_commit(kvEmpty + 8 * (t % (2 * NS)));
             }
             __syncwarp();
-            return true;
-        };
-        auto issue_o = [&](int i) -> bool {
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------- products O += P V
+        constexpr uint32_t kind = mma_desc(D, true);
+        bool ok = true;
+        for (int i = 0; ok && i < items; ++i) {
             const int j = MT == 2 ? i >> 1 : i, tile = MT == 2 ? i & 1 : 0;
-            const int st = (2 * j + 1) % NS;
-            if (tile == 0 && !mbar_wait_warp(kvFull + 8 * st, ((2 * j + 1) / NS) & 1, failed))
-                return false;
-            if (!mbar_wait_warp(pFull + 8 * (i % SL), (i / SL) & 1, failed))
-                return false;
-            if (elect_one()) {
+            const int t = 2 * j + 1, st = t % NS;
+            if (tile == 0)
+                ok = mbar_wait_warp(kvFull + 8 * st, (t / NS) & 1, failed);
+            ok = ok && mbar_wait_warp(pFull + 8 * (i % SL), (i / SL) & 1, failed);
+            if (ok && elect_one()) {
                 if (FMT == kF16 && tile == 0)
                     fence_async_smem();
                 tmem_fence_after();
@@ -351,22 +357,16 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 const uint32_t to = tmem + C::kColO + tile * D, from = tmem + (i % SL) * TN;
 #pragma unroll
                 for (int k = 0; k < TN / 16; ++k)
-                    mma_ts(to, from + k * 8, desc(vd + k * (2048 / 16)), descO, j > 0 || k > 0);
+                    mma_ts(to, from + k * 8, desc(vd + k * (2048 / 16)), kind, j > 0 || k > 0);
                 mma_commit(oDone + 8 * (i % SL));
-                if (tile == MT - 1 && 2 * j + 1 + NS < 2 * J)
-                    mma_commit(kvEmpty + 8 * ((2 * j + 1) % (2 * NS)));
+                if (tile == MT - 1 && t + NS < 2 * J)
+                    mma_commit(kvEmpty + 8 * (t % (2 * NS)));
             }
             __syncwarp();
-            return true;
-        };
-        bool ok = items > 0 && mbar_wait_warp(qFull, 0, failed);
-        for (int i = 0; ok && i < SL && i < items; ++i)
-            ok = issue_s(i);
-        for (int i = 0; ok && i < items; ++i)
-            ok = issue_o(i) && (i + SL >= items || issue_s(i + SL));
-    } else if (warp > 8) {
+        }
+    } else if (warp > 9) {
         // ------------------------------------------------------- page fetch
-        const int me = warp - 9;
+        const int me = warp - 10;
         const int groups = 2 * J * GP;
         const size_t rowStride = (size_t)a.Hkv * D * kEsize;
         const uint8_t* headBase = a.pool + (size_t)h * D * kEsize;
@@ -400,9 +400,8 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         // Waits until tile t - NS, which had tile t's stage, is consumed. Barriers of two
         // laps of the ring: a barrier's parity tells only its last two phases apart, and a
         // warp does not visit every tile. With barrier (t - NS) % 2 NS the phase before the
-        // one waited for is tile t - 3 NS, which is consumed: the warp waited for one of
-        // the tiles from t - 4 - NS on, and products are taken less than NS tiles out of
-        // order. The phase after is tile t + NS, for which tile t would be needed.
+        // one waited for is tile t - 3 NS, which is consumed: the warp waited for tile
+        // t - 3 - NS, and products are taken less than NS tiles out of order. The phase after is tile t + NS, for which tile t would be needed.
         auto stage_free = [&](int t) -> bool {
             const int old = t - NS;
             return old < 0 || mbar_wait_warp(kvEmpty + 8 * (old % (2 * NS)), (old / (2 * NS)) & 1, failed);
