@@ -82,10 +82,6 @@ int launch(Kern kern, long long grid, int threads, int smem, bool dependent, cud
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ROPEKV_OK : ROPEKV_ERR_LAUNCH;
 }
 
-#ifndef START
-#define START 8.0
-#define PARTC 0.5
-#endif
 // How a call is cut into launches, from its sizes alone.
 struct Plan {
     int nt;             // row tiles of the stream kernel: 8, 16 or 32 rows
@@ -154,7 +150,7 @@ Plan make_plan(const ropekv_attention_dims* d)
         double best = 1e30;
         for (int k = 1; k <= ropekv_attn::kMaxParts && k <= kv; ++k) {
             const double waves = (double)((units * k + kSMs - 1) / kSMs);
-            const double cost = waves * ((double)((kv + k - 1) / k) + START) + PARTC * k;
+            const double cost = waves * ((double)((kv + k - 1) / k) + 8.0) + 0.5 * k;
             if (cost < best) {
                 best = cost;
                 p.parts = k;
