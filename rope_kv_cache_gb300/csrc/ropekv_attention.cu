@@ -3,6 +3,7 @@
 // (include/ropekv_serving.h). Nothing allocates or synchronises.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <math.h>
 #include <stdint.h>
@@ -117,9 +118,20 @@ int team_size(int Hkv, int perSm)
 // Tiles of 8 rows, or of 16 or 32 (D = 256: 16 at most) where a sequence has
 // more, so that its tokens are fetched once. The prefix joins the stream if all
 // rows of a KV head fit into one such tile.
-// Ranges of a tensor-core prefix: their number p minimises the K/V tiles that the
-// busiest SM walks, waves(units * p) * ceil(tiles / p), where each CTA costs about
-// three tiles more to start and to write its partial.
+//
+// A tensor-core prefix of p ranges takes p CTAs per row tile, one to an SM, and the
+// stream's CTAs start where there is room. Either the two kernels follow one another,
+// each on all SMs, or the stream gets the SMs that the prefix leaves free and runs
+// beside it: the prefix's products and the stream's loads then overlap. The estimate
+// below, in microseconds, chooses p and the form. The lengths lie on the device: it
+// takes the form that is best over calls three quarters of which fill half of their
+// tables and one quarter a twentieth, as a prefix on few SMs is long and short
+// sequences do not hide it (64 of 1 to 64 tokens in tables of 8192 behind 4096: 76 us
+// if only the former count, 36 us). Measured, one after the other against side by
+// side: 256 sequences of 1 to 512 tokens behind 8192, FP16: 89 against 79 us; 128 of
+// 1 to 2048 behind 4097, E4M3: 78 against 68; 61 x 7 rows behind 2000, INT8: 86
+// against 60; 40 of 1 to 900 behind 3001, D = 256: 32 against 22. Against it: 128 of
+// 1 to 2048 behind 16000, E4M3: 105 against 114.
 Plan make_plan(const ropekv_attention_dims* d)
 {
     Plan p = {};
@@ -139,25 +151,41 @@ Plan make_plan(const ropekv_attention_dims* d)
     const long long items = (long long)d->batch * p.tilesSeq * p.groups;
     const long long steps = items * (own > 0 ? own / 16 + 2 : 0) +
                             (p.tilesPrefix ? (long long)p.groups * (d->prefixLen / 16 + 1) : 0);
-    const long long most = (long long)kSMs * (perSm / p.teamSize), want = (steps + 1) / 2;
-    p.teams = (int)(want < 1 ? 1 : want < most ? want : most);
-    p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
+    const int teamsPerSm = perSm / p.teamSize;
+    long long most = (long long)kSMs * teamsPerSm;
     if (p.tensor) {
+        const bool f16 = d->cacheFormat == ROPEKV_CACHE_F16;
         const int tileRows = d->headDim != 256 && rows > 128 ? 256 : 128;
         p.prefixTiles = (int)((rows + tileRows - 1) / tileRows);
         const long long units = (long long)p.prefixTiles * d->numKVHeads;
         const long long kv = ((long long)d->prefixLen + 63) / 64;
-        double best = 1e30;
+        // one prefix tile, one warp's step on an SM, one range's partial written and read
+        const double tile = f16 && d->headDim != 256 ? 0.95 : 1.3;
+        const double step = (p.nt > 1 ? 0.12 * p.nt : f16 ? 0.16 : 0.1) * d->headDim / 128;
+        const double work = (double)steps * p.teamSize * step;
+        const double part = 0.1 + (double)units * tileRows * d->headDim * 8 / 5e6;
+        double best = HUGE_VAL;
         for (int k = 1; k <= ropekv_attn::kMaxParts && k <= kv; ++k) {
-            const double waves = (double)((units * k + kSMs - 1) / kSMs);
-            const double cost = waves * ((double)((kv + k - 1) / k) + 8.0) + 0.5 * k;
-            if (cost < best) {
-                best = cost;
-                p.parts = k;
+            const long long ctas = units * k, waves = (ctas + kSMs - 1) / kSMs;
+            const double prefix = (double)waves * (8.0 + tile * (double)((kv + k - 1) / k));
+            for (int beside = 0; beside <= (ctas < kSMs); ++beside) {
+                const double sms = (double)(beside ? kSMs - ctas : kSMs);
+                double half = 8.0 + 0.5 * work / sms, few = 8.0 + 0.05 * work / sms;
+                half = part * k + (beside ? std::max(prefix, half) : prefix + half);
+                few = part * k + (beside ? std::max(prefix, few) : prefix + few);
+                const double cost = half * half * half * few;
+                if (cost < best) {
+                    best = cost;
+                    p.parts = k;
+                    most = (beside ? kSMs - ctas : kSMs) * teamsPerSm;
+                }
             }
         }
-        p.partRows = (int64_t)p.parts * d->numKVHeads * rows;
     }
+    const long long want = (steps + 1) / 2;
+    p.teams = (int)(want < 1 ? 1 : want < most ? want : most);
+    p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
+    p.partRows = (int64_t)p.parts * d->numKVHeads * rows;
     return p;
 }
 
