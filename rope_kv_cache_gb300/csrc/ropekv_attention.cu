@@ -146,7 +146,7 @@ Plan make_plan(const ropekv_attention_dims* d)
     const int perSm = stream_warps(d->headDim, d->cacheFormat, p.nt);
     p.teamSize = team_size(d->numKVHeads, perSm);
     p.groups = d->numKVHeads / p.teamSize;
-    // the table's capacity bounds the steps; at least two of them make a share
+    // the table's capacity bounds the steps
     const long long own = (long long)d->maxPagesPerSeq * d->tokensPerPage - d->prefixLen;
     const long long items = (long long)d->batch * p.tilesSeq * p.groups;
     const long long steps = items * (own > 0 ? own / 16 + 2 : 0) +
@@ -182,8 +182,7 @@ Plan make_plan(const ropekv_attention_dims* d)
             }
         }
     }
-    const long long want = (steps + 1) / 2;
-    p.teams = (int)(want < 1 ? 1 : want < most ? want : most);
+    p.teams = (int)(steps < 1 ? 1 : steps < most ? steps : most);
     p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
     p.partRows = (int64_t)p.parts * d->numKVHeads * rows;
     return p;
@@ -202,7 +201,7 @@ Layout make_layout(const Plan& p, int D)
     w.segO = w.partL + up(p.partRows * 4);
     w.segL = w.segO + up(p.slots * p.pitch * D * 4);
     w.offsets = w.segL + up(p.slots * p.pitch * 4);
-    w.size = w.offsets + up((p.units + 4) * 8);
+    w.size = w.offsets + up((p.units + 1) * 8);
     return w;
 }
 

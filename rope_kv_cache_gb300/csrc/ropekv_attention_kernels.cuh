@@ -59,7 +59,7 @@ struct Args {
     float* partL;                // [numParts, Hkv, B*S*G]
     float* segO;                 // [slots, pitch, D]          segments of the streamed tokens
     float* segL;                 // [slots, pitch]
-    long long* offsets;          // [units + 4]: first step of each unit, their sum, steps of a share, its divisor
+    long long* offsets;          // [units + 1]: first step of each unit, their sum
     float scaleLog2;             // smScale * log2(e)
     int32_t B, S, Hq, Hkv, G, numPages, tpp, mpps, P, prefixPages;
     int32_t rowsPrefix;          // B * S * G
@@ -290,6 +290,14 @@ __device__ __forceinline__ int unit_steps(int lo, int hi)
     return hi > lo ? ((hi + 15) >> 4) - (lo >> 4) : 0;
 }
 
+// Steps of a team's share.
+__device__ __forceinline__ long long share_of(long long total, int teams)
+{
+    if (total < (1LL << 31))
+        return max(1u, ((uint32_t)total + (uint32_t)teams - 1) / (uint32_t)teams);
+    return (total + teams - 1) / teams;
+}
+
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(StreamConfig<D, FMT, NT>::kPerSm * 32, 1)
 stream_kernel(const __grid_constant__ Args a)
@@ -330,23 +338,15 @@ stream_kernel(const __grid_constant__ Args a)
         total += warpSum[x];
     }
     scan[threadIdx.x] = before + sum - mine;
-    const long long share = max(2LL, (total + a.teams - 1) / a.teams);
+    const long long share = share_of(total, a.teams);
     if (blockIdx.x == 0) {
         long long at = before + sum - mine;
         for (int u = u0; u < u1; ++u) {
             a.offsets[u] = at;
             at += weight(u);
         }
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0)
             a.offsets[units] = total;
-            a.offsets[units + 1] = share;
-            if (total < (1LL << 31)) {
-                // multiplier and shift of the division by the share (see Divisor)
-                const int c = share > 1 ? 64 - __clzll(share - 1) : 0;
-                a.offsets[units + 2] = (long long)(((1ULL << (31 + c)) + share - 1) / (unsigned long long)share);
-                a.offsets[units + 3] = 31 + c;
-            }
-        }
     }
     __syncthreads();
 
@@ -775,12 +775,16 @@ stream_kernel(const __grid_constant__ Args a)
 // segments of the prefix unit) and the row's own segments, in that order. A group
 // of D / 8 threads holds a row; SPLIT: the CTA's groups share one row's partials
 // (few rows with many segments each).
+//
+// Bound by latency: a launch, the steps' sums, the partials. What depends on the
+// lengths alone is computed before the wait for the grids before this one, and the
+// partials of all kinds form one list, so that the loads of four are in flight together
+// (registers for that: with 64 a thread instead of 85 a call took 0.8 us longer).
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int tileShift)
+__global__ void __launch_bounds__(256, 3) join_kernel(const __grid_constant__ Args a, int tileShift)
 {
     constexpr int TG = D / 8, kGroups = 256 / TG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int group = threadIdx.x / TG, d = threadIdx.x % TG * 8;
     const int hv = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * kGroups + group;   // (token, q head)
     const int rows = a.B * a.S * a.Hq;
@@ -790,77 +794,76 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const int h = divide(hq, a.divG), g = hq - h * a.G;
     const int b = divide(tok, a.divS), s = tok - b * a.S;
     const bool active = __ldg(a.kvLens + b) - (long long)a.S + s >= a.P;
-    const int units = a.B + a.prefixUnit;
-    const long long offset = a.offsets[b + a.prefixUnit], share = a.offsets[units + 1];
-    const bool small = a.offsets[units] < (1LL << 31);
-    const Divisor divShare = {(uint32_t)a.offsets[units + 2], (uint32_t)a.offsets[units + 3], 0};
+    const int units = a.B + a.prefixUnit, unit = b + a.prefixUnit;
+    int lo, hi;
+    unit_range(a, unit, lo, hi);
+    const int steps = unit_steps(lo, hi);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long offset = a.offsets[unit], total = a.offsets[units];
+    const long long share = share_of(total, a.teams);
 
     float m = -INFINITY, l = 0.0f;
     float o[8] = {};
-    // four partials at a time: their loads are in flight together
-    auto join4 = [&](const float* L, size_t strideL, const float* O, size_t strideO, int n) {
-        float x[4];
-        float4 v[4][2];
-        float top = m;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = -INFINITY;
-            v[j][0] = v[j][1] = make_float4(0, 0, 0, 0);
-            if (j < n) {
-                x[j] = *L;
-                v[j][0] = *reinterpret_cast<const float4*>(O);
-                v[j][1] = *reinterpret_cast<const float4*>(O + 4);
-            }
-            L += strideL;
-            O += strideO;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            top = fmaxf(top, x[j]);
-        const float mm = top == -INFINITY ? 0.0f : top;
-        const float f = exp2_fast(m - mm);
-        m = top;
-        l *= f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            o[k] *= f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float w = exp2_fast(x[j] - mm);
-            const float* y = reinterpret_cast<const float*>(v[j]);
-            l += w;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                o[k] += w * y[k];
-        }
-    };
+    int count = 0;      // partials of this row
     if (active) {
-        const int first = SPLIT ? 4 * group : 0, stride = SPLIT ? 4 * kGroups : 4;
+        const bool small = total < (1LL << 31);
         const size_t headRow = (size_t)h * a.rowsPrefix + (size_t)tok * a.G + g;
         const size_t partStride = (size_t)a.Hkv * a.rowsPrefix;
-        for (int k = first; k < a.numParts; k += stride)
-            join4(a.partL + k * partStride + headRow, partStride, a.partO + (k * partStride + headRow) * D + d,
-                  partStride * D, a.numParts - k);
         const int grp = divide(h, a.divTeam), member = h - grp * a.teamSize;
-        auto join_segments = [&](int n, long long at, int row, long long itemBase) {
-            if (n == 0)
-                return;
+        const size_t slotStride = (size_t)a.teamSize * a.pitch;
+        // segments of an item: the shares that its n steps, from step `at`, fall into
+        auto segments = [&](int n, long long at, int row, long long itemBase, size_t& slot) -> int {
             const int t = row >> tileShift, sub = t * a.groups + grp;
             at += (long long)sub * n;
-            const long long w0 = small ? divide((int)at, divShare) : at / share;
-            const long long w1 = small ? divide((int)at + n - 1, divShare) : (at + n - 1) / share;
-            const size_t slot = (size_t)((itemBase + sub + w0) * a.teamSize + member) * a.pitch + (row - (t << tileShift));
-            const size_t stepL = (size_t)a.teamSize * a.pitch;
-            const int segments = (int)(w1 - w0) + 1;
-            for (int k = first; k < segments; k += stride)
-                join4(a.segL + slot + k * stepL, stepL, a.segO + (slot + k * stepL) * D + d, stepL * D, segments - k);
+            const long long w0 = small ? (uint32_t)at / (uint32_t)share : at / share;
+            const long long w1 = small ? ((uint32_t)at + n - 1) / (uint32_t)share : (at + n - 1) / share;
+            slot = (size_t)((itemBase + sub + w0) * a.teamSize + member) * a.pitch + (row - (t << tileShift));
+            return n == 0 ? 0 : (int)(w1 - w0) + 1;
         };
-        if (a.prefixUnit)
-            join_segments(unit_steps(0, a.P), 0, tok * a.G + g, 0);
-        int lo, hi;
-        unit_range(a, b + a.prefixUnit, lo, hi);
-        join_segments(unit_steps(lo, hi), offset, s * a.G + g,
-                      (a.tilesPrefix + (long long)b * a.tilesSeq) * a.groups);
+        size_t slotPrefix = 0, slotOwn = 0;
+        const int nPrefix = a.prefixUnit ? segments(unit_steps(0, a.P), 0, tok * a.G + g, 0, slotPrefix) : 0;
+        const int nOwn = segments(steps, offset, s * a.G + g, (a.tilesPrefix + (long long)b * a.tilesSeq) * a.groups, slotOwn);
+        const int n0 = a.numParts + nPrefix;
+        count = n0 + nOwn;
+        for (int k = SPLIT ? 4 * group : 0; k < count; k += SPLIT ? 4 * kGroups : 4) {
+            float x[4];
+            float4 v[4][2];
+            float top = m;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = k + j;
+                const bool part = i < a.numParts;
+                const size_t at = part ? i * partStride + headRow
+                                : i < n0 ? slotPrefix + (i - a.numParts) * slotStride : slotOwn + (i - n0) * slotStride;
+                x[j] = -INFINITY;
+                v[j][0] = v[j][1] = make_float4(0, 0, 0, 0);
+                if (i < count) {
+                    const float* O = (part ? a.partO : a.segO) + at * D + d;
+                    x[j] = (part ? a.partL : a.segL)[at];
+                    v[j][0] = *reinterpret_cast<const float4*>(O);
+                    v[j][1] = *reinterpret_cast<const float4*>(O + 4);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = fmaxf(top, x[j]);
+            const float mm = top == -INFINITY ? 0.0f : top;
+            const float f = exp2_fast(m - mm);
+            m = top;
+            l *= f;
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                o[y] *= f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w = exp2_fast(x[j] - mm);
+                const float* y = reinterpret_cast<const float*>(v[j]);
+                l += w;
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    o[z] += w * y[z];
+            }
+        }
     }
     if (SPLIT) {
         __shared__ float sm[kGroups], sl[kGroups];
@@ -875,14 +878,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         __syncthreads();
         if (group > 0)
             return;
-        for (int k = 1; k < kGroups; ++k)
+        const int filled = min(kGroups, (count + 3) / 4);
+        for (int k = 1; k < filled; ++k)
             m = fmaxf(m, sm[k]);
         const float mm = m == -INFINITY ? 0.0f : m;
         l = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             o[k] = 0.0f;
-        for (int x = 0; x < kGroups; ++x) {
+        for (int x = 0; x < filled; ++x) {
             const float w = exp2_fast(sm[x] - mm);
             l += w * sl[x];
 #pragma unroll
