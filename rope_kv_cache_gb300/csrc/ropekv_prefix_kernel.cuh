@@ -65,7 +65,9 @@ struct PrefixConfig {
     static constexpr int kOffRv = kOffVs + kMeta * kTile * 4;
     static constexpr int kOffMask = kOffRv + kMeta * kTile * 4;
     static constexpr int kOffBar = kOffMask + kMeta * 16;
-    static constexpr int kUsed = kOffBar + kBars * 8 + 16;
+    // 8-bit, D = 128: one more group per fetch warp on its way, raw
+    static constexpr int kOffStage = (kOffBar + kBars * 8 + 16 + 15) / 16 * 16;
+    static constexpr int kUsed = kOffStage + (FMT != kF16 && D == 128 ? kFetchers * 32 * D : 0);
     // one CTA per SM (each takes all of TMEM)
     static constexpr int kSmem = (kUsed > 120 * 1024 ? kUsed : 120 * 1024) + 1024;
 };
@@ -372,7 +374,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         const uint8_t* headBase = a.pool + (size_t)h * D * kEsize;
         constexpr int kVecs = D * kEsize / 16;         // 16-byte vectors of a row
         constexpr int kPerLane = kVecs;                // 32 rows of kVecs vectors over 32 lanes
-        constexpr int kDepth = kVecs > 4 ? 1 : 2;      // 8-bit: groups of a warp in flight
+        // 8-bit: groups of a warp in flight; D = 128 keeps every other one in shared memory (two
+        // in registers spill, one alone cannot cover the latency beside a busy stream)
+        constexpr int kDepth = kVecs > 8 ? 1 : 2;
+        constexpr bool kStaged = kVecs == 8;
 
         // page ids of this lane's row of the next kIds groups: an id is a round trip to L2
         // ahead of the copies that need it
@@ -475,7 +480,8 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 if (lane == 0)
                     mbar_arrive(kvFull + 8 * ((u / GP) % NS));
             };
-            uint4 buf[kDepth][kPerLane];
+            uint4 buf[kStaged ? 1 : kDepth][kPerLane];
+            const uint32_t staging = base + C::kOffStage + me * (32 * kVecs * 16) + lane * 16;
             float ks[kDepth], vs[kDepth];
             uint32_t mask[kDepth];
             auto load = [&](int u, int k, int& idK, int& idV) {
@@ -491,9 +497,13 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                 for (int i = 0; i < kPerLane; ++i) {
                     const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
                     const uint32_t src = __shfl_sync(0xffffffffu, row, r);
-                    buf[k][i] = make_uint4(0, 0, 0, 0);
+                    if (kStaged && k == 1) {
+                        copy16(staging + i * 512, headBase + (size_t)src * rowStride + c * 16, (mask[k] >> r) & 1);
+                        continue;
+                    }
+                    buf[kStaged ? 0 : k][i] = make_uint4(0, 0, 0, 0);
                     if ((mask[k] >> r) & 1)
-                        buf[k][i] = __ldg(reinterpret_cast<const uint4*>(headBase + (size_t)src * rowStride + c * 16));
+                        buf[kStaged ? 0 : k][i] = __ldg(reinterpret_cast<const uint4*>(headBase + (size_t)src * rowStride + c * 16));
                 }
                 fetch_ids(u + kStep * kIds, idK, idV);
             };
@@ -518,10 +528,14 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                     const uint32_t dead = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] == 0.0f) : ~mask[k];
                     const uint32_t flip = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] < 0.0f) : 0u;
                     const bool plain = (dead | flip) == 0;
+                    if (kStaged && k == 1)
+                        copy_wait_all();       // each lane reads what it copied
 #pragma unroll
                     for (int i = 0; i < kPerLane; ++i) {
                         const int idx = i * 32 + lane, r = idx / kVecs, c = idx % kVecs;
-                        const uint32_t w[4] = {buf[k][i].x, buf[k][i].y, buf[k][i].z, buf[k][i].w};
+                        const uint4 raw = kStaged && k == 1
+                            ? *reinterpret_cast<const uint4*>(smem + (staging - base) + i * 512) : buf[kStaged ? 0 : k][i];
+                        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
                         uint32_t o[8];
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
@@ -543,6 +557,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                         load(u + kStep * kDepth, k, idsK[ahead], idsV[ahead]);
                 }
             }
+            copy_wait_all();
         }
     } else if (warp < 4 * MT) {
         // ----------------------------------------------------------- softmax
