@@ -85,7 +85,7 @@ int launch(Kern kern, long long grid, int threads, int smem, bool dependent, cud
 
 // How a call is cut into launches, from its sizes alone.
 struct Plan {
-    int nt;             // row tiles of the stream kernel: 8, 16 or 32 rows
+    int nt;             // 1, 2: row tiles of the stream kernel of 8, 16 rows
     bool tensor;        // the prefix goes to the tensor-core kernel
     int parts;          // its ranges of the prefix
     int prefixTiles;    // its row tiles per KV head
@@ -115,9 +115,11 @@ int team_size(int Hkv, int perSm)
     return best;
 }
 
-// Tiles of 8 rows, or of 16 or 32 (D = 256: 16 at most) where a sequence has
-// more, so that its tokens are fetched once. The prefix joins the stream if all
-// rows of a KV head fit into one such tile.
+// Tiles of 8 rows, or of 16 where a sequence has more. A sequence of more than 16
+// rows is fetched once per tile, mostly from L2: tiles of 32 rows, which leave a warp
+// too few registers to overlap anything, were slower (61 sequences x 28 rows of 7 to
+// 700 tokens behind 2000, FP16: 66 us with 32, 55 with 16, 81 with 8). The prefix joins
+// the stream if all rows of a KV head fit into one such tile.
 //
 // A tensor-core prefix of p ranges takes p CTAs per row tile, one to an SM, and the
 // stream's CTAs start where there is room. Either the two kernels follow one another,
@@ -136,7 +138,7 @@ Plan make_plan(const ropekv_attention_dims* d)
 {
     Plan p = {};
     const long long G = d->numQHeads / d->numKVHeads, rowsSeq = d->seqLen * G, rows = d->batch * rowsSeq;
-    p.nt = rowsSeq <= 8 ? 1 : rowsSeq <= 16 || d->headDim == 256 ? 2 : 4;
+    p.nt = rowsSeq <= 8 ? 1 : 2;
     p.tilesSeq = (int)((rowsSeq + 8 * p.nt - 1) / (8 * p.nt));
     p.tensor = d->prefixLen > 0 && rows > 8 * p.nt;
     p.tilesPrefix = d->prefixLen > 0 && !p.tensor ? 1 : 0;
@@ -161,7 +163,7 @@ Plan make_plan(const ropekv_attention_dims* d)
         const long long kv = ((long long)d->prefixLen + 63) / 64;
         // one prefix tile, one warp's step on an SM, one range's partial written and read
         const double tile = f16 && d->headDim != 256 ? 0.95 : 1.3;
-        const double step = (p.nt > 1 ? 0.12 * p.nt : f16 ? 0.16 : 0.1) * d->headDim / 128;
+        const double step = (p.nt > 1 ? 0.22 : f16 ? 0.16 : 0.1) * d->headDim / 128;
         const double work = (double)steps * p.teamSize * step;
         const double part = 0.1 + (double)units * tileRows * d->headDim * 8 / 5e6;
         double best = HUGE_VAL;
@@ -238,18 +240,13 @@ int launch_all(const Args& a, const Plan& p, cudaStream_t st)
     }
     if (rc != ROPEKV_OK)
         return rc;
-    if (p.nt == 1)
-        rc = launch_stream<D, FMT, 1>(a, p, st);
-    else if (p.nt == 2)
-        rc = launch_stream<D, FMT, 2>(a, p, st);
-    else if constexpr (D != 256)
-        rc = launch_stream<D, FMT, 4>(a, p, st);
+    rc = p.nt == 1 ? launch_stream<D, FMT, 1>(a, p, st) : launch_stream<D, FMT, 2>(a, p, st);
     if (rc != ROPEKV_OK)
         return rc;
     // few rows whose items many warps share: all groups of a CTA join one row
     const long long rows = (long long)a.B * a.S * a.Hq;
     constexpr int perCta = 2048 / D;
-    const int tileShift = p.nt == 1 ? 3 : p.nt == 2 ? 4 : 5;
+    const int tileShift = p.nt == 1 ? 3 : 4;
     if (rows < 4LL * kSMs)
         return launch(ropekv_attn::join_kernel<D, true>, rows, 256, 0, true, st, a, tileShift);
     return launch(ropekv_attn::join_kernel<D, false>, (rows + perCta - 1) / perCta, 256, 0, true, st, a, tileShift);
@@ -269,10 +266,6 @@ int dispatch(const Args& a, const Plan& p, int fmt, cudaStream_t st)
 template <int D>
 int stream_warps(bool f16, int nt)
 {
-    if constexpr (D != 256) {
-        if (nt == 4)
-            return f16 ? StreamConfig<D, ROPEKV_CACHE_F16, 4>::kPerSm : StreamConfig<D, ROPEKV_CACHE_E4M3, 4>::kPerSm;
-    }
     if (nt == 2)
         return f16 ? StreamConfig<D, ROPEKV_CACHE_F16, 2>::kPerSm : StreamConfig<D, ROPEKV_CACHE_E4M3, 2>::kPerSm;
     return f16 ? StreamConfig<D, ROPEKV_CACHE_F16, 1>::kPerSm : StreamConfig<D, ROPEKV_CACHE_E4M3, 1>::kPerSm;
