@@ -76,6 +76,8 @@ ROPEKV_API int rope_write_kv_mrope(const float* cosSin, const int64_t* positions
  *   keyScales, valueScales  [numBlocks, Hkv, blockSize] FP32, written.
  *   cacheFormat             ROPEKV_CACHE_E4M3 or ROPEKV_CACHE_INT8, else
  *                           ROPEKV_ERR_STYLE.
+ * Slots of one call that are in range are distinct: of two tokens with the same slot
+ * either may stay, and codes and scale need not come from the same one.
  * The other arguments, skip rules and errors are those of
  * rope_write_kv_slot_mapping.
  */
@@ -151,13 +153,15 @@ ROPEKV_API int64_t paged_attention_workspace_size(const ropekv_attention_dims* d
  *   lse          [B, S, Hq] FP32 natural logarithm of the softmax sum, or NULL.
  *   workspace    paged_attention_workspace_size bytes; its content needs no
  *                preparation and means nothing afterwards. Calls that may run
- *                at the same time need workspaces of their own.
+ *                at the same time, from graphs too, need workspaces of their own.
  * A position whose K or V page is unmapped, or past maxPagesPerSeq, is not
  * seen. A query whose position lies before P (an inactive sequence, kvLens[b] =
  * 0, for one) or that sees nothing gets a zero row and lse = -infinity. What
  * lies in cache slots that no query sees does not matter, whatever its bits.
  * Sums, softmax and partial results are FP32; the weights of V are rounded to
- * FP16 once.
+ * FP16 once. out may be q itself. The call is two or three launches; the split of the
+ * work follows from the sizes alone (pageTable's columns stand for the lengths: a table
+ * much wider than kvLens costs time, not correctness), so equal calls give equal bits.
  * Host errors: sizes negative, tokensPerPage <= 0, seqLen > 2^15, prefixLen >
  * maxPrefixPages * tokensPerPage, 2 * numPages * tokensPerPage >= 2^31,
  * prefixLen or maxPagesPerSeq * tokensPerPage > 2^30, or more than 2^30 query

@@ -31,6 +31,13 @@
 // (A V row with scale 0 is fetched as zeros with vs = 1, one with a negative scale
 // as its negative.)
 //
+// Bound by the chain of products and exponentials of an item: 256 sequences x 4 rows,
+// 8 KV heads of 128, 8192 tokens, FP16: 64 CTAs walk 64 tiles each in 68 us, of which 3.4
+// until the first scores and 3 to write the partials; a tile of two items takes 0.98 us,
+// against 0.68 us of tensor-core time at the measured 1.88 PFLOP/s and 0.53 us of
+// exponentials at 16 a cycle. On all SMs (four ranges) 41 us. 8-bit caches take 1.2 to
+// 1.5 us a tile: the fetch warps' decoding comes on top.
+//
 // Every wait on an mbarrier is bounded. One that runs out ends its role's loop and,
 // through a flag, those of the others, and the CTA writes NaN; no role goes on past
 // a wait that was not satisfied, so no barrier gets an arrival too many.

@@ -236,3 +236,36 @@ def test_sequences_that_share_their_own_pages():
     t = run(c)
     # equal rows of one batch: equal up to where the work is cut
     assert (t["out"].float() - t["out"][:1].float()).abs().max() <= 2.0 ** -9 * t["out"].float().abs().max()
+
+
+@pytest.mark.parametrize("fmt", [F16, E4M3])
+@pytest.mark.parametrize("B,S", [(6, 1), (40, 1), (12, 3)])
+def test_queries_of_inactive_sequences_hold_anything(B, S, fmt):
+    own = [None if i % 3 == 1 else S + 19 * i % 60 for i in range(B)]
+    c = AttentionCase(990 + B, B, S, 8, 2, 128, 16, 90, own, fmt)
+    t = tensors(c)
+    idle = [i for i in range(B) if own[i] is None]
+    t["q"][idle[::2]] = float("nan")
+    t["q"][idle[1::2]] = float("inf")
+    call(c, t)
+    check(c, t)
+
+
+def test_result_in_place_of_the_queries():
+    c = AttentionCase(1000, 30, 1, 8, 2, 128, 16, 200, [1 + 7 * i % 40 for i in range(30)], F16)
+    t = tensors(c)
+    call(c, t)
+    want = t["out"].clone()
+    t["out"] = t["q"]
+    call(c, t)
+    assert torch.equal(t["q"], want)
+
+
+@pytest.mark.parametrize("B", [6, 40])
+def test_table_wider_than_the_lengths(B):
+    """Columns that no sequence reaches change the split of the work, not the result."""
+    own = [1 + 5 * i % 70 for i in range(B)]
+    c = AttentionCase(1010 + B, B, 1, 8, 2, 128, 16, 700, own, F16)
+    c.page_table = np.ascontiguousarray(np.concatenate(
+        [c.page_table, np.full((B, 2, 3000), -1, np.int32)], -1))
+    run(c)
