@@ -12,9 +12,11 @@
 //   warp 8            issues the products S (both operands K-major in shared memory)
 //   warp 9            issues the products O (P in TMEM, V from shared memory, N-major:
 //                     V is stored as it lies in the cache)
-//   warps 10-15       fetch pages: a ring of tiles K0, V0, K1, V1, ... of 64 tokens in
-//                     shared memory, 128-byte swizzled rows of 64 dims. FP16 rows
-//                     come by cp.async, 8-bit rows are decoded to FP16 (exact) on the way
+//   warps 10-15 (and 4-7 with MT = 1)  fetch pages: a ring of tiles K0, V0, K1, V1,
+//                     ... of 64 tokens in shared memory, 128-byte swizzled rows of 64
+//                     dims. FP16 rows come by cp.async, 8-bit rows are decoded to FP16
+//                     (exact) on the way, which paces it with D = 256 (166 rows of 8, E4M3,
+//                     2248 tokens: 127 us with six warps, 91 with ten)
 //
 // Items i = 0, 1, ... take the SL TMEM slots for S in turn. With two row tiles item
 // i is (tile i & 1, K/V tile i >> 1), with one it is K/V tile i. S(i + SL) overwrites
@@ -36,7 +38,7 @@
 // until the first scores and 3 to write the partials; a tile of two items takes 0.98 us,
 // against 0.68 us of tensor-core time at the measured 1.88 PFLOP/s and 0.53 us of
 // exponentials at 16 a cycle. On all SMs (four ranges) 41 us. 8-bit caches take 1.2 to
-// 1.5 us a tile: the fetch warps' decoding comes on top.
+// 1.4 us a tile: the fetch warps' decoding comes on top.
 //
 // Every wait on an mbarrier is bounded. One that runs out ends its role's loop and,
 // through a flag, those of the others, and the CTA writes NaN; no role goes on past
@@ -57,8 +59,8 @@ struct PrefixConfig {
     static constexpr int kMeta = 8;                        // tiles whose scales are kept
     static constexpr int kQBytes = MT * 128 * D * 2;
     static constexpr int kGroups = kTile / 32;             // 32 rows of a tile: one warp's copy
-    static constexpr int kFetchers = 6;
-    static constexpr int kThreads = (10 + kFetchers) * 32;
+    static constexpr int kFetchers = MT == 1 ? 10 : 6;     // warps 10-15, and 4-7 if no softmax needs them
+    static constexpr int kThreads = 16 * 32;
     // arrivals that complete a tile: per group of rows one of each lane's copies and one of
     // the warp (FP16), or the warp's alone
     static constexpr int kArrivals = kGroups * (FMT == kF16 ? 33 : 1);
@@ -373,9 +375,9 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             }
             __syncwarp();
         }
-    } else if (warp > 9) {
+    } else if (warp > 9 || (MT == 1 && warp >= 4)) {
         // ------------------------------------------------------- page fetch
-        const int me = warp - 10;
+        const int me = warp > 9 ? warp - 10 : warp + 2;
         const int groups = 2 * J * GP;
         const size_t rowStride = (size_t)a.Hkv * D * kEsize;
         const uint8_t* headBase = a.pool + (size_t)h * D * kEsize;
@@ -411,9 +413,11 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
         };
         // Waits until tile t - NS, which had tile t's stage, is consumed. Barriers of two
         // laps of the ring: a barrier's parity tells only its last two phases apart, and a
-        // warp does not visit every tile. With barrier (t - NS) % 2 NS the phase before the
-        // one waited for is tile t - 3 NS, which is consumed: the warp waited for tile
-        // t - 3 - NS, and products are taken less than NS tiles out of order. The phase after is tile t + NS, for which tile t would be needed.
+        // warp visits only every d-th tile, d = kFetchers / GP. With barrier (t - NS) % 2 NS
+        // the phase before the one waited for is tile t - 3 NS, which is consumed: the warp
+        // waited for tile t - d - NS, and with a tile all up to NS - 1 before it are consumed.
+        // The phase after is tile t + NS, for which tile t would be needed.
+        static_assert(C::kFetchers % GP == 0 && C::kFetchers / GP <= NS + 1, "see above");
         auto stage_free = [&](int t) -> bool {
             const int old = t - NS;
             return old < 0 || mbar_wait_warp(kvEmpty + 8 * (old % (2 * NS)), (old / (2 * NS)) & 1, failed);
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             }
             copy_wait_all();
         }
-    } else if (warp < 4 * MT) {
+    } else {
         // ----------------------------------------------------------- softmax
         // first of all Q, zeros past the last row, while the first pages come
         for (int i = threadIdx.x; i < MT * 128 * (D / 8); i += MT * 128) {
