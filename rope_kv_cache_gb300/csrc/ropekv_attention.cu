@@ -184,7 +184,14 @@ Plan make_plan(const ropekv_attention_dims* d)
             }
         }
     }
-    p.teams = (int)(steps < 1 ? 1 : steps < most ? steps : most);
+    // Few long units: a share of s steps leaves n / s partials to a row, of which the join
+    // takes 8192 / D at a time, in about the time of a step: s = sqrt(n D / 8192) balances
+    // the two (one sequence, one KV head, 14000 prefix tokens, INT8, D = 256: 27 us with
+    // s = 1, 16 with 5; two sequences, four KV heads of 128, 6000 tokens: 12.6 and 12.7).
+    const long long longestSteps = std::max(p.tilesPrefix ? (long long)d->prefixLen / 16 : 0LL, own > 0 ? own / 16 : 0LL);
+    const long long least = std::max(1LL, (long long)(sqrt((double)longestSteps * d->headDim / 8192) + 0.5));
+    most = std::min(most, (steps + least - 1) / least);
+    p.teams = (int)std::max(1LL, most);
     p.slots = (items + (long long)p.tilesPrefix * p.groups + p.teams) * p.teamSize;
     p.partRows = (int64_t)p.parts * d->numKVHeads * rows;
     return p;
