@@ -269,3 +269,23 @@ def test_table_wider_than_the_lengths(B):
     c.page_table = np.ascontiguousarray(np.concatenate(
         [c.page_table, np.full((B, 2, 3000), -1, np.int32)], -1))
     run(c)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    """Sizes drawn over the whole range, the workspace guarded by bytes behind its end."""
+    import rope_kv_cache_gb300 as rk
+    rng = np.random.Generator(np.random.PCG64(2000 + seed))
+    pick = lambda *x: x[rng.integers(len(x))]
+    log = lambda a, b: int(round(np.exp(rng.uniform(np.log(a), np.log(b)))))
+    D, Hkv, G, S = pick(64, 128, 256), pick(1, 2, 3, 4, 5, 8, 9), pick(1, 2, 3, 4, 7, 8, 16), pick(1, 1, 1, 2, 5, 8, 16)
+    P, tpp, fmt, B = pick(0, log(1, 60), log(16, 1500)), pick(1, 3, 8, 16, 24, 64, 100), pick(F16, E4M3, INT8), log(1, 40)
+    own = [None if rng.random() < 0.1 else S + int(rng.integers(log(1, 300))) for _ in range(B)]
+    c = AttentionCase(3000 + seed, B, S, Hkv * G, Hkv, D, tpp, P, own, fmt, q_scale=pick(0.3, 1.0, 3.0),
+                      unmapped=pick(0, 0, 0.2), spread=pick(0, 0, 3))
+    t = tensors(c)
+    size = rk.paged_attention_workspace_size(t["q"], t["pool"], t["prefix"], c.P, t["table"], kv_scales=t["scales"])
+    ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    call(c, t, workspace=ws[:size])
+    check(c, t)
+    assert (ws[size:] == 0xFF).all()
