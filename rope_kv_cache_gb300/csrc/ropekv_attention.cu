@@ -132,8 +132,8 @@ int team_size(int Hkv, int perSm)
 // if only the former count, 36 us). Measured, one after the other against side by
 // side: 256 sequences of 1 to 512 tokens behind 8192, FP16: 89 against 79 us; 128 of
 // 1 to 2048 behind 4097, E4M3: 78 against 68; 61 x 7 rows behind 2000, INT8: 86
-// against 60; 40 of 1 to 900 behind 3001, D = 256: 32 against 22. Against it: 128 of
-// 1 to 2048 behind 16000, E4M3: 105 against 114.
+// against 60; 40 of 1 to 900 behind 3001, D = 256: 32 against 22. The estimate keeps
+// 128 of 1 to 2048 behind 16000, E4M3, apart: 105 against 114.
 Plan make_plan(const ropekv_attention_dims* d)
 {
     Plan p = {};
