@@ -30,8 +30,10 @@
 // row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: with ks and vs
 // a token's scales, x = ks c s + log2(vs) and P = 2^(x - M) is weight times V scale
 // in one exponential, near [0, 2^8] whatever the scales; the row sum adds P / vs.
-// (A V row with scale 0 is fetched as zeros with vs = 1, one with a negative scale
-// as its negative.)
+// (A V row whose scale is below 2^-40 in magnitude is fetched as zeros with vs = 1, one
+// with a negative scale as its negative. The codes of such a row are worth less than
+// 2^-31 each, nothing beside an FP16 result's last place of 2^-24; 1 / vs of a smaller
+// scale would push the sum P / vs out of FP32, and P itself below it.)
 //
 // Bound by the chain of products and exponentials of an item: 256 sequences x 4 rows,
 // 8 KV heads of 128, 8192 tokens, FP16: 64 CTAs walk 64 tiles each in 68 us, of which 3.4
@@ -48,6 +50,9 @@
 #include "ropekv_attention_kernels.cuh"
 
 namespace ropekv_attn {
+
+// V scales of smaller magnitude count as 0.
+constexpr float kSmallestScale = 9.094947017729282e-13f;   // 2^-40
 
 template <int D, int FMT, int MT>
 struct PrefixConfig {
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             const int j = (u / GP) >> 1, g = u % GP, slot = j % C::kMeta;
             if (FMT != kF16) {
                 const int at = slot * TN + g * 32 + lane;
-                const float v = vs == 0.0f ? 1.0f : fabsf(vs);
+                const float v = fabsf(vs) < kSmallestScale ? 1.0f : fabsf(vs);
                 reinterpret_cast<float*>(smem + C::kOffKs)[at] = ks * a.scaleLog2;
                 reinterpret_cast<float*>(smem + C::kOffVs)[at] = log2f(v);
                 reinterpret_cast<float*>(smem + C::kOffRv)[at] = 1.0f / v;
@@ -535,8 +540,8 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                     }
                     uint8_t* dst = smem + C::kOffRing + (t % NS) * C::kTileBytes;
                     const int r0 = (u % GP) * 32;
-                    // zero rows: unmapped tokens and V rows with scale 0; V rows with a negative scale
-                    const uint32_t dead = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] == 0.0f) : ~mask[k];
+                    // zero rows: unmapped tokens and V rows whose scale counts as 0; V rows with a negative scale
+                    const uint32_t dead = (t & 1) ? __ballot_sync(0xffffffffu, fabsf(vs[k]) < kSmallestScale) : ~mask[k];
                     const uint32_t flip = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] < 0.0f) : 0u;
                     const bool plain = (dead | flip) == 0;
                     if (kStaged && k == 1)

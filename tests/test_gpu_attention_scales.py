@@ -1,0 +1,71 @@
+"""paged_attention_shared_prefix over 8-bit caches whose scales lie outside what the 8-bit
+write makes of FP16 rows: zero, subnormal, very small, negative, large and not finite. A
+batch of one has its prefix streamed, a larger one takes it to the tensor cores: both
+are held to the same 64-bit softmax, with the bounds of serving_plain."""
+import numpy as np
+import pytest
+
+from serving_plain import E4M3, INT8, AttentionCase
+from test_gpu_attention import call, check, tensors
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+BATCHES = [1, 40]           # 4 and 160 rows a KV head
+FORMATS = [E4M3, INT8]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from rope_kv_cache_gb300 import build
+    build.build_library()
+
+
+def make(seed, B, fmt, D=128, P=90, **kw):
+    return AttentionCase(seed, B, 1, 8, 2, D, 16, P, [3 + 7 * i % 40 for i in range(B)], fmt, **kw)
+
+
+def slots(c, plane, which):
+    """(page, row) of the prefix positions and of every sequence's own positions whose number
+    modulo 5 is in `which`."""
+    out = []
+    for p in range(c.P):
+        if p % 5 in which:
+            out.append((int(c.prefix_table[plane, p // c.tpp]) - plane * c.pages, p % c.tpp))
+    for b in range(c.B):
+        for p in range(c.P, int(c.kv_lens[b])):
+            if p % 5 in which:
+                out.append((int(c.page_table[b, plane, p // c.tpp]) - plane * c.pages, p % c.tpp))
+    return out
+
+
+def set_scale(c, plane, which, value, head=slice(None)):
+    for page, row in slots(c, plane, which):
+        c.scales[plane, page, head, row] = value
+
+
+def run(c):
+    t = tensors(c)
+    call(c, t)
+    check(c, t)
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, 2.0 ** -134.8, 2.0 ** -128.5, 2.0 ** -126, 2.0 ** -115,
+                                   2.0 ** -101, 2.0 ** -61, 2.0 ** -41, 2.0 ** -33])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B", BATCHES)
+def test_small_v_scales_beside_ordinary_ones(B, fmt, scale):
+    c = make(900, B, fmt)
+    set_scale(c, 1, {1, 3}, scale)
+    run(c)
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, 2.0 ** -130, 2.0 ** -115, 2.0 ** -80, 2.0 ** -39])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("B", BATCHES)
+def test_all_v_scales_small(B, D, scale):
+    c = make(910, B, INT8, D=D)
+    set_scale(c, 1, {0, 1, 2, 3, 4}, scale)
+    run(c)
