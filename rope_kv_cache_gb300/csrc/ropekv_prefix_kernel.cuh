@@ -30,10 +30,12 @@
 // row's O is rescaled in TMEM; the first tile sets it. 8-bit caches: with ks and vs
 // a token's scales, x = ks c s + log2(vs) and P = 2^(x - M) is weight times V scale
 // in one exponential, near [0, 2^8] whatever the scales; the row sum adds P / vs.
-// (A V row whose scale is below 2^-40 in magnitude is fetched as zeros with vs = 1, one
-// with a negative scale as its negative. The codes of such a row are worth less than
+// (A V row whose scale is below 2^-40 in magnitude is fetched as zeros with vs = 2^-40,
+// one with a negative scale as its negative. The codes of such a row are worth less than
 // 2^-31 each, nothing beside an FP16 result's last place of 2^-24; 1 / vs of a smaller
-// scale would push the sum P / vs out of FP32, and P itself below it.)
+// scale would push the sum P / vs out of FP32, and P itself below it, while a larger vs
+// would lift M, and with it the FP16 weights of rows whose values are small would lose
+// their last bits.)
 //
 // Bound by the chain of products and exponentials of an item: 256 sequences x 4 rows,
 // 8 KV heads of 128, 8192 tokens, FP16: 64 CTAs walk 64 tiles each in 68 us, of which 3.4
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             const int j = (u / GP) >> 1, g = u % GP, slot = j % C::kMeta;
             if (FMT != kF16) {
                 const int at = slot * TN + g * 32 + lane;
-                const float v = fabsf(vs) < kSmallestScale ? 1.0f : fabsf(vs);
+                const float v = fabsf(vs) < kSmallestScale ? kSmallestScale : fabsf(vs);
                 reinterpret_cast<float*>(smem + C::kOffKs)[at] = ks * a.scaleLog2;
                 reinterpret_cast<float*>(smem + C::kOffVs)[at] = log2f(v);
                 reinterpret_cast<float*>(smem + C::kOffRv)[at] = 1.0f / v;

@@ -69,3 +69,15 @@ def test_all_v_scales_small(B, D, scale):
     c = make(910, B, INT8, D=D)
     set_scale(c, 1, {0, 1, 2, 3, 4}, scale)
     run(c)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B", BATCHES)
+def test_a_zero_row_of_v_costs_the_others_no_accuracy(B, D, fmt):
+    """Tokens with V scale 0 and the largest scores, beside V rows of about 2^-10 with small weights."""
+    c = make(920, B, fmt, D=D, P=40, v_scale=2.0 ** -10)
+    set_scale(c, 1, {1}, 0.0)
+    for page, row in slots(c, 0, {1}):
+        c.scales[0, page, :, row] *= 6
+    run(c)
