@@ -195,6 +195,12 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t& lo, uint32_t& 
     hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+__device__ __forceinline__ uint32_t half2_times(uint32_t x, uint32_t y)
+{
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Not 0 if a word of V (two halves, four codes) holds an infinity or NaN.
 template <int FMT>
 __device__ __forceinline__ uint32_t non_finite(uint32_t w)

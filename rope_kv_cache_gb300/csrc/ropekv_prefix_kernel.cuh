@@ -35,7 +35,8 @@
 // 2^-31 each, nothing beside an FP16 result's last place of 2^-24; 1 / vs of a smaller
 // scale would push the sum P / vs out of FP32, and P itself below it, while a larger vs
 // would lift M, and with it the FP16 weights of rows whose values are small would lose
-// their last bits.)
+// their last bits. A row whose scale is not finite is fetched as NaN with vs = 2^-40: it
+// belongs to the sum of the softmax like any other.)
 //
 // Bound by the chain of products and exponentials of an item: 256 sequences x 4 rows,
 // 8 KV heads of 128, 8192 tokens, FP16: 64 CTAs walk 64 tiles each in 68 us, of which 3.4
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
             const int j = (u / GP) >> 1, g = u % GP, slot = j % C::kMeta;
             if (FMT != kF16) {
                 const int at = slot * TN + g * 32 + lane;
-                const float v = fabsf(vs) < kSmallestScale ? kSmallestScale : fabsf(vs);
+                const float v = fabsf(vs) >= kSmallestScale && fabsf(vs) < INFINITY ? fabsf(vs) : kSmallestScale;
                 reinterpret_cast<float*>(smem + C::kOffKs)[at] = ks * a.scaleLog2;
                 reinterpret_cast<float*>(smem + C::kOffVs)[at] = log2f(v);
                 reinterpret_cast<float*>(smem + C::kOffRv)[at] = 1.0f / v;
@@ -542,10 +543,11 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                     }
                     uint8_t* dst = smem + C::kOffRing + (t % NS) * C::kTileBytes;
                     const int r0 = (u % GP) * 32;
-                    // zero rows: unmapped tokens and V rows whose scale counts as 0; V rows with a negative scale
-                    const uint32_t dead = (t & 1) ? __ballot_sync(0xffffffffu, fabsf(vs[k]) < kSmallestScale) : ~mask[k];
-                    const uint32_t flip = (t & 1) ? __ballot_sync(0xffffffffu, vs[k] < 0.0f) : 0u;
-                    const bool plain = (dead | flip) == 0;
+                    // V rows are taken times 1, -1 (negative scale), 0 (small scale, unmapped token) or
+                    // NaN (scale not finite); unmapped K rows are zeros as loaded
+                    const uint32_t factor = fabsf(vs[k]) < kSmallestScale ? 0u : !(fabsf(vs[k]) < INFINITY) ? 0x7fff7fffu
+                                            : vs[k] < 0.0f ? 0xbc00bc00u : 0x3c003c00u;
+                    const bool plain = !(t & 1) || __all_sync(0xffffffffu, factor == 0x3c003c00u);
                     if (kStaged && k == 1)
                         copy_wait_all();       // each lane reads what it copied
 #pragma unroll
@@ -559,11 +561,10 @@ __global__ void __launch_bounds__(PrefixConfig<D, FMT, MT>::kThreads, 1) prefix_
                         for (int x = 0; x < 4; ++x)
                             decode_word<FMT, false>(w[x], o[2 * x], o[2 * x + 1]);
                         if (!plain) {
-                            const uint32_t keep = (dead >> r) & 1 ? 0u : 0xffffffffu;
-                            const uint32_t sign = (flip >> r) & 1 ? 0x80008000u : 0u;
+                            const uint32_t f = __shfl_sync(0xffffffffu, factor, r);
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                o[x] = (o[x] ^ sign) & keep;
+                                o[x] = half2_times(o[x], f);
                         }
                         *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4*>(dst + tile_pos(TN, r0 + r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);

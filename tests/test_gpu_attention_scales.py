@@ -81,3 +81,55 @@ def test_a_zero_row_of_v_costs_the_others_no_accuracy(B, D, fmt):
     for page, row in slots(c, 0, {1}):
         c.scales[0, page, :, row] *= 6
     run(c)
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("where", ["prefix", "own"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B", BATCHES)
+def test_a_v_scale_that_is_not_finite_leaves_lse_alone(B, fmt, where, value):
+    """Only `out` depends on V: the rows that see the token get no finite element, their
+    lse and the other heads are as ever."""
+    c = make(930, B, fmt)
+    p = 7 if where == "prefix" else c.P + 1
+    tab = c.prefix_table if where == "prefix" else c.page_table[0]
+    c.scales[1, tab[1, p // c.tpp] - c.pages, 1, p % c.tpp] = value
+    t = tensors(c)
+    call(c, t)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        out, lse, tol_o, tol_l = c.solve()
+    got, gl = t["out"].cpu().numpy().astype(np.float64), t["lse"].cpu().numpy().astype(np.float64)
+    assert (np.abs(gl - lse) <= tol_l).all()
+    hit = np.zeros(got.shape, bool)
+    hit[slice(None) if where == "prefix" else 0, :, 4:] = True
+    assert not np.isfinite(got[hit]).any()
+    assert (np.abs(got[~hit] - out[~hit]) <= tol_o[~hit]).all()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("B", BATCHES)
+def test_a_k_scale_that_is_nan_reaches_out_and_lse(B, value):
+    """The scores are not finite (the codes of the token have both signs): no row of that
+    head has a result, on either path, and the join passes it on."""
+    c = make(940, B, INT8)
+    c.scales[0, c.prefix_table[0, 0], 0, 3] = value
+    if not np.isnan(value):
+        c.pool[0, c.prefix_table[0, 0], 3, 0] = 0            # 0 * infinity
+    t = tensors(c)
+    call(c, t)
+    torch.cuda.synchronize()
+    got, gl = t["out"].cpu().numpy(), t["lse"].cpu().numpy()
+    assert np.isnan(got[:, :, :4]).all() and np.isnan(gl[:, :, :4]).all()
+    assert np.isfinite(got[:, :, 4:]).all() and np.isfinite(gl[:, :, 4:]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B", BATCHES)
+def test_negative_and_zero_scales(B, fmt):
+    c = make(950, B, fmt)
+    for plane in (0, 1):
+        for page, row in slots(c, plane, {0, 3}):
+            c.scales[plane, page, :, row] *= -1
+    set_scale(c, 0, {2}, 0.0)
+    run(c)
