@@ -158,9 +158,10 @@ ROPEKV_API int64_t paged_attention_workspace_size(const ropekv_attention_dims* d
  * seen. A query whose position lies before P (an inactive sequence, kvLens[b] =
  * 0, for one) or that sees nothing gets a zero row and lse = -infinity. What
  * lies in cache slots that no query sees does not matter, whatever its bits.
- * Scales may be any FP32 numbers; a V scale below 2^-40 in magnitude may count as 0 (such a
+ * Scales may have either sign. A V scale below 2^-40 in magnitude may count as 0 (such a
  * token adds less than 2^-31 to an element of out). A token whose V scale is infinite or NaN
- * leaves no finite element in the rows that see it; their lse does not depend on it.
+ * leaves no finite element in the rows that see it; their lse does not depend on it. V
+ * scales between 2^60 and infinity are not supported (elements may be NaN).
  * Sums, softmax and partial results are FP32; the weights of V are rounded to
  * FP16 once. out may be q itself. The call is two or three launches; the split of the
  * work follows from the sizes alone (pageTable's columns stand for the lengths: a table

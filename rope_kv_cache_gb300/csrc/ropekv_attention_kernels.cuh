@@ -263,10 +263,11 @@ __device__ __forceinline__ int swizzle(int r, int c)
 // 8 columns) keep the ALU pipes 55 % busy.
 constexpr int kMaxParts = 32;    // prefix partials at most
 
-// Exponent of a V scale, kept where 2^(s - m) cannot leave FP32.
+// Exponent of a V scale, kept where 2^(s - m) cannot leave FP32. Up to 2^60, the largest
+// finite scale that is supported, weight times scale stays below 2^9 in FP16.
 __device__ __forceinline__ float scale_exponent(float scale)
 {
-    return (float)max(-60, min(40, (int)((__float_as_uint(scale) >> 23) & 0xff) - 127));
+    return (float)max(-60, min(60, (int)((__float_as_uint(scale) >> 23) & 0xff) - 127));
 }
 
 template <int D, int FMT, int NT>

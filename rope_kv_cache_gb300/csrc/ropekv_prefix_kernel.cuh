@@ -35,8 +35,9 @@
 // 2^-31 each, nothing beside an FP16 result's last place of 2^-24; 1 / vs of a smaller
 // scale would push the sum P / vs out of FP32, and P itself below it, while a larger vs
 // would lift M, and with it the FP16 weights of rows whose values are small would lose
-// their last bits. A row whose scale is not finite is fetched as NaN with vs = 2^-40: it
-// belongs to the sum of the softmax like any other.)
+// their last bits; beside the largest supported scale, 2^60, a token with 2^-40 is still
+// summed down to 2^-26 of the other's share. A row whose scale is not finite is fetched
+// as NaN with vs = 2^-40: it belongs to the sum of the softmax like any other.)
 //
 // Bound by the chain of products and exponentials of an item: 256 sequences x 4 rows,
 // 8 KV heads of 128, 8192 tokens, FP16: 64 CTAs walk 64 tiles each in 68 us, of which 3.4

@@ -133,3 +133,26 @@ def test_negative_and_zero_scales(B, fmt):
             c.scales[plane, page, :, row] *= -1
     set_scale(c, 0, {2}, 0.0)
     run(c)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 59])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B", BATCHES)
+def test_large_v_scales(B, fmt, scale):
+    """Elements past FP16's range become infinite; a dim whose codes are 0 in all tokens of
+    such a scale stays finite."""
+    c = make(960, B, fmt)
+    set_scale(c, 1, {2}, scale)
+    set_scale(c, 1, {4}, 0.0)
+    for page, row in slots(c, 1, {2}):
+        c.pool[1, page, row, :, :64] = 0
+    t = tensors(c)
+    call(c, t)
+    torch.cuda.synchronize()
+    out, lse, _, tol_l = c.solve()
+    got, gl = t["out"].cpu().numpy().astype(np.float64), t["lse"].cpu().numpy().astype(np.float64)
+    assert (np.abs(gl - lse) <= tol_l).all()
+    assert np.isfinite(got[..., :64]).all()
+    big = np.abs(out) > scale          # a sum of FP16 weights times codes is off by far less
+    assert big.any() and not big[..., :64].any()
+    assert np.isinf(got[big]).all() and (np.sign(got) == np.sign(out))[big].all()
