@@ -288,11 +288,12 @@ __global__ void __launch_bounds__(256) quant_write_kernel(const __grid_constant_
         const float amax = __uint_as_float(top);
         const bool finite = top < 0x7f800000u;
         const bool zero = amax < kTiny;
-        const float mul = (finite && !zero) ? __fdiv_rn(kMaxCode, amax) : 0.0f;
+        const bool coded = finite && !zero;
+        const float mul = coded ? __fdiv_rn(kMaxCode, amax) : 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            fa[j] = finite ? fa[j] * mul : 0.0f;
-            fb[j] = finite ? fb[j] * mul : 0.0f;
+            fa[j] = coded ? fa[j] * mul : 0.0f;    // +0: a negative element times 0 would be code 0x80
+            fb[j] = coded ? fb[j] * mul : 0.0f;
         }
         const int hk = isK ? head - a.Hq : head - a.Hq - a.Hkv;
         uint8_t* dst = (uint8_t*)(isK ? a.keyCache : a.valueCache) + ((size_t)slot * a.Hkv + hk) * D;
