@@ -68,7 +68,10 @@ ROPEKV_API int rope_write_kv_mrope(const float* cosSin, const int64_t* positions
  * rope_write_kv_slot_mapping into an 8-bit cache whose scales are found as it
  * is written. For every token and KV head, with x the rotated K head (FP32, not
  * rounded to FP16) or the V head and M = 448 (E4M3) or 127 (INT8):
- *   scale = max|x| / M,   code = round to nearest even of x / scale.
+ *   scale = max|x| / M,   code = x * (M / max|x|), rounded to the nearest code (ties to
+ *                                                  the even one);
+ * both quotients and the product are rounded to FP32 first, so that an element next to the
+ * border between two codes may get another one than x / scale has.
  * A head of zeros (or whose largest magnitude is below 2^-100) gets scale 0 and
  * codes 0; a head that holds an infinity or a NaN gets scale NaN and codes 0,
  * so that every element reads back as NaN.
