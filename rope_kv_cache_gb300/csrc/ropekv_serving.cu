@@ -3,7 +3,10 @@
 // kernels and C entry points (include/ropekv_serving.h). All three are
 // streaming kernels, bound by HBM, and share the item decomposition, the L2
 // policies and the dependent-launch prologue of ropekv_kernels.cuh: an item is
-// two 16-byte vectors of one head, D/16 consecutive lanes hold a head.
+// two 16-byte vectors of one head, D/16 consecutive lanes hold a head. All but the
+// cos/sin rows comes by ordinary loads: a CTA may be resident before the grid in front of
+// it has overwritten what it will read (its wait orders the two), so these are not
+// constant for the life of the kernel, as the non-coherent path asks.
 #include <cuda_runtime.h>
 
 #include <cuda_fp16.h>
@@ -105,26 +108,26 @@ __global__ void __launch_bounds__(256) mrope_kernel(const __grid_constant__ Writ
         const int item = item0 + k * blockDim.x;
         if (item < a.itemsPerToken) {
             const uint16_t* p = head_row(a, tok, item / kItemsPerHead, D);
-            xa[k] = load_ro<POL>(p + 8 * va, pol);
-            xb[k] = load_ro<POL>(p + 8 * vb, pol);
+            xa[k] = load_rw<POL>(p + 8 * va, pol);
+            xb[k] = load_rw<POL>(p + 8 * vb, pol);
         }
     }
 
     int64_t rowOff[kMaxAxes];
-    const int64_t pos0 = __ldg(a.positions + tok);
+    const int64_t pos0 = a.positions[tok];
     bool ok = pos0 >= 0 && pos0 < a.csRows, same = true;
     rowOff[0] = pos0 * a.r;
 #pragma unroll
     for (int x = 1; x < kMaxAxes; ++x) {
         rowOff[x] = rowOff[0];
         if (x < a.numAxes) {
-            const int64_t p = __ldg(a.positions + (int64_t)x * a.T + tok);
+            const int64_t p = a.positions[(int64_t)x * a.T + tok];
             ok = ok && p >= 0 && p < a.csRows;
             same = same && p == pos0;
             rowOff[x] = p * a.r;
         }
     }
-    const int64_t slot = __ldg(a.slots + tok);
+    const int64_t slot = a.slots[tok];
     if (!ok)
         return;  // no cos/sin row: nothing written for the token
     const bool kvOk = slot >= 0 && slot < a.numSlots;
@@ -236,12 +239,12 @@ __global__ void __launch_bounds__(256) quant_write_kernel(const __grid_constant_
         const int item = item0 + k * blockDim.x;
         if (item < a.itemsPerToken) {
             const uint16_t* p = head_row(a, tok, item / kItemsPerHead, D);
-            xa[k] = load_ro<POL>(p + 8 * va, pol);
-            xb[k] = load_ro<POL>(p + 8 * vb, pol);
+            xa[k] = load_rw<POL>(p + 8 * va, pol);
+            xb[k] = load_rw<POL>(p + 8 * vb, pol);
         }
     }
-    const int64_t pos = __ldg(a.positions + tok);
-    const int64_t slot = __ldg(a.slots + tok);
+    const int64_t pos = a.positions[tok];
+    const int64_t slot = a.slots[tok];
     if (pos < 0 || pos >= a.csRows)
         return;  // no cos/sin row: nothing written for the token
     const bool kvOk = slot >= 0 && slot < a.numSlots;
@@ -329,13 +332,8 @@ __device__ __forceinline__ float2 decode2(uint32_t two)
     return make_float2((float)(int8_t)(two & 0xff), (float)(int8_t)((two >> 8) & 0xff));
 }
 
-__device__ __forceinline__ uint4 load_code(const uint8_t* p, const L2Policies& pol)
-{
-    return load_ro<kStreamHint>(reinterpret_cast<const uint16_t*>(p), pol);
-}
-
 // One thread: the same 16-byte vector of a row's K and of its V. Rows of few
-// vectors share a CTA. 65521 rows of 8 heads of 128 E4M3 codes: 61.9 us, 6.58 TB/s.
+// vectors share a CTA. 65521 rows of 8 heads of 128 E4M3 codes: 61.1 us, 6.67 TB/s.
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ ReadArgs a)
 {
@@ -347,8 +345,8 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
     if (t >= a.N)
         return;
     const int vec = (int)(g - t * a.vecsPerRow);
-    const int pos = __ldg(a.positions + t);
-    const int seq = __ldg(a.seqIds + t);
+    const int pos = a.positions[t];
+    const int seq = a.seqIds[t];
     if (pos < 0 || seq < 0 || seq >= a.B)
         return;
     const int lp = pos / a.tpp;
@@ -356,8 +354,8 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
         return;
     const int inPage = pos - lp * a.tpp;
     const int32_t* pt = a.pageTable + (size_t)seq * 2 * a.mpps + lp;
-    const int idK = __ldg(pt);
-    const int idV = __ldg(pt + a.mpps);
+    const int idK = pt[0];
+    const int idV = pt[a.mpps];
     const bool ok[2] = {idK >= 0 && idK < a.numPages,
                         idV >= a.numPages && idV - a.numPages < a.numPages};
     const int id[2] = {idK, idV};
@@ -369,10 +367,11 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
 #pragma unroll
     for (int p = 0; p < 2; ++p)
         if (ok[p]) {
-            x[p] = load_code(a.pool + (((size_t)id[p] * a.tpp + inPage) * rowElems) *
-                                 (FMT == ROPEKV_CACHE_F16 ? 2 : 1) + 16 * (size_t)vec, pol);
+            x[p] = load_rw<kStreamHint>(reinterpret_cast<const uint16_t*>(
+                a.pool + ((size_t)id[p] * a.tpp + inPage) * rowElems * (FMT == ROPEKV_CACHE_F16 ? 2 : 1) +
+                16 * (size_t)vec), pol);
             if (FMT != ROPEKV_CACHE_F16)
-                sc[p] = __ldg(a.scales + ((size_t)id[p] * a.Hkv + head) * a.tpp + inPage);
+                sc[p] = a.scales[((size_t)id[p] * a.Hkv + head) * a.tpp + inPage];
         }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
