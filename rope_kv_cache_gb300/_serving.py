@@ -17,10 +17,10 @@ from typing import Optional, Sequence
 import torch
 
 from ._binding import NEOX, RopeKVError
+from .build import bind_path
 
 _LIB_DIR = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib")
 SERVING_LIB_PATH = os.path.join(_LIB_DIR, "libropekv_serving.so")
-BIND_PATH = os.path.join(_LIB_DIR, "ropekv_bind.so")
 _lib = None
 _bind = None
 
@@ -40,11 +40,11 @@ def _require(path: str) -> str:
 
 
 def _native():
-    """The compiled binding, loaded once."""
+    """The compiled binding of the running torch, loaded once."""
     global _bind
     if _bind is None:
         _require(SERVING_LIB_PATH)
-        spec = importlib.util.spec_from_file_location("ropekv_bind", _require(BIND_PATH))
+        spec = importlib.util.spec_from_file_location("ropekv_bind", _require(bind_path()))
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _bind = module

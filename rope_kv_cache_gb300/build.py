@@ -1,6 +1,6 @@
 """Build libropekv.so (the C ABI and its sm_103a kernels) in-tree with nvcc,
 libropekv_serving.so (the serving operators around the paged cache) with
-ropekv_bind.so, its Python module for torch tensors, and libropekv_floor.so, the
+ropekv_bind-*.so, its Python module for torch tensors, and libropekv_floor.so, the
 copy kernel the benchmark times as the floor of a decode-sized launch.
 
 Each library is compiled for sm_103a only and linked against the static CUDA
@@ -32,7 +32,6 @@ SERVING_SOURCES = [os.path.join(CSRC, "ropekv_serving.cu"),
 SERVING_DEPS = SERVING_SOURCES + [os.path.join(CSRC, n) for n in (
     "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh", "ropekv_prefix_kernel.cuh")] + [
     os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
-BIND_PATH = os.path.join(LIB_DIR, "ropekv_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "ropekv_bind.cpp")
 BIND_DEPS = [BIND_SOURCE] + [os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
@@ -49,6 +48,15 @@ def nvcc_command(out: str, extra=(), sources=None) -> list:
     return [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
             "-Xcompiler", "-fPIC,-fvisibility=hidden", "-cudart", "static",
             "-I", INCLUDE, "-I", CSRC, *extra, "-o", out, *(sources or SOURCES)]
+
+
+def bind_path() -> str:
+    """The Python module for the running torch and Python. Its name holds both: it is tied
+    to torch's C++ ABI, which file times say nothing about, so that after another torch was
+    installed the module is missing (and built again) instead of loaded."""
+    import torch
+
+    return os.path.join(LIB_DIR, f"ropekv_bind-torch{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def bind_commands(out: str, obj: str) -> tuple:
@@ -92,11 +100,12 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
                 procs = [subprocess.Popen([a for a in nvcc_command(o, (*extra, "-c"), [src])
                                            if a != "-shared"]) for o, src in zip(objs, sources)]
                 jobs.append((procs, objs, nvcc_command(tmp, (), objs), tmp, lib))
-    if force or _stale(BIND_PATH, BIND_DEPS):
+    bind = bind_path()
+    if force or _stale(bind, BIND_DEPS):
         # after the library that it links with
-        tmp = BIND_PATH + f".{os.getpid()}.tmp"
+        tmp = bind + f".{os.getpid()}.tmp"
         compile_, link = bind_commands(tmp, tmp + ".o")
-        jobs.append(([subprocess.Popen(compile_)], [tmp + ".o"], link, tmp, BIND_PATH))
+        jobs.append(([subprocess.Popen(compile_)], [tmp + ".o"], link, tmp, bind))
     failed = []
     for procs, objs, link, tmp, lib in jobs:
         ok = all([p.wait() == 0 for p in procs])
