@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -59,6 +60,18 @@ def bind_path() -> str:
     return os.path.join(LIB_DIR, f"ropekv_bind-torch{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
+def bind_lacks() -> str:
+    """What the Python module needs and this machine does not have ("" if nothing)."""
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    return "" if os.path.exists(os.path.join(lib, "libc10_cuda.so")) else "a CUDA build of torch"
+
+
 def bind_commands(out: str, obj: str) -> tuple:
     """Compile and link commands of the Python module."""
     import torch  # headers and libraries of the installed torch
@@ -84,7 +97,9 @@ def _stale(lib: str, deps) -> bool:
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Build the libraries where stale (or always with force); returns the
-    path of libropekv.so."""
+    path of libropekv.so. The C libraries need nvcc alone. Where the Python module's
+    needs are not met it is left out with a warning, and the Python functions of the
+    serving operators raise."""
     os.makedirs(LIB_DIR, exist_ok=True)
     extra = ("-Xptxas", "-v") if verbose else ()
     jobs = []   # (compilers, their objects, link command (None: nothing to link), output, library)
@@ -100,8 +115,11 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
                 procs = [subprocess.Popen([a for a in nvcc_command(o, (*extra, "-c"), [src])
                                            if a != "-shared"]) for o, src in zip(objs, sources)]
                 jobs.append((procs, objs, nvcc_command(tmp, (), objs), tmp, lib))
-    bind = bind_path()
-    if force or _stale(bind, BIND_DEPS):
+    lacks = bind_lacks()
+    if lacks:
+        warnings.warn(f"the Python module of the serving operators is not built: {lacks} is not there")
+    elif force or _stale(bind_path(), BIND_DEPS):
+        bind = bind_path()
         # after the library that it links with
         tmp = bind + f".{os.getpid()}.tmp"
         compile_, link = bind_commands(tmp, tmp + ".o")
