@@ -169,6 +169,8 @@ ROPEKV_API int64_t paged_attention_workspace_size(const ropekv_attention_dims* d
  * FP16 once. out may be q itself. The call is two or three launches; the split of the
  * work follows from the sizes alone (pageTable's columns stand for the lengths: a table
  * much wider than kvLens costs time, not correctness), so equal calls give equal bits.
+ * The status is that of the launches. Waits inside the kernels are bounded; should one run
+ * out, which no argument makes it do, the rows concerned are NaN in out and lse.
  * Host errors: sizes negative, tokensPerPage <= 0, seqLen > 2^15, prefixLen >
  * maxPrefixPages * tokensPerPage, 2 * numPages * tokensPerPage >= 2^31,
  * prefixLen or maxPagesPerSeq * tokensPerPage > 2^30, or more than 2^30 query

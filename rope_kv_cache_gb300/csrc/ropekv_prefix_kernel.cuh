@@ -110,7 +110,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, int parity)
     return done != 0;
 }
 
-// Bounded wait, of a second at most; false, for the whole CTA, if it runs out.
+// Wait of at most 2^20 polls, each of which the hardware may suspend for a time of its own
+// choosing; false, for the whole CTA, if it runs out.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int* failed)
 {
     if (mbar_try(bar, parity))
