@@ -129,7 +129,12 @@ int team_size(int Hkv, int perSm)
 // takes the form that is best over calls three quarters of which fill half of their
 // tables and one quarter a twentieth, as a prefix on few SMs is long and short
 // sequences do not hide it (64 of 1 to 64 tokens in tables of 8192 behind 4096: 76 us
-// if only the former count, 36 us). Measured, one after the other against side by
+// if only the former count, 36 us). A table much wider than that misleads it towards one
+// range of the prefix, or towards the forms apart (real lengths as before, tables of 16384
+// and 131072 tokens instead of exact ones): 256 sequences behind 8192, FP16: 80 us, 92,
+// 92; 128 behind 4097, E4M3: 67, 79, 78; 61 x 7 rows behind 2000, INT8: 59, 73, 73; 40
+// behind 3001, 2 KV heads of 256: 21, 27, 58; 64 behind 4096 + 256, 2 KV heads of 128: 19,
+// 23, 46. Measured, one after the other against side by
 // side: 256 sequences of 1 to 512 tokens behind 8192, FP16: 89 against 79 us; 128 of
 // 1 to 2048 behind 4097, E4M3: 78 against 68; 61 x 7 rows behind 2000, INT8: 86
 // against 60; 40 of 1 to 900 behind 3001, D = 256: 32 against 22. The estimate keeps
@@ -188,6 +193,8 @@ Plan make_plan(const ropekv_attention_dims* d)
     // takes 8192 / D at a time, in about the time of a step: s = sqrt(n D / 8192) balances
     // the two (one sequence, one KV head, 14000 prefix tokens, INT8, D = 256: 27 us with
     // s = 1, 16 with 5; two sequences, four KV heads of 128, 6000 tokens: 12.6 and 12.7).
+    // That is the join of few rows; one of 4 * kSMs rows and more takes four partials at a
+    // time, but so many rows have steps enough that `most` decides.
     const long long longestSteps = std::max(p.tilesPrefix ? (long long)d->prefixLen / 16 : 0LL, own > 0 ? own / 16 : 0LL);
     const long long least = std::max(1LL, (long long)(sqrt((double)longestSteps * d->headDim / 8192) + 0.5));
     most = std::min(most, (steps + least - 1) / least);

@@ -256,11 +256,12 @@ __device__ __forceinline__ int swizzle(int r, int c)
 // ldmatrix delivers bytes (lane j: codes 4j..4j+3); Q's fragments follow it.
 //
 // What it measured (group of 4 rows, 8 KV heads, D = 128). FP16, 256 sequences of 1 to
-// 512 tokens: 6.3 to 6.9 TB/s alone on all SMs, which is the HBM's rate; on 88 SMs beside
-// a prefix 60 us, 4.5 TB/s, where an SM's 8 warps with three stages of 8 KB wait for
-// loads. 8-bit, 128 sequences of 1 to 2048: 4.8 to 5.5 TB/s alone: about 450 instructions
-// a step of 4 KB and warp (decoding, the transposes and the softmax of 16 tokens for 4 of
-// 8 columns) keep the ALU pipes 55 % busy.
+// 512 tokens: a call without a prefix (this kernel and the join) 51 us, 5.3 TB/s, against
+// 6.78 of a plain copy; on 88 SMs beside a prefix this kernel takes 60 us, 4.5 TB/s, where
+// an SM's 8 warps with three stages of 8 KB wait for loads. 8-bit, 128 sequences of 1 to
+// 2048: 57 us, 5.0 TB/s: about 450 instructions a step of 4 KB and warp (decoding, the
+// transposes and the softmax of 16 tokens for 4 of 8 columns) keep the ALU pipes 55 % and
+// the issue slots 51 % busy; neither is a limit, so latency is the rest of it.
 constexpr int kMaxParts = 32;    // prefix partials at most
 
 // Exponent of a V scale, kept where 2^(s - m) cannot leave FP32. Up to 2^60, the largest
