@@ -797,6 +797,14 @@ stream_kernel(const __grid_constant__ Args a)
 // (registers for that: with 64 a thread instead of 85 a call took 0.8 us longer). From
 // the last CTA before it to its own last: 3 us with few rows, 7 us for 8192 rows of 128
 // with three partials each (12 MB).
+// A weighted mean of FP16 values, before its rounding to FP16. The weights in O were rounded
+// to FP16, those in l were not, so that a mean of values at FP16's limit of 65504 can come
+// out by up to 2^-11 above it, where it would round to infinity.
+__device__ __forceinline__ float within_half(float x)
+{
+    return fabsf(x) > 65504.0f && fabsf(x) < 65504.0f * (1.0f + 1.0f / 1024) ? copysignf(65504.0f, x) : x;
+}
+
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(256, 3) join_kernel(const __grid_constant__ Args a, int tileShift)
 {
@@ -914,9 +922,12 @@ __global__ void __launch_bounds__(256, 3) join_kernel(const __grid_constant__ Ar
     const bool none = l == 0.0f;
     const float inv = none ? 0.0f : 1.0f / l;
     uint4 y = make_uint4(0, 0, 0, 0);
-    if (!none)
-        y = make_uint4(half2_bits(o[0] * inv, o[1] * inv), half2_bits(o[2] * inv, o[3] * inv),
-                       half2_bits(o[4] * inv, o[5] * inv), half2_bits(o[6] * inv, o[7] * inv));
+    if (!none) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            o[k] = within_half(o[k] * inv);
+        y = make_uint4(half2_bits(o[0], o[1]), half2_bits(o[2], o[3]), half2_bits(o[4], o[5]), half2_bits(o[6], o[7]));
+    }
     *reinterpret_cast<uint4*>(a.out + (size_t)hv * D + d) = y;
     if (d == 0 && a.lse != nullptr)
         a.lse[hv] = none ? -INFINITY : kLn2 * (m + log2f(l));
