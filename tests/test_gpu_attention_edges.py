@@ -95,12 +95,44 @@ def test_the_same_page_twice(B, fmt):
     run(c)
 
 
-@pytest.mark.parametrize("sm_scale", [1e-38, 1e-6, 40.0])
+@pytest.mark.parametrize("sm_scale", [0.0, -0.3, 1e-38, 1e-6, 40.0])
 @pytest.mark.parametrize("fmt", ALL)
 @pytest.mark.parametrize("B", [2, 30])
-def test_small_and_large_softmax_scales(B, fmt, sm_scale):
+def test_softmax_scales(B, fmt, sm_scale):
     c = AttentionCase(1050, B, 1, 8, 2, 64, 16, 50, [1 + 3 * i % 40 for i in range(B)], fmt)
     run(c, sm_scale=sm_scale)
+
+
+@pytest.mark.parametrize("P,Hq,Hkv,D", [(0, 1, 1, 64), (100, 2, 1, 64), (1000, 2, 2, 128)])
+def test_the_most_query_tokens(P, Hq, Hkv, D):
+    """2^15 query tokens of one sequence; every 911th row against a softmax in 64 bits."""
+    import rope_kv_cache_gb300 as rk
+    S, tpp = 1 << 15, 64
+    N = P + S
+    pages = -(-N // tpp)
+    gen = torch.Generator(device="cuda:0").manual_seed(P)
+    q = torch.randn(1, S, Hq, D, device="cuda:0", generator=gen).half()
+    pool = torch.randn(2, pages, tpp, Hkv, D, device="cuda:0", generator=gen).half()
+    ids = torch.randperm(pages, device="cuda:0", generator=gen).int()
+    table = torch.stack([ids, ids + pages]).contiguous()
+    out, lse = torch.empty_like(q), torch.empty(1, S, Hq, device="cuda:0")
+    rk.paged_attention_shared_prefix(q, pool, table[:, :-(-P // tpp)].contiguous() if P else None, P, table[None].contiguous(),
+                                     torch.tensor([N], dtype=torch.int32, device="cuda:0"), out, lse=lse)
+    k, v = (pool[p, ids.long()].reshape(-1, Hkv, D)[:N].double().repeat_interleave(Hq // Hkv, 1) for p in (0, 1))
+    for s in list(range(0, S, 911)) + [S - 1]:
+        n = P + s + 1
+        sc = torch.einsum("hd,nhd->hn", q[0, s].double(), k[:n]) * D ** -0.5
+        w = torch.softmax(sc, 1)
+        want = torch.einsum("hn,nhd->hd", w, v[:n])
+        wv = torch.einsum("hn,nhd->hd", w, v[:n].abs())
+        # as serving_plain derives it: scores, weights in FP16, FP32 sums of n terms, one FP16 rounding
+        ds = (D + 8) * 2.0 ** -23 * torch.einsum("hd,nhd->hn", q[0, s].double().abs(), k[:n].abs()).max() * D ** -0.5
+        rel = 2 * torch.expm1(ds) + 2.0 ** -11 + (2 * n + 40) * 2.0 ** -23
+        tol = rel * wv + 2.0 ** -11 * want.abs() + 2.0 ** -24 + 2.0 ** -24 * v.abs().max() * n / torch.exp(
+            torch.logsumexp(sc, 1) - sc.max(1).values)[:, None]
+        assert ((out[0, s].double() - want).abs() <= tol).all(), s
+        ref = torch.logsumexp(sc, 1)
+        assert ((lse[0, s].double() - ref).abs() <= ds + (n + 40) * 2.0 ** -23 + 2.0 ** -22 * ref.abs()).all(), s
 
 
 @pytest.mark.parametrize("fmt", ALL)
