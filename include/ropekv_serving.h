@@ -169,7 +169,7 @@ ROPEKV_API int64_t paged_attention_workspace_size(const ropekv_attention_dims* d
  * FP16 once. out may be q itself. The call is two or three launches; the split of the
  * work follows from the sizes alone (pageTable's columns stand for the lengths: a table
  * much wider than kvLens costs time, not correctness; 16384 to 131072 columns x tokens for
- * sequences of 3000 to 9000 took 1.2 to 2.7 times as long as exact tables), so equal calls
+ * sequences of 3000 to 9000 took up to 2.7 times as long as exact tables), so equal calls
  * give equal bits.
  * The status is that of the launches. Waits inside the kernels are bounded; should one run
  * out, which no argument makes it do, the rows concerned are NaN in out and lse.
