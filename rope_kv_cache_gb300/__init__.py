@@ -26,6 +26,19 @@ from ._binding import (  # noqa: F401
     rope_write_kv_tree,
     ropekv_status_string,
 )
+from ._sequence import (  # noqa: F401
+    kv_accept_drafts,
+    paged_kv_accept_drafts,
+    paged_kv_copy_pages,
+    paged_kv_fork,
+    paged_kv_fork_workspace_size,
+    paged_kv_free,
+    prompt_attention,
+    prompt_attention_workspace_size,
+    tree_attention,
+    tree_attention_workspace_size,
+    tree_mask_from_parents,
+)
 from ._serving import (  # noqa: F401
     load_serving_library,
     mrope_freq_axis,
@@ -46,4 +59,7 @@ __all__ = [
     "ropekv_set_residency_cap", "ropekv_floor_copy", "ropekv_status_string",
     "rope_write_kv_mrope", "mrope_freq_axis", "rope_write_kv_slot_mapping_quant", "paged_kv_read",
     "paged_attention_shared_prefix", "paged_attention_workspace_size", "load_serving_library",
+    "prompt_attention", "prompt_attention_workspace_size", "tree_attention", "tree_attention_workspace_size",
+    "tree_mask_from_parents", "kv_accept_drafts", "paged_kv_accept_drafts", "paged_kv_copy_pages",
+    "paged_kv_fork", "paged_kv_fork_workspace_size", "paged_kv_free",
 ]

@@ -31,6 +31,16 @@ class ropekv_attention_dims(ctypes.Structure):
         "maxPagesPerSeq", "prefixLen", "maxPrefixPages", "cacheFormat")]
 
 
+class ropekv_prompt_dims(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "numTokens", "numKVTokens", "batch", "numQHeads", "numKVHeads", "headDim")]
+
+
+class ropekv_tree_dims(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "batch", "seqLen", "numQHeads", "numKVHeads", "headDim", "kvCapacity")]
+
+
 def _require(path: str) -> str:
     if not os.path.exists(path):
         raise RuntimeError(
@@ -69,8 +79,25 @@ def load_serving_library():
         lib.paged_attention_workspace_size.argtypes = [D]
         lib.paged_attention_workspace_size.restype = I64
         lib.paged_attention_shared_prefix.argtypes = [P] * 9 + [I64, D, ctypes.c_float, P]
+        # include/ropekv_sequence.h
+        S = ctypes.POINTER(ropekv_prompt_dims)
+        lib.prompt_attention_workspace_size.argtypes = [S]
+        lib.prompt_attention_workspace_size.restype = I64
+        lib.prompt_attention.argtypes = [P, I64, P, I64, P, I64] + [P] * 5 + [I64, S, ctypes.c_float, P]
+        S = ctypes.POINTER(ropekv_tree_dims)
+        lib.tree_attention_workspace_size.argtypes = [S]
+        lib.tree_attention_workspace_size.restype = I64
+        lib.tree_attention.argtypes = [P] * 7 + [I64, S, ctypes.c_float, P]
+        lib.kv_accept_drafts.argtypes = [P] * 5 + [I32] * 6 + [P]
+        lib.paged_kv_accept_drafts.argtypes = [P] * 7 + [I32] * 9 + [P]
+        lib.paged_kv_copy_pages.argtypes = [P] * 4 + [I32] * 6 + [P]
+        lib.paged_kv_fork_workspace_size.argtypes = [I32, I32]
+        lib.paged_kv_fork_workspace_size.restype = I64
+        lib.paged_kv_fork.argtypes = [P] * 8 + [I64] + [I32] * 8 + [P]
+        lib.paged_kv_free.argtypes = [P] * 5 + [I32] * 5 + [P]
         for fn in ("rope_write_kv_mrope", "rope_write_kv_slot_mapping_quant", "paged_kv_read",
-                   "paged_attention_shared_prefix"):
+                   "paged_attention_shared_prefix", "prompt_attention", "tree_attention", "kv_accept_drafts",
+                   "paged_kv_accept_drafts", "paged_kv_copy_pages", "paged_kv_fork", "paged_kv_free"):
             getattr(lib, fn).restype = ctypes.c_int
         _lib = lib
     return _lib

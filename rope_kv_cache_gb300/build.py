@@ -1,5 +1,5 @@
 """Build libropekv.so (the C ABI and its sm_103a kernels) in-tree with nvcc,
-libropekv_serving.so (the serving operators around the paged cache) with
+libropekv_serving.so (the serving operators around the caches) with
 ropekv_bind-*.so, its Python module for torch tensors, and libropekv_floor.so, the
 copy kernel the benchmark times as the floor of a decode-sized launch.
 
@@ -28,13 +28,14 @@ SOURCES = [os.path.join(CSRC, "ropekv_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ropekv_kernels.cuh"), os.path.join(INCLUDE, "ropekv.h")]
 FLOOR_SOURCES = [os.path.join(CSRC, "ropekv_floor.cu")]
 FLOOR_DEPS = FLOOR_SOURCES + [os.path.join(INCLUDE, "ropekv_floor.h")]
-SERVING_SOURCES = [os.path.join(CSRC, "ropekv_serving.cu"),
-                   os.path.join(CSRC, "ropekv_attention.cu")]
+SERVING_SOURCES = [os.path.join(CSRC, n) for n in (
+    "ropekv_serving.cu", "ropekv_attention.cu", "ropekv_sequence.cu", "ropekv_pages.cu")]
+_SERVING_HEADERS = [os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h", "ropekv_sequence.h")]
 SERVING_DEPS = SERVING_SOURCES + [os.path.join(CSRC, n) for n in (
-    "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh", "ropekv_prefix_kernel.cuh")] + [
-    os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
+    "ropekv_kernels.cuh", "ropekv_attention_kernels.cuh", "ropekv_prefix_kernel.cuh",
+    "ropekv_rows_kernel.cuh")] + _SERVING_HEADERS
 BIND_SOURCE = os.path.join(CSRC, "ropekv_bind.cpp")
-BIND_DEPS = [BIND_SOURCE] + [os.path.join(INCLUDE, n) for n in ("ropekv.h", "ropekv_serving.h")]
+BIND_DEPS = [BIND_SOURCE] + _SERVING_HEADERS
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -1,5 +1,5 @@
-// ropekv_bind.cpp -- Python binding of libropekv_serving.so (include/ropekv_serving.h)
-// for torch tensors: checks type, device, layout and shape agreement, reads
+// ropekv_bind.cpp -- Python binding of libropekv_serving.so (include/ropekv_serving.h,
+// include/ropekv_sequence.h) for torch tensors: checks type, device, layout and shape agreement, reads
 // sizes and addresses, calls the C entry point on the current (or given) stream
 // and returns its status. It computes nothing. A module of its own, because the
 // checks of a call's ten tensors in Python take longer (20 us) than a decode-sized
@@ -15,6 +15,7 @@
 
 #include <string>
 
+#include "ropekv_sequence.h"
 #include "ropekv_serving.h"
 
 namespace {
@@ -359,6 +360,264 @@ int attention(PyObject* const* x)
     });
 }
 
+double scale_of(PyObject* o, int32_t D)
+{
+    if (o == Py_None)
+        return 1.0 / std::sqrt((double)D);
+    const double scale = PyFloat_AsDouble(o);
+    if (scale == -1.0 && PyErr_Occurred())
+        throw PythonError{};
+    return scale;
+}
+
+// A workspace of `size` bytes: the given one, or one of the stream's that is freed when
+// the call returns (reuse is ordered by the stream).
+struct Workspace {
+    at::Tensor own;
+    void* data = nullptr;
+    int64_t size = 0;
+    Workspace(const at::Tensor* given, int64_t need, at::Device dev, const c10::cuda::CUDAStream& st)
+    {
+        data = dense(given, "workspace", at::kByte, dev);
+        size = given ? given->numel() : need;
+        if (!given && need > 0) {
+            const c10::cuda::CUDAStreamGuard guard(st);
+            own = at::empty({need}, at::TensorOptions().dtype(at::kByte).device(dev));
+            data = own.data_ptr();
+        }
+    }
+};
+
+ropekv_prompt_dims prompt_dims(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v,
+                               const at::Tensor& qStarts, const at::Tensor* kvStarts)
+{
+    if (q.dim() != 3 || k.dim() != 3 || q.size(2) != k.size(2) || v.sizes() != k.sizes())
+        value_error("q [T,Hq,D] and k, v [Tk,Hkv,D] expected");
+    if (qStarts.dim() != 1 || qStarts.size(0) < 1 || (kvStarts && kvStarts->sizes() != qStarts.sizes()))
+        value_error("q_starts, kv_starts [B + 1] expected");
+    if (!kvStarts && q.size(0) != k.size(0))
+        value_error("kv_starts is needed where q and k differ in their numbers of tokens");
+    return {small(q.size(0), "T"), small(k.size(0), "Tk"), small(qStarts.size(0) - 1, "B"),
+            small(q.size(1), "Hq"), small(k.size(1), "Hkv"), small(q.size(2), "D")};
+}
+
+// prompt_workspace(q, k, v, q_starts, kv_starts)
+int64_t prompt_workspace(PyObject* const* x)
+{
+    const ropekv_prompt_dims d = prompt_dims(tensor(x[0], "q"), tensor(x[1], "k"), tensor(x[2], "v"),
+                                             tensor(x[3], "q_starts"), optional(x[4], "kv_starts"));
+    return prompt_attention_workspace_size(&d);
+}
+
+// prompt(q, k, v, q_starts, out, kv_starts, lse, sm_scale, workspace, stream)
+int prompt(PyObject* const* x)
+{
+    const at::Tensor &q = tensor(x[0], "q"), &k = tensor(x[1], "k"), &v = tensor(x[2], "v"),
+                     &qStarts = tensor(x[3], "q_starts"), &out = tensor(x[4], "out");
+    const at::Tensor *kvStarts = optional(x[5], "kv_starts"), *lse = optional(x[6], "lse"),
+                     *given = optional(x[8], "workspace");
+    const ropekv_prompt_dims d = prompt_dims(q, k, v, qStarts, kvStarts);
+    if (out.sizes() != q.sizes() || (lse && !is(*lse, {q.size(0), q.size(1)})))
+        value_error("out [T,Hq,D], lse [T,Hq] expected");
+    const double scale = scale_of(x[7], d.headDim);
+    const at::Device dev = q.device();
+    int64_t qs, ks, vs;
+    const uint16_t *qp = rows(q, "q", dev, qs), *kp = rows(k, "k", dev, ks), *vp = rows(v, "v", dev, vs);
+    const int32_t *qsp = dense<int32_t>(qStarts, "q_starts", at::kInt, dev),
+                  *ksp = dense<int32_t>(kvStarts, "kv_starts", at::kInt, dev);
+    uint16_t* op = dense<uint16_t>(out, "out", at::kHalf, dev);
+    float* ep = dense<float>(lse, "lse", at::kFloat, dev);
+    const auto st = stream_of(x[9], dev);
+    const int64_t need = prompt_attention_workspace_size(&d);
+    if (need < 0)
+        return (int)need;
+    const Workspace ws(given, need, dev, st);
+    return on_stream(dev, [&] {
+        return prompt_attention(qp, qs, kp, ks, vp, vs, qsp, ksp, op, ep, ws.data, ws.size, &d, (float)scale,
+                                st.stream());
+    });
+}
+
+ropekv_tree_dims tree_dims(const at::Tensor& q, const at::Tensor& cache)
+{
+    if (q.dim() != 4 || cache.dim() != 5 || cache.size(0) != q.size(0) || cache.size(1) != 2 ||
+        cache.size(4) != q.size(3))
+        value_error("q [B,S,Hq,D] and kv_cache [B,2,Hkv,cap,D] expected");
+    return {small(q.size(0), "B"), small(q.size(1), "S"), small(q.size(2), "Hq"), small(cache.size(2), "Hkv"),
+            small(q.size(3), "D"), small(cache.size(3), "cap")};
+}
+
+// tree_workspace(q, kv_cache)
+int64_t tree_workspace(PyObject* const* x)
+{
+    const ropekv_tree_dims d = tree_dims(tensor(x[0], "q"), tensor(x[1], "kv_cache"));
+    return tree_attention_workspace_size(&d);
+}
+
+// tree(q, kv_cache, kv_cache_end_lens, out, tree_mask, lse, sm_scale, workspace, stream)
+int tree(PyObject* const* x)
+{
+    const at::Tensor &q = tensor(x[0], "q"), &cache = tensor(x[1], "kv_cache"),
+                     &lens = tensor(x[2], "kv_cache_end_lens"), &out = tensor(x[3], "out");
+    const at::Tensor *mask = optional(x[4], "tree_mask"), *lse = optional(x[5], "lse"),
+                     *given = optional(x[7], "workspace");
+    const ropekv_tree_dims d = tree_dims(q, cache);
+    if (!is(lens, {d.batch}) || out.sizes() != q.sizes() || (lse && !is(*lse, {q.size(0), q.size(1), q.size(2)})))
+        value_error("kv_cache_end_lens [B], out [B,S,Hq,D], lse [B,S,Hq] expected");
+    if (mask && !is(*mask, {d.batch, d.seqLen, (d.seqLen + 31) / 32}))
+        value_error("tree_mask [B, S, ceil(S / 32)] expected");
+    const double scale = scale_of(x[6], d.headDim);
+    const at::Device dev = q.device();
+    const uint16_t *qp = dense<uint16_t>(q, "q", at::kHalf, dev), *cp = dense<uint16_t>(cache, "kv_cache", at::kHalf, dev);
+    const int32_t *lp = dense<int32_t>(lens, "kv_cache_end_lens", at::kInt, dev),
+                  *mp = dense<int32_t>(mask, "tree_mask", at::kInt, dev);
+    uint16_t* op = dense<uint16_t>(out, "out", at::kHalf, dev);
+    float* ep = dense<float>(lse, "lse", at::kFloat, dev);
+    const auto st = stream_of(x[8], dev);
+    const int64_t need = tree_attention_workspace_size(&d);
+    if (need < 0)
+        return (int)need;
+    const Workspace ws(given, need, dev, st);
+    return on_stream(dev, [&] {
+        return tree_attention(qp, cp, lp, mp, op, ep, ws.data, ws.size, &d, (float)scale, st.stream());
+    });
+}
+
+// accept(kv_cache, kv_cache_end_lens, seq_len, accepted, accepted_lens, end_lens_out, stream)
+int accept(PyObject* const* x)
+{
+    const at::Tensor &cache = tensor(x[0], "kv_cache"), &lens = tensor(x[1], "kv_cache_end_lens"),
+                     &acc = tensor(x[3], "accepted"), &accLens = tensor(x[4], "accepted_lens");
+    const at::Tensor* lensOut = optional(x[5], "end_lens_out");
+    if (cache.dim() != 5 || cache.size(1) != 2)
+        value_error("kv_cache [B,2,Hkv,cap,D] expected");
+    const int64_t B = cache.size(0);
+    if (!is(lens, {B}) || acc.dim() != 2 || acc.size(0) != B || !is(accLens, {B}) || (lensOut && !is(*lensOut, {B})))
+        value_error("kv_cache_end_lens [B], accepted [B,A], accepted_lens [B], end_lens_out [B] expected");
+    const int32_t S = whole(x[2], "seq_len"), A = small(acc.size(1), "A"), b = small(B, "B"),
+                  Hkv = small(cache.size(2), "Hkv"), cap = small(cache.size(3), "cap"), D = small(cache.size(4), "D");
+    const at::Device dev = cache.device();
+    uint16_t* cp = dense<uint16_t>(cache, "kv_cache", at::kHalf, dev);
+    const int32_t *lp = dense<int32_t>(lens, "kv_cache_end_lens", at::kInt, dev),
+                  *ap = dense<int32_t>(acc, "accepted", at::kInt, dev),
+                  *np = dense<int32_t>(accLens, "accepted_lens", at::kInt, dev);
+    int32_t* op = dense<int32_t>(lensOut, "end_lens_out", at::kInt, dev);
+    const auto st = stream_of(x[6], dev);
+    return on_stream(dev, [&] {
+        return kv_accept_drafts(cp, lp, ap, np, op, b, S, A, Hkv, D, cap, st.stream());
+    });
+}
+
+// paged_accept(kv_cache, page_table, kv_lens, seq_len, accepted, accepted_lens, kv_lens_out, kv_scales, stream)
+int paged_accept(PyObject* const* x)
+{
+    const at::Tensor &cache = tensor(x[0], "kv_cache"), &table = tensor(x[1], "page_table"),
+                     &lens = tensor(x[2], "kv_lens"), &acc = tensor(x[4], "accepted"),
+                     &accLens = tensor(x[5], "accepted_lens");
+    const at::Tensor *lensOut = optional(x[6], "kv_lens_out"), *scales = optional(x[7], "kv_scales");
+    const Pool p = check_pool(cache, scales, table);
+    if (!is(lens, {p.B}) || acc.dim() != 2 || acc.size(0) != p.B || !is(accLens, {p.B}) || (lensOut && !is(*lensOut, {p.B})))
+        value_error("kv_lens [B], accepted [B,A], accepted_lens [B], kv_lens_out [B] expected");
+    const int32_t S = whole(x[3], "seq_len"), A = small(acc.size(1), "A");
+    const at::Device dev = cache.device();
+    void* cp = dense(cache, "kv_cache", cache.scalar_type(), dev);
+    float* sp = dense<float>(scales, "kv_scales", at::kFloat, dev);
+    const int32_t *tp = dense<int32_t>(table, "page_table", at::kInt, dev),
+                  *lp = dense<int32_t>(lens, "kv_lens", at::kInt, dev),
+                  *ap = dense<int32_t>(acc, "accepted", at::kInt, dev),
+                  *np = dense<int32_t>(accLens, "accepted_lens", at::kInt, dev);
+    int32_t* op = dense<int32_t>(lensOut, "kv_lens_out", at::kInt, dev);
+    const auto st = stream_of(x[8], dev);
+    return on_stream(dev, [&] {
+        return paged_kv_accept_drafts(cp, sp, tp, lp, ap, np, op, p.B, S, A, p.Hkv, p.D, p.pages, p.M, p.tpp, p.fmt,
+                                      st.stream());
+    });
+}
+
+// A pool alone: as check_pool, without a page table.
+Pool check_pool(const at::Tensor& cache, const at::Tensor* scales)
+{
+    if (cache.dim() != 5 || cache.size(0) != 2)
+        value_error("kv_cache [2,P,TPP,Hkv,D] expected");
+    const int fmt = format_of(cache, "kv_cache", false);
+    if (fmt == ROPEKV_CACHE_F16 ? scales != nullptr
+                                : !scales || !is(*scales, {2, cache.size(1), cache.size(3), cache.size(2)}))
+        value_error(fmt == ROPEKV_CACHE_F16 ? "a float16 cache has no kv_scales"
+                                            : "kv_scales [2, P, Hkv, TPP] expected for an 8-bit cache");
+    return {small(cache.size(1), "P"), small(cache.size(2), "TPP"), small(cache.size(3), "Hkv"),
+            small(cache.size(4), "D"), fmt, 0, 0};
+}
+
+// copy_pages(kv_cache, src_pages, dst_pages, kv_scales, stream)
+int copy_pages(PyObject* const* x)
+{
+    const at::Tensor &cache = tensor(x[0], "kv_cache"), &src = tensor(x[1], "src_pages"), &dst = tensor(x[2], "dst_pages");
+    const at::Tensor* scales = optional(x[3], "kv_scales");
+    const Pool p = check_pool(cache, scales);
+    if (src.dim() != 1 || dst.sizes() != src.sizes())
+        value_error("src_pages, dst_pages [N] expected");
+    const at::Device dev = cache.device();
+    void* cp = dense(cache, "kv_cache", cache.scalar_type(), dev);
+    float* scp = dense<float>(scales, "kv_scales", at::kFloat, dev);
+    const int32_t *sp = dense<int32_t>(src, "src_pages", at::kInt, dev), *dp = dense<int32_t>(dst, "dst_pages", at::kInt, dev);
+    const int32_t n = small(src.size(0), "N");
+    const auto st = stream_of(x[4], dev);
+    return on_stream(dev, [&] {
+        return paged_kv_copy_pages(cp, scp, sp, dp, n, p.Hkv, p.D, p.pages, p.tpp, p.fmt, st.stream());
+    });
+}
+
+// fork(kv_cache, page_table, kv_lens, ref_counts, parents, children, kv_scales, workspace, stream)
+int fork(PyObject* const* x)
+{
+    const at::Tensor &cache = tensor(x[0], "kv_cache"), &table = tensor(x[1], "page_table"), &lens = tensor(x[2], "kv_lens"),
+                     &refs = tensor(x[3], "ref_counts"), &parents = tensor(x[4], "parents"),
+                     &children = tensor(x[5], "children");
+    const at::Tensor *scales = optional(x[6], "kv_scales"), *given = optional(x[7], "workspace");
+    const Pool p = check_pool(cache, scales, table);
+    if (!is(lens, {p.B}) || !is(refs, {p.pages}) || parents.dim() != 1 || children.sizes() != parents.sizes())
+        value_error("kv_lens [B], ref_counts [P], parents, children [N] expected");
+    const at::Device dev = cache.device();
+    void* cp = dense(cache, "kv_cache", cache.scalar_type(), dev);
+    float* scp = dense<float>(scales, "kv_scales", at::kFloat, dev);
+    int32_t *tp = dense<int32_t>(table, "page_table", at::kInt, dev), *lp = dense<int32_t>(lens, "kv_lens", at::kInt, dev),
+            *rp = dense<int32_t>(refs, "ref_counts", at::kInt, dev);
+    const int32_t *pp = dense<int32_t>(parents, "parents", at::kInt, dev),
+                  *chp = dense<int32_t>(children, "children", at::kInt, dev);
+    const int32_t n = small(parents.size(0), "N");
+    const auto st = stream_of(x[8], dev);
+    const int64_t need = paged_kv_fork_workspace_size(n, p.B);
+    if (need < 0)
+        return (int)need;
+    const Workspace ws(given, need, dev, st);
+    return on_stream(dev, [&] {
+        return paged_kv_fork(cp, scp, tp, lp, rp, pp, chp, ws.data, ws.size, n, p.B, p.Hkv, p.D, p.pages, p.M, p.tpp,
+                             p.fmt, st.stream());
+    });
+}
+
+// release(page_table, kv_lens, ref_counts, sequences, tokens_per_page, keep_lens, stream)
+int release(PyObject* const* x)
+{
+    const at::Tensor &table = tensor(x[0], "page_table"), &lens = tensor(x[1], "kv_lens"), &refs = tensor(x[2], "ref_counts"),
+                     &seqs = tensor(x[3], "sequences");
+    const at::Tensor* keep = optional(x[5], "keep_lens");
+    if (table.dim() != 3 || table.size(1) != 2 || !is(lens, {table.size(0)}) || refs.dim() != 1)
+        value_error("page_table [B,2,M], kv_lens [B], ref_counts [P] expected");
+    if (seqs.dim() != 1 || (keep && keep->sizes() != seqs.sizes()))
+        value_error("sequences, keep_lens [N] expected");
+    const at::Device dev = table.device();
+    int32_t *tp = dense<int32_t>(table, "page_table", at::kInt, dev), *lp = dense<int32_t>(lens, "kv_lens", at::kInt, dev),
+            *rp = dense<int32_t>(refs, "ref_counts", at::kInt, dev);
+    const int32_t *sp = dense<int32_t>(seqs, "sequences", at::kInt, dev), *kp = dense<int32_t>(keep, "keep_lens", at::kInt, dev);
+    const int32_t n = small(seqs.size(0), "N"), B = small(table.size(0), "B"), M = small(table.size(2), "M"),
+                  P = small(refs.size(0), "P"), tpp = whole(x[4], "tokens_per_page");
+    const auto st = stream_of(x[6], dev);
+    return on_stream(dev, [&] {
+        return paged_kv_free(tp, lp, rp, sp, kp, n, B, P, M, tpp, st.stream());
+    });
+}
+
 template <typename R, R (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
@@ -389,6 +648,15 @@ PyMethodDef kMethods[] = {
     method<int, read, 8>("read"),
     method<int, attention, 12>("attention"),
     method<int64_t, attention_workspace, 6>("attention_workspace"),
+    method<int, prompt, 10>("prompt"),
+    method<int64_t, prompt_workspace, 5>("prompt_workspace"),
+    method<int, tree, 9>("tree"),
+    method<int64_t, tree_workspace, 2>("tree_workspace"),
+    method<int, accept, 7>("accept"),
+    method<int, paged_accept, 9>("paged_accept"),
+    method<int, copy_pages, 5>("copy_pages"),
+    method<int, fork, 9>("fork"),
+    method<int, release, 7>("release"),
     {nullptr, nullptr, 0, nullptr},
 };
 
