@@ -13,18 +13,29 @@
 //
 //   warps 0 .. 4 MT - 1   softmax: a thread owns one row, which is one TMEM lane; S
 //                         comes by tcgen05.ld, the weights go back by tcgen05.st over
-//                         the columns of S that they were made from
+//                         the columns of S that they were made from, in two halves
 //   warp 4 MT             fetches by TMA: Q once, then a ring of K and V tiles in the
 //                         order in which the products want them
 //   warp 4 MT + 1         issues all products: S = Q K^T from shared memory, O += P V with
 //                         P in TMEM and V as it lies in memory (N-major); V rows behind a
 //                         sequence's last key it makes zeros first, whatever they hold (0
 //                         times infinity or NaN would not be 0)
-//   warp 4 MT + 2         allocates TMEM
+//   warp 4 MT + 2         allocates TMEM, then cuts the CTA's share into segments
 //
 // With two row tiles one tile's products run while the other's softmax works; with one
 // the scores run ahead by kSlots tiles. The products of a CTA are issued by one thread
 // and run in that order, so S may be put over weights that an earlier product reads.
+//
+// Work. A unit is MT row tiles of one sequence and head group with the K/V tiles that
+// they see, its steps. All steps of all units form one sequence, of which every CTA takes an
+// equal share whatever the lengths, so that few rows behind long contexts and many short
+// prompts fill the SMs alike (lengths are on the device, so each CTA sums them first). A share
+// covers the end of a unit, whole units, the start of another: its segments. A whole unit's
+// rows go to out; a piece's to a slot of the workspace (O / l, m + log2 l), which no
+// other piece has: 2 c for the piece of CTA c that continues a unit, 2 c + 1 for one that
+// begins it; the join kernel reads them in order. Between segments nothing drains but
+// the softmax warps' own last products: K and V of the next are on their way. What such a
+// change costs counts as kSwitch steps at the head of every unit.
 //
 // m moves only when a row's scores exceed it by more than 8 (2^8 stays far inside FP16
 // and FP32), in which case the row's O is rescaled in TMEM; the first tile sets it.
@@ -57,8 +68,9 @@ struct RowsArgs {
     const int32_t* kvStarts;
     const int32_t* endLens;    // [B] (tree)
     const int32_t* treeMask;   // [B, S, W] or NULL
-    float* partO;              // [parts, T * Hq, D]
-    float* partL;              // [parts, T * Hq]
+    float* partO;              // [2 ctas, D / 4, 128 MT, 4] pieces of units
+    float* partL;              // [2 ctas, 128 MT]
+    struct Joint* joints;      // [ctas] the unit that CTA c begins and others end
     int64_t qStride, kTok, vTok, kvHead, kvBatch;
     float scaleLog2;
     int32_t T, Tk, B, S, W, cap, Hq;
@@ -66,9 +78,49 @@ struct RowsArgs {
     int32_t heads;             // Hq / G
     int32_t headsPerKv;        // heads / Hkv
     int32_t tokens;            // tokens of a CTA's tiles: 128 MT / G
-    int32_t parts, tilesSeq;
+    int32_t tilesSeq;          // tree: units of a sequence and head group
+    int32_t ctas;
+    int32_t whole;             // units are not split: each goes to the CTA in whose share it begins
+    int32_t leastShare;        // steps of a share, at least
     Divisor divG;
 };
+
+struct Joint {
+    int qRow, tok0, nq, head;
+    int pieces;                // 0: nothing to join
+};
+
+// Steps that changing from one unit to the next costs.
+constexpr int kSwitch = 2;
+
+// A sequence as the kernel sees it.
+struct Sequence {
+    int b;
+    int nq;                    // its query tokens
+    int qRow;                  // row of its token 0 in q
+    int kvRow;                 // its key 0 along the token axis of k and v
+    int base;                  // keys before its token 0 (prompt: nk - nq, tree: end - S)
+    int nk;                    // its keys
+    int units;                 // of each head group
+};
+
+// MT row tiles of a sequence and head group, and a range of K/V tiles.
+struct Segment : Sequence {
+    int head;                  // head group: heads head * G ..; below 0: the end
+    int tok0;                  // first token of the tiles
+    int j0, j1;                // K/V tiles
+    int slot;                  // of the workspace; below 0: the whole unit
+};
+
+// Where a CTA's share begins.
+struct Start {
+    long long at, end;         // first step and the one behind the last, of all steps
+    long long share;
+    long long inside;          // steps of sequence b before `at`
+    int b;                     // a.B: no work
+};
+
+constexpr int kSegments = 4;   // that are known ahead
 
 template <int D, int MT>
 struct RowsConfig {
@@ -81,27 +133,19 @@ struct RowsConfig {
     static constexpr int kThreads = kSoftmax + 128;
     static constexpr int kColO = MT * kSlots * kTile;
     static constexpr int kCols = 512;
-    // barriers: full, empty of the stages; S full, P full, O done of the slots (a wait tells
-    // only the last two phases of a barrier apart, and O(j - kSlots) is done when S(j) is); O
-    // free of the row tiles; Q full, Q free
-    static constexpr int kBars = 2 * kStages + 3 * MT * kSlots + MT + 2;
+    // barriers: full, empty of the stages; S full, the two halves of P, O done of the slots (a
+    // wait tells only the last two phases of a barrier apart, and O(j - kSlots) is done when S(j)
+    // is); Q full, Q free; full, free of the segments
+    static constexpr int kBars = 2 * kStages + 4 * MT * kSlots + 2 + 2 * kSegments;
     static constexpr int kOffRing = kQBytes;
     static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
-    static constexpr int kSmem = kOffBar + kBars * 8 + 64 + 1024;
+    static constexpr int kOffSegs = (kOffBar + kBars * 8 + 15) / 16 * 16;
+    static constexpr int kOffStart = kOffSegs + kSegments * (int)sizeof(Segment);
+    static constexpr int kOffSums = (kOffStart + (int)sizeof(Start) + 15) / 16 * 16;
+    static constexpr int kOffFlags = kOffSums + kThreads / 32 * 8;
+    static constexpr int kSmem = kOffFlags + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kColO + MT * D <= kCols, "TMEM");
-};
-
-// One piece of work: MT row tiles of a sequence and head group, and a range of K/V tiles.
-struct Segment {
-    int b, head;               // sequence; head group (heads head * G ..)
-    int tok0, nq;              // first token of the tiles in the sequence; its tokens
-    int qRow;                  // row of its token 0 in q
-    int kvRow;                 // its key 0 along the token axis of k and v
-    int base;                  // keys before its token 0 (prompt: nk - nq, tree: end - S)
-    int nk;                    // its keys
-    int j0, j1;                // K/V tiles
-    int part;
 };
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar)
@@ -151,19 +195,51 @@ __device__ __forceinline__ uint32_t sees32(const RowsArgs& a, const int32_t* wor
     return bits;
 }
 
-// A row of O / l from the segment's tokens that the row sees, in FP32 throughout.
-template <int D>
-__device__ __noinline__ void plain_row(const RowsArgs& a, const Segment& s, const uint16_t* q, int token, int end,
-                                       float m, float l, float* o)
+__device__ __forceinline__ void tmem_load16(float* f, uint32_t addr)
 {
+    uint32_t* r = reinterpret_cast<uint32_t*>(f);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void pin16(float* f)
+{
+    asm volatile(""
+        : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
+          "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]));
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(addr),
+           "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// A row of O / l from the segment's tokens that the row sees, in FP32 throughout, in place of
+// what the products made of it.
+template <int D, int MT>
+__device__ __noinline__ void plain_row(const RowsArgs& a, const Segment& s, int token, int at, int row, float m, float l)
+{
+    constexpr int TN = RowsConfig<D, MT>::kTile;
     const int kvHead = s.head / a.headsPerKv;
-    const int lo = s.j0 * RowsConfig<D, 1>::kTile, limit = min(row_limit(a, s, token), end);
+    const int limit = min(row_limit(a, s, token), s.j1 * TN);
     const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)s.b * a.S + token) * a.W : nullptr;
+    const uint16_t* q = a.q + (size_t)(s.qRow + token) * a.qStride + (size_t)(at % a.Hq) * D;
     const uint16_t* kBase = a.k + (size_t)s.b * a.kvBatch + (size_t)kvHead * a.kvHead;
     const uint16_t* vBase = a.v + (size_t)s.b * a.kvBatch + (size_t)kvHead * a.kvHead;
+    float o[D];
+#pragma unroll 1
     for (int d = 0; d < D; ++d)
         o[d] = 0.0f;
-    for (int t = lo; t < limit; ++t) {
+#pragma unroll 1
+    for (int t = s.j0 * TN; t < limit; ++t) {
         if (words != nullptr && !(sees32(a, words, s.base, limit, t) & 1))
             continue;
         const uint4* kr = reinterpret_cast<const uint4*>(kBase + (size_t)(s.kvRow + t) * a.kTok);
@@ -182,6 +258,7 @@ __device__ __noinline__ void plain_row(const RowsArgs& a, const Segment& s, cons
         }
         const float p = exp2_fast(dot * a.scaleLog2 - m) / l;
         const uint4* vr = reinterpret_cast<const uint4*>(vBase + (size_t)(s.kvRow + t) * a.vTok);
+#pragma unroll 1
         for (int x = 0; x < D / 8; ++x) {
             uint4 vw = vr[x];
             const __half2* vh = reinterpret_cast<const __half2*>(&vw);
@@ -193,69 +270,171 @@ __device__ __noinline__ void plain_row(const RowsArgs& a, const Segment& s, cons
             }
         }
     }
+    if (s.slot >= 0) {
+#pragma unroll 1
+        for (int d = 0; d < D; ++d)
+            a.partO[(((size_t)s.slot * (D / 4) + d / 4) * (MT * 128) + row) * 4 + d % 4] = o[d];
+    } else {
+#pragma unroll 1
+        for (int d = 0; d < D; d += 2)
+            *reinterpret_cast<uint32_t*>(a.out + (size_t)at * D + d) = half2_bits(within_half(o[d]), within_half(o[d + 1]));
+    }
 }
 
-// The work of CTA `index`, found by one warp; false where there is none.
-template <int D, int MT, bool TREE>
-__device__ __forceinline__ bool find_segment(const RowsArgs& a, int index, Segment& s)
+template <bool TREE>
+__device__ __forceinline__ Sequence sequence(const RowsArgs& a, int b)
 {
-    constexpr int TN = RowsConfig<D, MT>::kTile;
-    const int lane = threadIdx.x & 31;
-    s.part = index % a.parts;
-    index /= a.parts;
-    s.head = index % a.heads;
-    int tile = index / a.heads;
+    Sequence s;
+    s.b = b;
     if (TREE) {
-        s.b = tile / a.tilesSeq;
-        tile -= s.b * a.tilesSeq;
-        const int end = a.endLens[s.b];
+        const int end = a.endLens[b];
         s.nq = a.S;
-        s.qRow = s.b * a.S;
+        s.qRow = b * a.S;
         s.kvRow = 0;
-        s.base = end - a.S;
+        s.base = end < -(1 << 30) ? -(1 << 30) : end - a.S;
         s.nk = max(0, min(end, a.cap));
+        s.units = a.tilesSeq;
     } else {
-        // prefix sums of the sequences' tiles, 32 sequences at a time
-        s.b = -1;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int b = b0 + lane;
-            int lo = 0, hi = 0;
-            if (b < a.B) {
-                lo = max(0, min(a.T, a.qStarts[b]));
-                hi = max(lo, min(a.T, a.qStarts[b + 1]));
-            }
-            const int tiles = (hi - lo + a.tokens - 1) / a.tokens;
-            int sum = tiles;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, sum, d);
-                sum += lane >= d ? y : 0;
-            }
-            const uint32_t past = __ballot_sync(0xffffffffu, tile < sum);
-            if (past != 0) {
-                const int src = __ffs(past) - 1;
-                const int before = __shfl_sync(0xffffffffu, sum - tiles, src);
-                s.b = b0 + src;
-                s.qRow = __shfl_sync(0xffffffffu, lo, src);
-                s.nq = __shfl_sync(0xffffffffu, hi - lo, src);
-                // the last tiles, which see most, first
-                tile = __shfl_sync(0xffffffffu, tiles, src) - 1 - (tile - before);
-                break;
-            }
-            tile -= __shfl_sync(0xffffffffu, sum, 31);
-        }
-        if (s.b < 0)
-            return false;
-        s.kvRow = max(0, min(a.Tk, a.kvStarts[s.b]));
-        s.nk = max(0, min(a.Tk, a.kvStarts[s.b + 1]) - s.kvRow);
+        s.qRow = max(0, min(a.T, a.qStarts[b]));
+        s.nq = max(0, min(a.T, a.qStarts[b + 1]) - s.qRow);
+        s.kvRow = max(0, min(a.Tk, a.kvStarts[b]));
+        s.nk = max(0, min(a.Tk, a.kvStarts[b + 1]) - s.kvRow);
         s.base = s.nk - s.nq;
+        s.units = (s.nq + a.tokens - 1) / a.tokens;
     }
-    s.tok0 = tile * a.tokens;
-    const int tiles = (tile_limit(a, s.nq, s.base, s.nk, s.tok0) + TN - 1) / TN;
-    const int per = (tiles + a.parts - 1) / a.parts;
-    s.j0 = min(tiles, s.part * per);
-    s.j1 = min(tiles, s.j0 + per);
-    return true;
+    return s;
+}
+
+// K/V tiles that the sequence's unit u sees.
+template <int TN>
+__device__ __forceinline__ int tiles_of(const RowsArgs& a, const Sequence& s, int u)
+{
+    return (tile_limit(a, s.nq, s.base, s.nk, u * a.tokens) + TN - 1) / TN;
+}
+
+// sum of floor((a i + b) / m) over 0 <= i < n, all non-negative, by Euclid's steps on (a, m).
+__device__ inline long long floor_sum(long long n, long long m, long long a, long long b)
+{
+    long long sum = 0;
+    while (n > 0) {
+        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+// Steps of a head group's units before unit u, with their changes; a unit has one at least.
+template <int TN, bool TREE>
+__device__ __forceinline__ long long steps_before(const RowsArgs& a, const Sequence& s, int u)
+{
+    if (TREE && a.treeMask != nullptr)
+        return (long long)u * (kSwitch + max(1, tiles_of<TN>(a, s, 0)));
+    // all but the last unit see base + (i + 1) tokens keys (at most nk of a tree's): one step as
+    // long as that is at most TN, then its quotient rounded up
+    if (u <= 0)
+        return 0;
+    const int last = s.units - 1, n = min(u, last);
+    long long sum = (long long)u * kSwitch + (u > last ? max(1, tiles_of<TN>(a, s, last)) : 0);
+    if (n <= 0)
+        return sum;
+    const long long first = (long long)s.base + a.tokens + TN - 1;        // floor(first / TN) tiles of unit 0
+    int ones = first >= 2 * TN ? 0 : (int)min((long long)n, (2 * TN - first + a.tokens - 1) / a.tokens);
+    // a tree's units behind the cache's end see nk
+    int full = n;
+    if (TREE && (long long)s.base + (long long)n * a.tokens > s.nk) {
+        full = s.nk <= s.base ? 0 : (int)min((long long)n, ((long long)s.nk - s.base) / a.tokens);
+        ones = min(ones, full);
+        sum += (long long)(n - full) * max(1, (s.nk + TN - 1) / TN);
+    }
+    return sum + ones + floor_sum(full - ones, TN, a.tokens, first + (long long)ones * a.tokens);
+}
+
+template <int D, int MT, bool TREE>
+__device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, Start* out)
+{
+    constexpr int TN = RowsConfig<D, MT>::kTile, kThreads = RowsConfig<D, MT>::kThreads, kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    auto work = [&](int b) -> long long {
+        const Sequence s = sequence<TREE>(a, b);
+        return a.heads * steps_before<TN, TREE>(a, s, s.units);
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += work(b);
+    long long sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+        sum += lane >= d ? y : 0;
+    }
+    if (lane == 31)
+        sums[warp] = sum;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? sums[w] : 0;
+        total += sums[w];
+    }
+    before += sum - mine;
+    const long long share = max((long long)a.leastShare, (total + a.ctas - 1) / a.ctas);
+    const long long at = share * blockIdx.x;
+    if (threadIdx.x == 0 && at >= total)
+        *out = {at, at, share, 0, a.B};
+    if (mine > 0 && at >= before && at < before + mine) {
+        int b = b0;
+        long long n = work(b);
+        while (at >= before + n) {
+            before += n;
+            n = work(++b);
+        }
+        *out = {at, min(total, at + share), share, at - before, b};
+    }
+}
+
+// The softmax warps, which hold kTile scores a thread, take registers of the others: 256 x 208 +
+// 128 x 88 are the 384 x 168 of the launch with two row tiles.
+template <int MT>
+__device__ __forceinline__ void few_registers()
+{
+    if constexpr (MT == 2)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
+
+template <int MT>
+__device__ __forceinline__ void more_registers()
+{
+    if constexpr (MT == 2)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// d = a * b of two values; FP16 of two, infinities and values past its range as +-65504.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float b)
+{
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1) : "f"(b));
+}
+
+__device__ __forceinline__ uint32_t half2_sat(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
 template <int D, int MT, bool TREE>
@@ -265,20 +444,19 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
 {
     using C = RowsConfig<D, MT>;
     constexpr int TN = C::kTile, NS = C::kStages, SL = C::kSlots, LA = SL;
-    extern __shared__ uint8_t smemRaw[];
-    __shared__ Segment shared;
-    __shared__ int haveWork;
-    const uint32_t rawAddr = smem_u32(smemRaw);
-    const uint32_t base = (rawAddr + 1023u) & ~1023u;
-    uint8_t* smem = smemRaw + (base - rawAddr);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    Segment* ring = reinterpret_cast<Segment*>(smem + C::kOffSegs);
+    Start& start = *reinterpret_cast<Start*>(smem + C::kOffStart);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kLoad = 4 * MT, kMma = kLoad + 1, kAlloc = kLoad + 2;
 
     const uint32_t bars = base + C::kOffBar;
     const uint32_t full = bars, empty = full + NS * 8, sFull = empty + NS * 8, pFull = sFull + MT * SL * 8,
-                   oDone = pFull + MT * SL * 8, oFree = oDone + MT * SL * 8, qFull = oFree + MT * 8, qFree = qFull + 8;
-    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffBar + C::kBars * 8);
-    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + C::kBars * 8 + 8);
+                   oDone = pFull + 2 * MT * SL * 8, qFull = oDone + MT * SL * 8, qFree = qFull + 8, segFull = qFree + 8,
+                   segFree = segFull + kSegments * 8;
+    volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffFlags);
+    uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffFlags + 8);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -287,14 +465,17 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         }
         for (int i = 0; i < MT * SL; ++i) {
             mbar_init(sFull + 8 * i, 1);
-            mbar_init(pFull + 8 * i, 128);
+            mbar_init(pFull + 16 * i, 4);
+            mbar_init(pFull + 16 * i + 8, 4);
             mbar_init(oDone + 8 * i, 1);
         }
-        for (int i = 0; i < MT; ++i)
-            mbar_init(oFree + 8 * i, 128);
         mbar_init(qFull, 1);
         mbar_init(qFree, 1);
-        *failed = 0;
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(segFull + 8 * i, 1);
+            mbar_init(segFree + 8 * i, 4 * MT + 2);
+        }
+        *failed = base & 1023;      // tiles of 1024 bytes: 0
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kAlloc) {
@@ -302,74 +483,85 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                      :: "r"(smem_u32(tmemSlot)), "n"(C::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == kLoad) {
-        Segment s;
-        const bool found = find_segment<D, MT, TREE>(a, blockIdx.x, s);
-        if (lane == 0) {
-            shared = s;
-            haveWork = found;
-        }
-    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    find_start<D, MT, TREE>(a, reinterpret_cast<long long*>(smem + C::kOffSums), &start);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = *tmemSlot;
-    const Segment seg = shared;
-    const bool work = haveWork != 0;
-    const int J = work ? seg.j1 - seg.j0 : 0;
-    const int look = min(LA, J);
-    // the last tile has V rows behind the sequence's last key
-    const bool tail = J > 0 && seg.j1 * TN > seg.nk;
+    // The segments, in order, for every warp that works on them; false at the end.
+    int segments = 0;
+    auto next = [&](Segment& s) -> bool {
+        const int i = segments % kSegments;
+        if (!mbar_wait_warp(segFull + 8 * i, (segments / kSegments) & 1, failed))
+            return false;
+        s = ring[i];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(segFree + 8 * i);
+        ++segments;
+        return s.head >= 0;
+    };
 
     if (warp == kLoad) {
         // --------------------------------------------------------------- TMA
-        bool ok = J > 0;
-        int n = 0;                                  // loads of K and V so far
-        const int kvHead = seg.head / a.headsPerKv;
-        auto load = [&](const CUtensorMap* map, int j) {
-            const int st = n % NS;
-            ok = ok && (n < NS || mbar_wait_warp(empty + 8 * st, (n / NS - 1) & 1, failed));
+        few_registers<MT>();
+        bool ok = true;
+        int n = 0, nq = 0;                          // loads of K and V, of Q so far
+        Segment seg;
+        while (ok && next(seg)) {
+            const int J = seg.j1 - seg.j0, look = min(LA, J), kvHead = seg.head / a.headsPerKv;
+            if (J == 0)
+                continue;
+            auto load = [&](const CUtensorMap* map, int j) {
+                const int st = n % NS;
+                ok = ok && (n < NS || mbar_wait_warp(empty + 8 * st, (n / NS - 1) & 1, failed));
+                if (ok && elect_one()) {
+                    mbar_expect(full + 8 * st, C::kTileBytes);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load(base + C::kOffRing + st * C::kTileBytes + x * (TN * 128), map, x * 64,
+                                 seg.kvRow + (seg.j0 + j) * TN, kvHead, TREE ? seg.b : 0, full + 8 * st);
+                }
+                __syncwarp();
+                n += ok;
+            };
+            // the scores of the segment before have read its Q
+            ok = nq == 0 || mbar_wait_warp(qFree, (nq - 1) & 1, failed);
             if (ok && elect_one()) {
-                mbar_expect(full + 8 * st, C::kTileBytes);
+                mbar_expect(qFull, (uint32_t)(a.G * a.tokens * D * 2));
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
-                    tma_load(base + C::kOffRing + st * C::kTileBytes + x * (TN * 128), map, x * 64,
-                             seg.kvRow + (seg.j0 + j) * TN, kvHead, TREE ? seg.b : 0, full + 8 * st);
+                    tma_load(base + x * (MT * 128 * 128), &mapQ, x * 64, 0, seg.qRow + seg.tok0, seg.head, qFull);
             }
             __syncwarp();
-            n += ok;
-        };
-        if (ok && elect_one()) {
-            mbar_expect(qFull, (uint32_t)(a.G * a.tokens * D * 2));
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-                tma_load(base + x * (MT * 128 * 128), &mapQ, x * 64, 0, seg.qRow + seg.tok0, seg.head, qFull);
+            nq += ok;
+            for (int j = 0; ok && j < look; ++j)
+                load(&mapK, j);
+            for (int j = 0; ok && j < J; ++j) {
+                load(&mapV, j);
+                if (j + LA < J)
+                    load(&mapK, j + LA);
+            }
         }
-        __syncwarp();
-        for (int j = 0; ok && j < look; ++j)
-            load(&mapK, j);
-        for (int j = 0; ok && j < J; ++j) {
-            load(&mapV, j);
-            if (j + LA < J)
-                load(&mapK, j + LA);
-        }
-        if (J > 0)
-            mbar_drain(qFull, 0);
+        if (nq > 0)
+            mbar_drain(qFull, (nq - 1) & 1);
         for (int i = n > NS ? n - NS : 0; i < n; ++i)
             mbar_drain(full + 8 * (i % NS), (i / NS) & 1);
     } else if (warp == kMma) {
         // ---------------------------------------------------------- products
+        few_registers<MT>();
         constexpr uint32_t kindS = mma_desc(TN, false), kindO = mma_desc(D, true);
-        bool ok = J > 0 && mbar_wait_warp(qFull, 0, failed);
-        int n = 0;
+        bool ok = true;
+        int n = 0, nq = 0, items = 0;               // loads taken, Q taken, items of a row tile before this segment
         auto acquire = [&]() -> int {
             const int st = n % NS;
             ok = ok && mbar_wait_warp(full + 8 * st, (n / NS) & 1, failed);
             ++n;
             return st;
         };
-        auto scores = [&](int st, int tile, int j) {
-            const int slot = tile * SL + j % SL;
+        auto scores = [&](int st, int tile, int item) {
+            const int slot = tile * SL + item % SL;
             if (ok && elect_one()) {
                 tmem_fence_after();
                 const uint32_t qd = desc_low(base + tile * (128 * 128), 16);
@@ -383,243 +575,357 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             }
             __syncwarp();
         };
-        auto release = [&](int st) {
+        auto commit = [&](uint32_t bar) {
             if (ok && elect_one())
-                mma_commit(empty + 8 * st);
+                mma_commit(bar);
             __syncwarp();
         };
-        for (int j = 0; ok && j < look; ++j) {
-            const int st = acquire();
-            for (int tile = 0; tile < MT; ++tile)
-                scores(st, tile, j);
-            release(st);
-        }
-        for (int j = 0; ok && j < J; ++j) {
-            const int sv = acquire();
-            if (ok && tail && j == J - 1) {
-                // V rows behind the sequence's last key become zeros, while its softmax works
-                const int keep = seg.nk - (seg.j1 - 1) * TN;     // rows that are keys, 0 < keep < TN
-                uint8_t* v = smem + C::kOffRing + sv * C::kTileBytes;
-                const int perBlock = (TN - keep) * 8;
-                for (int x = lane; x < (D / 64) * perBlock; x += 32) {
-                    const int blk = x / perBlock, y = x - blk * perBlock;
-                    *reinterpret_cast<uint4*>(v + blk * (TN * 128) + keep * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_async_smem();
-                __syncwarp();
+        Segment seg;
+        while (ok && next(seg)) {
+            const int J = seg.j1 - seg.j0, look = min(LA, J);
+            if (J == 0)
+                continue;
+            ok = mbar_wait_warp(qFull, nq & 1, failed);
+            ++nq;
+            for (int j = 0; ok && j < look; ++j) {
+                const int st = acquire();
+                for (int tile = 0; tile < MT; ++tile)
+                    scores(st, tile, items + j);
+                commit(empty + 8 * st);
             }
-            int sk = 0;
-            for (int tile = 0; tile < MT; ++tile) {
-                const int slot = tile * SL + j % SL;
-                ok = ok && mbar_wait_warp(pFull + 8 * slot, (j / SL) & 1, failed);
-                if (ok && elect_one()) {
-                    tmem_fence_after();
+            if (look == J)
+                commit(qFree);
+            for (int j = 0; ok && j < J; ++j) {
+                const int sv = acquire(), item = items + j;
+                if (ok && j == J - 1 && seg.j1 * TN > seg.nk) {
+                    // V rows behind the sequence's last key become zeros, while its softmax works
+                    const int keep = seg.nk - (seg.j1 - 1) * TN;     // rows that are keys, 0 < keep < TN
+                    uint8_t* v = smem + C::kOffRing + sv * C::kTileBytes;
+                    const int perBlock = (TN - keep) * 8;
+                    for (int x = lane; x < (D / 64) * perBlock; x += 32) {
+                        const int blk = x / perBlock, y = x - blk * perBlock;
+                        *reinterpret_cast<uint4*>(v + blk * (TN * 128) + keep * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                int sk = 0;
+                for (int tile = 0; tile < MT; ++tile) {
+                    // the weights; with them the rows of the segment before have left O
+                    const int slot = tile * SL + item % SL;
                     const uint32_t vd = desc_low(base + C::kOffRing + sv * C::kTileBytes, TN * 128);
                     const uint32_t to = tmem + C::kColO + tile * D, from = tmem + slot * TN;
 #pragma unroll
-                    for (int k = 0; k < TN / 16; ++k)
-                        mma_ts(to, from + k * 8, desc(vd + k * (2048 / 16)), kindO, j > 0 || k > 0);
-                    mma_commit(oDone + 8 * slot);
-                }
-                __syncwarp();
-                if (tile == MT - 1)
-                    release(sv);
-                if (j + LA < J) {
-                    if (tile == 0)
-                        sk = acquire();
-                    scores(sk, tile, j + LA);
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && mbar_wait_warp(pFull + 16 * slot + 8 * h, (item / SL) & 1, failed);
+                        if (ok && elect_one()) {
+                            tmem_fence_after();
+#pragma unroll
+                            for (int k = h * TN / 32; k < (h + 1) * TN / 32; ++k)
+                                mma_ts(to, from + k * 8, desc(vd + k * (2048 / 16)), kindO, j > 0 || k > 0);
+                            if (h == 1)
+                                mma_commit(oDone + 8 * slot);
+                        }
+                        __syncwarp();
+                    }
                     if (tile == MT - 1)
-                        release(sk);
+                        commit(empty + 8 * sv);
+                    if (j + LA < J) {
+                        if (tile == 0)
+                            sk = acquire();
+                        scores(sk, tile, item + LA);
+                        if (tile == MT - 1) {
+                            commit(empty + 8 * sk);
+                            if (j + LA == J - 1)
+                                commit(qFree);
+                        }
+                    }
                 }
             }
+            items += J;
         }
         // the last products' arrivals
         for (int i = n > NS ? n - NS : 0; i < n; ++i)
             mbar_wait_warp(empty + 8 * (i % NS), (i / NS) & 1, failed);
+        if (nq > 0)
+            mbar_wait_warp(qFree, (nq - 1) & 1, failed);
+    } else if (warp == kAlloc) {
+        // ---------------------------------------------------------- segments
+        few_registers<MT>();
+        bool ok = true;
+        int n = 0;
+        auto publish = [&](const Segment& s) {
+            const int i = n % kSegments;
+            ok = ok && (n < kSegments || mbar_wait_warp(segFree + 8 * i, (n / kSegments - 1) & 1, failed));
+            if (ok && lane == 0) {
+                ring[i] = s;
+                mbar_arrive(segFull + 8 * i);
+            }
+            __syncwarp();
+            ++n;
+        };
+        Segment s;
+        Joint joint = {};
+        long long at = start.at;
+        const long long end = start.end, share = start.share;
+        if (start.b < a.B) {
+            static_cast<Sequence&>(s) = sequence<TREE>(a, start.b);
+            const long long perHead = steps_before<TN, TREE>(a, s, s.units);
+            s.head = (int)(start.inside / perHead);
+            long long inside = start.inside - s.head * perHead;      // steps of the head group before `at`
+            // the unit: the last with no more steps before it, by 32 guesses at a time
+            int lo = 0, hi = s.units;
+            while (hi - lo > 1) {
+                const int width = (hi - lo + 31) / 32, u = min(hi, lo + lane * width);
+                const uint32_t fits = __ballot_sync(0xffffffffu, u < hi && steps_before<TN, TREE>(a, s, u) <= inside);
+                lo += (31 - __clz(fits)) * width;
+                hi = min(hi, lo + width);
+            }
+            inside -= steps_before<TN, TREE>(a, s, lo);
+            int unit = lo;
+            while (ok && at < end) {
+                const int tiles = tiles_of<TN>(a, s, unit), len = kSwitch + max(1, tiles);
+                const long long first = at - inside + kSwitch;       // of the unit's real steps, among all
+                long long take = min((long long)len - inside, end - at);
+                if (a.whole)
+                    take = len - inside;                             // nothing of a unit that began before
+                const int r0 = max(0, (int)inside - kSwitch), r1 = max(0, (int)(inside + take) - kSwitch);
+                if (a.whole ? inside == 0 : r1 > r0) {
+                    s.tok0 = unit * a.tokens;
+                    s.j0 = min(r0, tiles);
+                    s.j1 = min(r1, tiles);
+                    const bool all = r0 == 0 && r1 == len - kSwitch;
+                    s.slot = all ? -1 : 2 * (int)blockIdx.x + (r0 == 0);
+                    if (r0 == 0 && !all)
+                        joint = {s.qRow, s.tok0, s.nq, s.head, (int)((first + (len - kSwitch) - 1) / share - first / share) + 1};
+                    publish(s);
+                }
+                at += take;
+                inside = 0;
+                if (++unit == s.units) {
+                    unit = 0;
+                    if (++s.head == a.heads) {
+                        s.head = 0;
+                        do {
+                            const int b = s.b + 1;
+                            if (b == a.B) {
+                                at = end;
+                                break;
+                            }
+                            static_cast<Sequence&>(s) = sequence<TREE>(a, b);
+                        } while (s.units == 0);
+                    }
+                }
+            }
+        }
+        s.head = -1;
+        publish(s);
+        if (lane == 0 && !a.whole)
+            a.joints[blockIdx.x] = joint;
     } else if (warp < 4 * MT) {
         // ----------------------------------------------------------- softmax
+        more_registers<MT>();
         const int tile = warp >> 2;
+        const int row = (int)threadIdx.x;                       // of the CTA's tiles
         const uint32_t laneBase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t oAddr = laneBase + C::kColO + tile * D;
-        const int row = (int)threadIdx.x;                       // of the CTA's tiles
         const int rowTok = divide(row, a.divG), g = row - rowTok * a.G;
-        const bool live = work && rowTok < a.tokens && seg.tok0 + rowTok < seg.nq;
-        const int token = live ? seg.tok0 + rowTok : max(0, seg.nq - 1);
-        const bool warpLive = __any_sync(0xffffffffu, live);
-        const int limit = work ? row_limit(a, seg, token) : 0;
-        const int32_t* words = a.treeMask != nullptr && work ? a.treeMask + ((size_t)seg.b * a.S + token) * a.W : nullptr;
-        // keys below this are seen by all of the warp's rows
-        int allSee = words != nullptr ? min(limit, seg.base) : limit;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            allSee = min(allSee, __shfl_xor_sync(0xffffffffu, allSee, d));
-        float M = -INFINITY, l = 0.0f;
         // |c|, kept above 0 so that a masked -infinity stays one (c = 0: all scores are 0)
         const float scale = fmaxf(fabsf(a.scaleLog2), 1e-30f);
         bool ok = true;
-        for (int j = 0; j < J; ++j) {
-            const int slot = tile * SL + j % SL;
-            const uint32_t sAddr = laneBase + slot * TN;
-            ok = mbar_wait_warp(sFull + 8 * slot, (j / SL) & 1, failed);
-            if (!ok)
-                break;
-            if (!warpLive) {
-                mbar_arrive(pFull + 8 * slot);
-                continue;
-            }
-            tmem_fence_after();
-            float s[TN];
+        int items = 0;
+        Segment seg;
+        while (ok && next(seg)) {
+            const int J = seg.j1 - seg.j0;
+            const bool live = rowTok < a.tokens && seg.tok0 + rowTok < seg.nq;
+            const int token = live ? seg.tok0 + rowTok : seg.nq - 1;
+            const bool warpLive = __any_sync(0xffffffffu, live);
+            const int limit = row_limit(a, seg, token);
+            const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)seg.b * a.S + token) * a.W : nullptr;
+            // keys below this are seen by all of the warp's rows
+            int allSee = words != nullptr ? min(limit, seg.base) : limit;
 #pragma unroll
-            for (int k = 0; k < TN / 32; ++k)
-                tmem_load32(s + 32 * k, sAddr + 32 * k);
-            tmem_wait_load();
-#pragma unroll
-            for (int k = 0; k < TN / 32; ++k)
-                pin32(s + 32 * k);
-            if (a.scaleLog2 < 0.0f) {
-#pragma unroll
-                for (int k = 0; k < TN; ++k)
-                    s[k] = -s[k];
-            }
-            const int t0 = (seg.j0 + j) * TN;
-            if (t0 + TN > allSee) {
-#pragma unroll
-                for (int w = 0; w < TN / 32; ++w) {
-                    const uint32_t bits = sees32(a, words, seg.base, limit, t0 + 32 * w);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        s[32 * w + k] = (bits >> k) & 1 ? s[32 * w + k] : -INFINITY;
+            for (int d = 16; d > 0; d >>= 1)
+                allSee = min(allSee, __shfl_xor_sync(0xffffffffu, allSee, d));
+            float M = -INFINITY, l = 0.0f;
+            for (int j = 0; ok && j < J; ++j) {
+                const int item = items + j, slot = tile * SL + item % SL;
+                const uint32_t sAddr = laneBase + slot * TN;
+                ok = mbar_wait_warp(sFull + 8 * slot, (item / SL) & 1, failed);
+                if (!ok)
+                    break;
+                if (!warpLive) {
+                    if (lane == 0) {
+                        mbar_arrive(pFull + 16 * slot);
+                        mbar_arrive(pFull + 16 * slot + 8);
+                    }
+                    continue;
                 }
-            }
-            float top4[4] = {s[0], s[1], s[2], s[3]};
+                tmem_fence_after();
+                float s[TN];
 #pragma unroll
-            for (int k = 4; k + 8 <= TN; k += 8)
+                for (int k = 0; k < TN / 32; ++k)
+                    tmem_load32(s + 32 * k, sAddr + 32 * k);
+                tmem_wait_load();
+#pragma unroll
+                for (int k = 0; k < TN / 32; ++k)
+                    pin32(s + 32 * k);
+                if (a.scaleLog2 < 0.0f) {
+#pragma unroll
+                    for (int k = 0; k < TN; ++k)
+                        s[k] = -s[k];
+                }
+                const int t0 = (seg.j0 + j) * TN;
+                if (t0 + TN > allSee) {
+#pragma unroll
+                    for (int w = 0; w < TN / 32; ++w) {
+                        const uint32_t bits = sees32(a, words, seg.base, limit, t0 + 32 * w);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            s[32 * w + k] = (bits >> k) & 1 ? s[32 * w + k] : -INFINITY;
+                    }
+                }
+                float top4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k + 8 <= TN; k += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        top4[x] = max3(top4[x], s[k + 2 * x], s[k + 2 * x + 1]);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    top4[x] = fmaxf(fmaxf(top4[x], s[k + 2 * x]), s[k + 2 * x + 1]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                top4[x] = fmaxf(top4[x], s[TN - 4 + x]);
-            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-            top = top == -INFINITY ? top : top * scale;
-            if (__any_sync(0xffffffffu, top > M + 8.0f)) {
-                const float next = fmaxf(M, top);
-                const float f = M == next ? 1.0f : exp2_fast(M - next);
-                M = next;
-                l *= f;
-                if (j > 0) {
-                    // O of this row tile is at rest: its last product has finished
-                    ok = mbar_wait_warp(oDone + 8 * (tile * SL + (j - 1) % SL), ((j - 1) / SL) & 1, failed);
-                    if (!ok)
-                        break;
-                    tmem_fence_after();
+                    top4[x] = fmaxf(top4[x], s[TN - 4 + x]);
+                float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                top = top == -INFINITY ? top : top * scale;
+                if (__any_sync(0xffffffffu, top > M + 8.0f)) {
+                    const float next = fmaxf(M, top);
+                    const float f = M == next ? 1.0f : exp2_fast(M - next);
+                    M = next;
+                    l *= f;
+                    if (j > 0) {
+                        // O of this row tile is at rest: its last product has finished
+                        ok = mbar_wait_warp(oDone + 8 * (tile * SL + (item - 1) % SL), ((item - 1) / SL) & 1, failed);
+                        if (!ok)
+                            break;
+                        tmem_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        float o[32];
-                        tmem_load32(o, oAddr + k);
-                        tmem_wait_load();
-                        pin32(o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            o[x] *= f;
-                        tmem_store32(oAddr + k, reinterpret_cast<const uint32_t*>(o));
-                    }
-                    tmem_wait_store();
-                }
-            }
-            const float mm = M == -INFINITY ? 0.0f : M;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < TN; k += 64) {
-                uint32_t p[32];
-#pragma unroll
-                for (int x = 0; x < 64; x += 4) {
-                    float v[4];
-                    fma2(v[0], v[1], s[k + x], s[k + x + 1], scale, scale, -mm, -mm);
-                    fma2(v[2], v[3], s[k + x + 2], s[k + x + 3], scale, scale, -mm, -mm);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        v[y] = exp2_fast(v[y]);
-                    add2(sum[0], sum[1], v[0], v[1]);
-                    add2(sum[2], sum[3], v[2], v[3]);
-                    p[x / 2] = half2_bits(v[0], v[1]);
-                    p[x / 2 + 1] = half2_bits(v[2], v[3]);
-                }
-                tmem_store32(sAddr + k / 2, p);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_store();
-            tmem_fence_before();
-            mbar_arrive(pFull + 8 * slot);
-        }
-        if (J > 0 && ok)
-            ok = mbar_wait_warp(oDone + 8 * (tile * SL + (J - 1) % SL), ((J - 1) / SL) & 1, failed);
-        tmem_fence_after();
-        const bool none = J == 0 || l == 0.0f;
-        const float inv = none ? 0.0f : 1.0f / l;
-        const float bad = *failed ? __int_as_float(0x7fc00000) : 0.0f;
-        const int hq = seg.head * a.G + g;
-        const size_t at = (size_t)(seg.qRow + token) * a.Hq + hq;       // row of out
-        const size_t partAt = (size_t)seg.part * a.T * a.Hq + at;
-        bool strange = false;
-        if (warpLive) {
-#pragma unroll 1
-            for (int pass = 0; pass < 2; ++pass) {
-                float again[D];
-                if (pass == 1) {
-                    if (!__any_sync(0xffffffffu, strange))
-                        break;
-                    if (strange)
-                        plain_row<D>(a, seg, a.q + (size_t)(seg.qRow + token) * a.qStride + (size_t)hq * D, token,
-                                     seg.j1 * TN, M, l, again);
-                }
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float o[32];
-                    if (pass == 0) {
-                        if (J > 0) {
-                            tmem_load32(o, oAddr + k);
+                        for (int k = 0; k < D; k += 16) {
+                            float o[16];
+                            tmem_load16(o, oAddr + k);
                             tmem_wait_load();
-                            pin32(o);
-                        }
-                    } else {
-                        for (int x = 0; x < 32; ++x)
-                            o[x] = again[k + x];
-                    }
+                            pin16(o);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        if (pass == 0)
-                            o[x] = none ? bad : o[x] * inv + bad;
-                        strange = strange || (pass == 0 && live && !none && !(fabsf(o[x]) < INFINITY) && fabsf(l) < INFINITY && bad == 0.0f);
-                    }
-                    if (live && (pass == 0 || strange)) {
-                        if (a.parts > 1) {
-#pragma unroll
-                            for (int x = 0; x < 32; x += 4)
-                                *reinterpret_cast<float4*>(a.partO + partAt * D + k + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 32; x += 8) {
-                                uint4 y;
-                                uint32_t* w = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    w[z] = half2_bits(within_half(o[x + 2 * z]), within_half(o[x + 2 * z + 1]));
-                                *reinterpret_cast<uint4*>(a.out + at * D + k + x) = y;
-                            }
+                            for (int x = 0; x < 16; ++x)
+                                o[x] *= f;
+                            tmem_store16(oAddr + k, reinterpret_cast<const uint32_t*>(o));
                         }
                     }
                 }
+                const float mm = M == -INFINITY ? 0.0f : M;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < TN; k += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        float v[4];
+                        fma2(v[0], v[1], s[k + x], s[k + x + 1], scale, scale, -mm, -mm);
+                        fma2(v[2], v[3], s[k + x + 2], s[k + x + 3], scale, scale, -mm, -mm);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            v[y] = exp2_fast(v[y]);
+                        add2(sum[0], sum[1], v[0], v[1]);
+                        add2(sum[2], sum[3], v[2], v[3]);
+                        p[x / 2] = half2_bits(v[0], v[1]);
+                        p[x / 2 + 1] = half2_bits(v[2], v[3]);
+                    }
+                    tmem_store16(sAddr + k / 2, p);
+                    if (k + 32 == TN / 2 || k + 32 == TN) {
+                        // this half's products may start
+                        tmem_wait_store();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(pFull + 16 * slot + (k + 32 == TN ? 8 : 0));
+                    }
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
+            items += J;
+            if (J > 0 && ok)
+                ok = mbar_wait_warp(oDone + 8 * (tile * SL + (items - 1) % SL), ((items - 1) / SL) & 1, failed);
+            if (!warpLive)
+                continue;
+            tmem_fence_after();
+            const bool none = J == 0 || l == 0.0f, wrong = *failed != 0;
+            const float inv = none ? 0.0f : 1.0f / l;
+            const int at = (seg.qRow + token) * a.Hq + seg.head * a.G + g;      // row of out
+            // two lanes write 32 bytes of one row, then of the other's
+            const int even = __shfl_sync(0xffffffffu, live ? at : -1, lane & ~1), odd = __shfl_sync(0xffffffffu, live ? at : -1, lane | 1);
+            const bool plain = __all_sync(0xffffffffu, !none && !wrong);
+            float nan0 = 0.0f, nan1 = 0.0f;                                     // NaN if an element is not finite
+#pragma unroll 2
+            for (int k = 0; k < D; k += 16) {
+                float o[16];
+                if (J > 0) {
+                    tmem_load16(o, oAddr + k);
+                    tmem_wait_load();
+                    pin16(o);
+                }
+                if (!plain) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        o[x] = wrong ? __int_as_float(0x7fc00000) : none ? 0.0f : o[x];
+                }
+#pragma unroll
+                for (int x = 0; x < 16; x += 2) {
+                    mul2(o[x], o[x + 1], inv);
+                    fma2(nan0, nan1, o[x], o[x + 1], 0.0f, 0.0f, nan0, nan1);
+                }
+                if (seg.slot >= 0) {
+                    // in quarters of 16 bytes, each of all rows
+                    float4* to = reinterpret_cast<float4*>(a.partO) + ((size_t)seg.slot * (D / 4) + k / 4) * (MT * 128) + row;
+#pragma unroll
+                    for (int x = 0; x < 16; x += 4)
+                        if (live)
+                            to[(x / 4) * (MT * 128)] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    continue;
+                }
+                uint32_t c[2][4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    c[0][z] = half2_sat(o[2 * z], o[2 * z + 1]);
+                    c[1][z] = half2_sat(o[8 + 2 * z], o[8 + 2 * z + 1]);
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? c[0][z] : c[1][z], 1);
+                    c[0][z] = lane & 1 ? got : c[0][z];
+                    c[1][z] = lane & 1 ? c[1][z] : got;
+                }
+                uint16_t* to = a.out + k + (lane & 1) * 8;
+                if (even >= 0)
+                    *reinterpret_cast<uint4*>(to + (size_t)even * D) = make_uint4(c[0][0], c[0][1], c[0][2], c[0][3]);
+                if (odd >= 0)
+                    *reinterpret_cast<uint4*>(to + (size_t)odd * D) = make_uint4(c[1][0], c[1][1], c[1][2], c[1][3]);
+            }
+            tmem_fence_before();
             if (live) {
-                if (a.parts > 1)
-                    a.partL[partAt] = none ? -INFINITY + bad : M + log2f(l) + bad;
+                const float bad = wrong ? __int_as_float(0x7fc00000) : 0.0f;
+                if (seg.slot >= 0)
+                    a.partL[(size_t)seg.slot * (MT * 128) + row] = none ? -INFINITY + bad : M + log2f(l) + bad;
                 else if (a.lse != nullptr)
                     a.lse[at] = none ? -INFINITY + bad : kLn2 * (M + log2f(l)) + bad;
             }
+            const bool strange = live && !none && !wrong && fabsf(l) < INFINITY && !(nan0 + nan1 == 0.0f);
+            if (__any_sync(0xffffffffu, strange)) {
+                __syncwarp();          // other lanes have written of the row
+                if (strange)
+                    plain_row<D, MT>(a, seg, token, at, row, M, l);
+                __syncwarp();
+            }
         }
-        tmem_fence_before();
+    } else {
+        few_registers<MT>();
     }
+    // the join may start; it waits for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
     if (warp == kAlloc) {
         __syncwarp();
@@ -628,30 +934,60 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     }
 }
 
-// Joins the partial results of a row, in the order of its parts. D / 8 threads hold a row.
-template <int D>
+// Joins the pieces of a unit, in the order of its steps: CTA c's piece, which begins it, then
+// those of the CTAs behind. A warp takes 8 rows x 32 dims, a thread 8 dims of a row; four
+// pieces' loads are in flight together.
+template <int D, int MT>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsArgs a)
 {
-    constexpr int TG = D / 8;
-    const int64_t row = (int64_t)blockIdx.x * (256 / TG) + threadIdx.x / TG;
-    const int64_t rows = (int64_t)a.T * a.Hq;
-    const int d = threadIdx.x % TG * 8;
-    if (row >= rows)
+    constexpr int kChunks = MT * 16 * (D / 32) / 8;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x / kChunks, warp = (blockIdx.x - c * kChunks) * 8 + (threadIdx.x >> 5);
+    const Joint joint = a.joints[c];
+    const int row = warp / (D / 32) * 8 + (threadIdx.x >> 2 & 7), d = warp % (D / 32) * 32 + (threadIdx.x & 3) * 8;
+    const int rowTok = divide(row, a.divG), g = row - rowTok * a.G;
+    if (joint.pieces == 0 || rowTok >= a.tokens || joint.tok0 + rowTok >= joint.nq)
         return;
     float m = -INFINITY, l = 0.0f, o[8] = {};
-    for (int p = 0; p < a.parts; ++p)
-        m = fmaxf(m, a.partL[p * rows + row]);
-    const float mm = m == -INFINITY ? 0.0f : m;
-    for (int p = 0; p < a.parts; ++p) {
-        const float x = a.partL[p * rows + row];
-        if (x == -INFINITY)
-            continue;
-        const float w = exp2_fast(x - mm);
-        l += w;
-        const float* y = a.partO + (p * rows + row) * D + d;
+    for (int k = 0; k < joint.pieces; k += 4) {
+        float x[4];
+        float4 v[4][2];
+        float top = m;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            o[k] += w * y[k];
+        for (int j = 0; j < 4; ++j) {
+            const int i = k + j, slot = i == 0 ? 2 * c + 1 : 2 * (c + i);
+            x[j] = -INFINITY;
+            v[j][0] = v[j][1] = make_float4(0, 0, 0, 0);
+            if (i < joint.pieces) {
+                const size_t at = (size_t)slot * (MT * 128) + row;
+                x[j] = a.partL[at];
+                const float4* from = reinterpret_cast<const float4*>(a.partO) + ((size_t)slot * (D / 4) + d / 4) * (MT * 128) + row;
+                v[j][0] = from[0];
+                v[j][1] = from[MT * 128];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            top = fmaxf(top, x[j]);
+        const float mm = top == -INFINITY ? 0.0f : top;
+        const float f = exp2_fast(m - mm);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+            o[y] *= f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float w = exp2_fast(x[j] - mm);
+            const float* y = reinterpret_cast<const float*>(v[j]);
+            if (x[j] != -INFINITY) {
+                l += w;
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    o[z] += w * y[z];
+            }
+        }
     }
     const bool none = l == 0.0f;
     const float inv = none ? 0.0f : 1.0f / l;
@@ -659,9 +995,10 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         w[k] = none ? 0u : half2_bits(within_half(o[2 * k] * inv), within_half(o[2 * k + 1] * inv));
-    *reinterpret_cast<uint4*>(a.out + row * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+    const size_t at = (size_t)(joint.qRow + joint.tok0 + rowTok) * a.Hq + joint.head * a.G + g;
+    *reinterpret_cast<uint4*>(a.out + at * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
     if (d == 0 && a.lse != nullptr)
-        a.lse[row] = none ? -INFINITY : kLn2 * (m + log2f(l));
+        a.lse[at] = none ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
 }  // namespace ropekv_rows

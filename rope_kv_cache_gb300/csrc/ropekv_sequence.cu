@@ -96,13 +96,14 @@ bool make_map(CUtensorMap* map, const uint16_t* p, int D, int64_t d1, int64_t s1
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a call is cut, from its sizes alone.
+// How a call is cut, from its sizes alone (the shares follow from the lengths, on the device).
 struct Plan {
     int mt;                   // row tiles of a CTA
     int G, heads, tokens;     // heads of a tile, head groups, tokens of a CTA's tiles
     int tilesSeq;             // tree: CTA tiles of a sequence
-    int parts;                // ranges of the keys
-    long long tiles;          // CTA tiles of a head group, at most
+    int ctas;
+    bool whole;               // no unit is split: there is nothing to join
+    int leastShare;
 };
 
 // Rows of a tile: the heads that share a KV head, or a divisor of them that fits.
@@ -123,18 +124,31 @@ Plan make_plan(bool tree, int64_t T, int B, int S, int Hq, int Hkv, int D, int64
     p.mt = D != 256 && rows > 128 ? 2 : 1;
     p.tokens = 128 * p.mt / p.G;
     p.tilesSeq = (S + p.tokens - 1) / p.tokens;
-    p.tiles = tree ? (long long)B * p.tilesSeq : T / p.tokens + std::min<int64_t>(B, T);
-    p.parts = 1;
-    if (tree) {
-        const long long kv = (keys + (D == 256 ? 63 : 127)) / (D == 256 ? 64 : 128), units = p.tiles * p.heads;
-        p.parts = (int)std::max(1LL, std::min({(2LL * kSMs + units - 1) / std::max(1LL, units), kv, 32LL}));
-    }
+    // at most so many units, of so many K/V tiles
+    const int64_t units = (tree ? (int64_t)B * p.tilesSeq : T / p.tokens + std::min<int64_t>(B, T)) * p.heads;
+    const int64_t tiles = std::max<int64_t>(1, (keys + (D == 256 ? 63 : 127)) / (D == 256 ? 64 : 128));
+    p.whole = tiles <= 2;
+    p.leastShare = 4;
+    p.ctas = (int)std::min<int64_t>(kSMs, p.whole ? units : units * ((tiles + ropekv_rows::kSwitch + p.leastShare - 1) / p.leastShare));
     return p;
 }
 
-int64_t workspace_of(const Plan& p, int64_t rows, int D)
+// Workspace: joints, partL, partO, each on a 256-byte boundary.
+struct Layout {
+    int64_t partL, partO, size;
+};
+
+Layout make_layout(const Plan& p, int D)
 {
-    return p.parts == 1 ? 16 : ((int64_t)p.parts * rows * 4 + 255) / 256 * 256 + (int64_t)p.parts * rows * D * 4;
+    if (p.whole)
+        return {0, 0, 16};
+    auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    const int64_t rows = 2LL * p.ctas * p.mt * 128;
+    Layout w;
+    w.partL = up(p.ctas * (int64_t)sizeof(ropekv_rows::Joint));
+    w.partO = w.partL + up(rows * 4);
+    w.size = w.partO + up(rows * D * 4);
+    return w;
 }
 
 template <int D, int MT, bool TREE>
@@ -145,12 +159,10 @@ int launch_rows(const RowsArgs& a, const Plan& p, const CUtensorMap& q, const CU
     using C = RowsConfig<D, MT>;
     if (!raise_smem<kern>(C::kSmem))
         return ROPEKV_ERR_LAUNCH;
-    int rc = launch(kern, p.tiles * p.heads * p.parts, C::kThreads, C::kSmem, false, st, a, q, k, v);
-    if (rc == ROPEKV_OK && p.parts > 1) {
-        const long long rows = (long long)a.T * a.Hq, per = 256 / (D / 8);
-        rc = launch(ropekv_rows::rows_join_kernel<D>, (rows + per - 1) / per, 256, 0, false, st, a);
-    }
-    return rc;
+    const int rc = launch(kern, p.ctas, C::kThreads, C::kSmem, true, st, a, q, k, v);
+    if (rc != ROPEKV_OK || p.whole)
+        return rc;
+    return launch(ropekv_rows::rows_join_kernel<D, MT>, p.ctas * (long long)(MT * 16 * (D / 32) / 8), 256, 0, true, st, a);
 }
 
 template <bool TREE>
@@ -160,12 +172,15 @@ int run(RowsArgs& a, const Plan& p, int D, int Hkv, int64_t kvTokens, int64_t kv
     a.heads = p.heads;
     a.headsPerKv = p.heads / Hkv;
     a.tokens = p.tokens;
-    a.parts = p.parts;
     a.tilesSeq = p.tilesSeq;
+    a.ctas = p.ctas;
+    a.whole = p.whole;
+    a.leastShare = p.leastShare;
     a.divG = make_divisor(p.G);
-    const int64_t rows = (int64_t)a.T * a.Hq;
-    a.partL = (float*)workspace;
-    a.partO = (float*)((uint8_t*)workspace + ((int64_t)p.parts * rows * 4 + 255) / 256 * 256);
+    const Layout at = make_layout(p, D);
+    a.joints = (ropekv_rows::Joint*)workspace;
+    a.partL = (float*)((uint8_t*)workspace + at.partL);
+    a.partO = (float*)((uint8_t*)workspace + at.partO);
     const int tile = D == 256 ? 64 : 128;
     CUtensorMap q, k, v;
     const int64_t batchStride = TREE ? a.kvBatch : 8;     // of a single batch any will do
@@ -244,7 +259,7 @@ int64_t prompt_attention_workspace_size(const ropekv_prompt_dims* dims)
         return rc;
     if (dims->numTokens == 0 || dims->batch == 0)
         return 0;
-    return workspace_of(plan_of(dims), (int64_t)dims->numTokens * dims->numQHeads, dims->headDim);
+    return make_layout(plan_of(dims), dims->headDim).size;
 }
 
 int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k, int64_t kTokenStride,
@@ -270,7 +285,7 @@ int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k,
     if (overlap(q, (dims->numTokens - 1) * qTokenStride + Hq * D, out, dims->numTokens * Hq * D))
         return ROPEKV_ERR_SHAPE;
     const Plan p = plan_of(dims);
-    if (workspaceBytes < workspace_of(p, dims->numTokens * Hq, dims->headDim))
+    if (workspaceBytes < make_layout(p, dims->headDim).size)
         return ROPEKV_ERR_CAPACITY;
     RowsArgs a = {};
     a.q = q;
@@ -302,7 +317,7 @@ int64_t tree_attention_workspace_size(const ropekv_tree_dims* dims)
         return rc;
     if (dims->batch == 0 || dims->seqLen == 0)
         return 0;
-    return workspace_of(plan_of(dims), (int64_t)dims->batch * dims->seqLen * dims->numQHeads, dims->headDim);
+    return make_layout(plan_of(dims), dims->headDim).size;
 }
 
 int tree_attention(const uint16_t* q, const uint16_t* kvCache, const int32_t* kvCacheEndLens,
@@ -325,7 +340,7 @@ int tree_attention(const uint16_t* q, const uint16_t* kvCache, const int32_t* kv
     if (overlap(q, T * row, out, T * row))
         return ROPEKV_ERR_SHAPE;
     const Plan p = plan_of(dims);
-    if (workspaceBytes < workspace_of(p, T * dims->numQHeads, dims->headDim))
+    if (workspaceBytes < make_layout(p, dims->headDim).size)
         return ROPEKV_ERR_CAPACITY;
     const int64_t cap = std::max(1, dims->kvCapacity), plane = cap * dims->numKVHeads * dims->headDim;
     RowsArgs a = {};
