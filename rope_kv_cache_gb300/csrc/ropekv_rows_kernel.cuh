@@ -82,6 +82,7 @@ struct RowsArgs {
     int32_t ctas;
     int32_t whole;             // units are not split: each goes to the CTA in whose share it begins
     int32_t leastShare;        // steps of a share, at least
+    int32_t out32;             // out is a multiple of 32 bytes, not of 16 alone
     Divisor divG;
 };
 
@@ -91,7 +92,7 @@ struct Joint {
 };
 
 // Steps that changing from one unit to the next costs.
-constexpr int kSwitch = 2;
+constexpr int kSwitch = 3;
 
 // A sequence as the kernel sees it.
 struct Sequence {
@@ -205,13 +206,6 @@ __device__ __forceinline__ void tmem_load16(float* f, uint32_t addr)
         : "r"(addr));
 }
 
-__device__ __forceinline__ void pin16(float* f)
-{
-    asm volatile(""
-        : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
-          "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]));
-}
-
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r)
 {
     asm volatile(
@@ -220,6 +214,53 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r)
            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
            "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(float* f, uint32_t addr)
+{
+#pragma unroll
+    for (int k = 0; k < N; k += 32)
+        tmem_load32(f + k, addr + k);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* r)
+{
+    if constexpr (N == 16)
+        tmem_store16(addr, r);
+    else
+        tmem_store8(addr, r);
+}
+
+// Ties values to this point, behind a wait: nothing that uses them can be scheduled before it.
+template <int N>
+__device__ __forceinline__ void pin(float* f)
+{
+#pragma unroll
+    for (int k = 0; k < N; k += 8)
+        asm volatile("" : "+f"(f[k]), "+f"(f[k + 1]), "+f"(f[k + 2]), "+f"(f[k + 3]), "+f"(f[k + 4]), "+f"(f[k + 5]),
+                          "+f"(f[k + 6]), "+f"(f[k + 7]));
+}
+
+// 32 bytes, in one piece if the address is a multiple of that.
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t* r, bool whole)
+{
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+        *reinterpret_cast<uint4*>(p + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+    }
 }
 
 // A row of O / l from the segment's tokens that the row sees, in FP32 throughout, in place of
@@ -734,19 +775,21 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         const float scale = fmaxf(fabsf(a.scaleLog2), 1e-30f);
         bool ok = true;
         int items = 0;
-        Segment seg;
-        while (ok && next(seg)) {
+        for (; ok; ++segments) {
+            const int at4 = segments % kSegments;
+            ok = mbar_wait_warp(segFull + 8 * at4, (segments / kSegments) & 1, failed);
+            const Segment& seg = ring[at4];                     // given back when its rows have left
+            if (!ok || seg.head < 0)
+                break;
             const int J = seg.j1 - seg.j0;
             const bool live = rowTok < a.tokens && seg.tok0 + rowTok < seg.nq;
             const int token = live ? seg.tok0 + rowTok : seg.nq - 1;
             const bool warpLive = __any_sync(0xffffffffu, live);
             const int limit = row_limit(a, seg, token);
             const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)seg.b * a.S + token) * a.W : nullptr;
-            // keys below this are seen by all of the warp's rows
-            int allSee = words != nullptr ? min(limit, seg.base) : limit;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-                allSee = min(allSee, __shfl_xor_sync(0xffffffffu, allSee, d));
+            // keys below this are seen by all of the warp's rows (limits do not fall from row to row)
+            const int least = __shfl_sync(0xffffffffu, limit, 0);
+            const int allSee = words != nullptr ? min(least, seg.base) : least;
             float M = -INFINITY, l = 0.0f;
             for (int j = 0; ok && j < J; ++j) {
                 const int item = items + j, slot = tile * SL + item % SL;
@@ -763,13 +806,9 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 }
                 tmem_fence_after();
                 float s[TN];
-#pragma unroll
-                for (int k = 0; k < TN / 32; ++k)
-                    tmem_load32(s + 32 * k, sAddr + 32 * k);
+                tmem_load<TN>(s, sAddr);
                 tmem_wait_load();
-#pragma unroll
-                for (int k = 0; k < TN / 32; ++k)
-                    pin32(s + 32 * k);
+                pin<TN>(s);
                 if (a.scaleLog2 < 0.0f) {
 #pragma unroll
                     for (int k = 0; k < TN; ++k)
@@ -812,7 +851,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                             float o[16];
                             tmem_load16(o, oAddr + k);
                             tmem_wait_load();
-                            pin16(o);
+                            pin<16>(o);
 #pragma unroll
                             for (int x = 0; x < 16; ++x)
                                 o[x] *= f;
@@ -853,63 +892,68 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             items += J;
             if (J > 0 && ok)
                 ok = mbar_wait_warp(oDone + 8 * (tile * SL + (items - 1) % SL), ((items - 1) / SL) & 1, failed);
-            if (!warpLive)
+            if (!warpLive) {
+                if (lane == 0)
+                    mbar_arrive(segFree + 8 * at4);
                 continue;
+            }
             tmem_fence_after();
             const bool none = J == 0 || l == 0.0f, wrong = *failed != 0;
             const float inv = none ? 0.0f : 1.0f / l;
             const int at = (seg.qRow + token) * a.Hq + seg.head * a.G + g;      // row of out
-            // two lanes write 32 bytes of one row, then of the other's
+            const int slot = seg.slot;
+            // two lanes write 64 bytes of one row, then of the other's
             const int even = __shfl_sync(0xffffffffu, live ? at : -1, lane & ~1), odd = __shfl_sync(0xffffffffu, live ? at : -1, lane | 1);
             const bool plain = __all_sync(0xffffffffu, !none && !wrong);
             float nan0 = 0.0f, nan1 = 0.0f;                                     // NaN if an element is not finite
-#pragma unroll 2
-            for (int k = 0; k < D; k += 16) {
-                float o[16];
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+                float o[32];
                 if (J > 0) {
-                    tmem_load16(o, oAddr + k);
+                    tmem_load<32>(o, oAddr + k);
                     tmem_wait_load();
-                    pin16(o);
+                    pin<32>(o);
                 }
                 if (!plain) {
 #pragma unroll
-                    for (int x = 0; x < 16; ++x)
+                    for (int x = 0; x < 32; ++x)
                         o[x] = wrong ? __int_as_float(0x7fc00000) : none ? 0.0f : o[x];
                 }
 #pragma unroll
-                for (int x = 0; x < 16; x += 2) {
+                for (int x = 0; x < 32; x += 2) {
                     mul2(o[x], o[x + 1], inv);
                     fma2(nan0, nan1, o[x], o[x + 1], 0.0f, 0.0f, nan0, nan1);
                 }
-                if (seg.slot >= 0) {
+                if (slot >= 0) {
                     // in quarters of 16 bytes, each of all rows
-                    float4* to = reinterpret_cast<float4*>(a.partO) + ((size_t)seg.slot * (D / 4) + k / 4) * (MT * 128) + row;
+                    float4* to = reinterpret_cast<float4*>(a.partO) + ((size_t)slot * (D / 4) + k / 4) * (MT * 128) + row;
+                    if (live) {
 #pragma unroll
-                    for (int x = 0; x < 16; x += 4)
-                        if (live)
+                        for (int x = 0; x < 32; x += 4)
                             to[(x / 4) * (MT * 128)] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    }
                     continue;
                 }
-                uint32_t c[2][4];
+                uint32_t c[2][8];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
+                for (int z = 0; z < 8; ++z) {
                     c[0][z] = half2_sat(o[2 * z], o[2 * z + 1]);
-                    c[1][z] = half2_sat(o[8 + 2 * z], o[8 + 2 * z + 1]);
+                    c[1][z] = half2_sat(o[16 + 2 * z], o[16 + 2 * z + 1]);
                     const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? c[0][z] : c[1][z], 1);
                     c[0][z] = lane & 1 ? got : c[0][z];
                     c[1][z] = lane & 1 ? c[1][z] : got;
                 }
-                uint16_t* to = a.out + k + (lane & 1) * 8;
+                uint16_t* to = a.out + k + (lane & 1) * 16;
                 if (even >= 0)
-                    *reinterpret_cast<uint4*>(to + (size_t)even * D) = make_uint4(c[0][0], c[0][1], c[0][2], c[0][3]);
+                    store32(to + (size_t)even * D, c[0], a.out32);
                 if (odd >= 0)
-                    *reinterpret_cast<uint4*>(to + (size_t)odd * D) = make_uint4(c[1][0], c[1][1], c[1][2], c[1][3]);
+                    store32(to + (size_t)odd * D, c[1], a.out32);
             }
             tmem_fence_before();
             if (live) {
                 const float bad = wrong ? __int_as_float(0x7fc00000) : 0.0f;
-                if (seg.slot >= 0)
-                    a.partL[(size_t)seg.slot * (MT * 128) + row] = none ? -INFINITY + bad : M + log2f(l) + bad;
+                if (slot >= 0)
+                    a.partL[(size_t)slot * (MT * 128) + row] = none ? -INFINITY + bad : M + log2f(l) + bad;
                 else if (a.lse != nullptr)
                     a.lse[at] = none ? -INFINITY + bad : kLn2 * (M + log2f(l)) + bad;
             }
@@ -918,8 +962,10 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 __syncwarp();          // other lanes have written of the row
                 if (strange)
                     plain_row<D, MT>(a, seg, token, at, row, M, l);
-                __syncwarp();
             }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(segFree + 8 * at4);
         }
     } else {
         few_registers<MT>();

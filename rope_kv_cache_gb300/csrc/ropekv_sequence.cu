@@ -176,6 +176,7 @@ int run(RowsArgs& a, const Plan& p, int D, int Hkv, int64_t kvTokens, int64_t kv
     a.ctas = p.ctas;
     a.whole = p.whole;
     a.leastShare = p.leastShare;
+    a.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     a.divG = make_divisor(p.G);
     const Layout at = make_layout(p, D);
     a.joints = (ropekv_rows::Joint*)workspace;

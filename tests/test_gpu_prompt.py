@@ -182,6 +182,20 @@ def test_starts_out_of_range_read_and_write_within_the_tensors(starts):
     assert (guard[0] == 7).all() and (guard[65] == 7).all() and guard.isfinite().all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_out_at_every_multiple_of_16_bytes(D):
+    c = Case(same(70, 200), 4, 2, D, seed=8)
+    c.run()
+    c.verify()
+    want = c.out
+    for off in (8, 16, 24):
+        flat = torch.full((c.out.numel() + 64,), 7.0, dtype=torch.float16, device=DEV)
+        c.out = flat[off:off + want.numel()].view(want.shape)
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, want) and (flat[:off] == 7).all() and (flat[off + want.numel():] == 7).all()
+
+
 def test_nothing_to_do():
     import rope_kv_cache_gb300 as rk
     e = lambda *s: torch.empty(*s, dtype=torch.float16, device=DEV)
