@@ -592,7 +592,9 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     } else if (warp == kMma) {
         // ---------------------------------------------------------- products
         few_registers<MT>();
-        constexpr uint32_t kindS = mma_desc(TN, false), kindO = mma_desc(D, true);
+        // a negative smScale: -Q K^T (bit 13 negates A), scaled by |smScale|
+        const uint32_t kindS = mma_desc(TN, false) | (a.scaleLog2 < 0.0f ? 1u << 13 : 0u);
+        constexpr uint32_t kindO = mma_desc(D, true);
         bool ok = true;
         int n = 0, nq = 0, items = 0;               // loads taken, Q taken, items of a row tile before this segment
         auto acquire = [&]() -> int {
@@ -809,11 +811,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 tmem_load<TN>(s, sAddr);
                 tmem_wait_load();
                 pin<TN>(s);
-                if (a.scaleLog2 < 0.0f) {
-#pragma unroll
-                    for (int k = 0; k < TN; ++k)
-                        s[k] = -s[k];
-                }
                 const int t0 = (seg.j0 + j) * TN;
                 if (t0 + TN > allSee) {
 #pragma unroll
@@ -902,8 +899,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             const float inv = none ? 0.0f : 1.0f / l;
             const int at = (seg.qRow + token) * a.Hq + seg.head * a.G + g;      // row of out
             const int slot = seg.slot;
-            // two lanes write 64 bytes of one row, then of the other's
-            const int even = __shfl_sync(0xffffffffu, live ? at : -1, lane & ~1), odd = __shfl_sync(0xffffffffu, live ? at : -1, lane | 1);
             const bool plain = __all_sync(0xffffffffu, !none && !wrong);
             float nan0 = 0.0f, nan1 = 0.0f;                                     // NaN if an element is not finite
 #pragma unroll 1
@@ -934,20 +929,15 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                     }
                     continue;
                 }
-                uint32_t c[2][8];
+                uint32_t c[16];
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    c[0][z] = half2_sat(o[2 * z], o[2 * z + 1]);
-                    c[1][z] = half2_sat(o[16 + 2 * z], o[16 + 2 * z + 1]);
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? c[0][z] : c[1][z], 1);
-                    c[0][z] = lane & 1 ? got : c[0][z];
-                    c[1][z] = lane & 1 ? c[1][z] : got;
+                for (int z = 0; z < 16; ++z)
+                    c[z] = half2_sat(o[2 * z], o[2 * z + 1]);
+                if (live) {
+                    uint16_t* to = a.out + (size_t)at * D + k;
+                    store32(to, c, a.out32);
+                    store32(to + 16, c + 8, a.out32);
                 }
-                uint16_t* to = a.out + k + (lane & 1) * 16;
-                if (even >= 0)
-                    store32(to + (size_t)even * D, c[0], a.out32);
-                if (odd >= 0)
-                    store32(to + (size_t)odd * D, c[1], a.out32);
             }
             tmem_fence_before();
             if (live) {
