@@ -117,8 +117,10 @@ struct Segment : Sequence {
 struct Start {
     long long at, end;         // first step and the one behind the last, of all steps
     long long share;
-    long long inside;          // steps of sequence b before `at`
-    int b;                     // a.B: no work
+    long long inside;          // steps of the sequence before `at`
+    long long perHead;         // steps of one of its head groups
+    Sequence s;
+    int found;                 // 0: no work
 };
 
 constexpr int kSegments = 4;   // that are known ahead
@@ -353,22 +355,30 @@ __device__ __forceinline__ int tiles_of(const RowsArgs& a, const Sequence& s, in
     return (tile_limit(a, s.nq, s.base, s.nk, u * a.tokens) + TN - 1) / TN;
 }
 
-// sum of floor((a i + b) / m) over 0 <= i < n, all non-negative, by Euclid's steps on (a, m).
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b)
+// Sum of floor((a i + b) / m) over 0 <= i < n, all non-negative, by Euclid's steps on (a, m).
+template <typename U>
+__device__ __forceinline__ long long floor_sum(U n, U m, U a, U b)
 {
     long long sum = 0;
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const long long y = a * n + b;
+        const U qa = a / m, qb = b / m;
+        sum += (long long)((uint64_t)n * (n - 1) / 2 * qa + (uint64_t)n * qb);
+        a -= qa * m;
+        b -= qb * m;
+        const U y = a * n + b;
         n = y / m;
-        b = y % m;
-        const long long t = m;
+        b = y - n * m;
+        const U t = m;
         m = a;
         a = t;
     }
     return sum;
+}
+
+// x / y, by 32 bits where they do (a tenth of the time).
+__device__ __forceinline__ long long quotient(long long x, long long y)
+{
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // Steps of a head group's units before unit u, with their changes; a unit has one at least.
@@ -394,7 +404,13 @@ __device__ __forceinline__ long long steps_before(const RowsArgs& a, const Seque
         ones = min(ones, full);
         sum += (long long)(n - full) * max(1, (s.nk + TN - 1) / TN);
     }
-    return sum + ones + floor_sum(full - ones, TN, a.tokens, first + (long long)ones * a.tokens);
+    const long long from = first + (long long)ones * a.tokens;
+    const int rest = full - ones;
+    if (rest <= 0)
+        return sum + ones;
+    if (from + (long long)rest * a.tokens < (1LL << 31))
+        return sum + ones + floor_sum<uint32_t>(rest, TN, a.tokens, (uint32_t)from);
+    return sum + ones + floor_sum<uint64_t>(rest, TN, a.tokens, from);
 }
 
 template <int D, int MT, bool TREE>
@@ -403,9 +419,12 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
     constexpr int TN = RowsConfig<D, MT>::kTile, kThreads = RowsConfig<D, MT>::kThreads, kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    Sequence q;
+    long long perHead = 0;
     auto work = [&](int b) -> long long {
-        const Sequence s = sequence<TREE>(a, b);
-        return a.heads * steps_before<TN, TREE>(a, s, s.units);
+        q = sequence<TREE>(a, b);
+        perHead = steps_before<TN, TREE>(a, q, q.units);
+        return a.heads * perHead;
     };
     long long mine = 0;
     for (int b = b0; b < b1; ++b)
@@ -420,23 +439,26 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
         sums[warp] = sum;
     __syncthreads();
     long long before = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         before += w < warp ? sums[w] : 0;
         total += sums[w];
     }
     before += sum - mine;
-    const long long share = max((long long)a.leastShare, (total + a.ctas - 1) / a.ctas);
+    const long long share = max((long long)a.leastShare, quotient(total + a.ctas - 1, a.ctas));
     const long long at = share * blockIdx.x;
     if (threadIdx.x == 0 && at >= total)
-        *out = {at, at, share, 0, a.B};
+        out->found = 0;
     if (mine > 0 && at >= before && at < before + mine) {
-        int b = b0;
-        long long n = work(b);
-        while (at >= before + n) {
-            before += n;
-            n = work(++b);
+        if (per > 1) {
+            int b = b0;
+            long long n = work(b);
+            while (at >= before + n) {
+                before += n;
+                n = work(++b);
+            }
         }
-        *out = {at, min(total, at + share), share, at - before, b};
+        *out = {at, min(total, at + share), share, at - before, perHead, q, 1};
     }
 }
 
@@ -518,6 +540,10 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         }
         *failed = base & 1023;      // tiles of 1024 bytes: 0
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kLoad && lane < 3) {
+        const CUtensorMap* map = lane == 0 ? &mapQ : lane == 1 ? &mapK : &mapV;
+        asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
     }
     if (warp == kAlloc) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -711,20 +737,23 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         Joint joint = {};
         long long at = start.at;
         const long long end = start.end, share = start.share;
-        if (start.b < a.B) {
-            static_cast<Sequence&>(s) = sequence<TREE>(a, start.b);
-            const long long perHead = steps_before<TN, TREE>(a, s, s.units);
-            s.head = (int)(start.inside / perHead);
-            long long inside = start.inside - s.head * perHead;      // steps of the head group before `at`
+        if (start.found) {
+            static_cast<Sequence&>(s) = start.s;
+            s.head = (int)quotient(start.inside, start.perHead);
+            long long inside = start.inside - s.head * start.perHead;      // steps of the head group before `at`
             // the unit: the last with no more steps before it, by 32 guesses at a time
             int lo = 0, hi = s.units;
+            long long skip = 0;
             while (hi - lo > 1) {
                 const int width = (hi - lo + 31) / 32, u = min(hi, lo + lane * width);
-                const uint32_t fits = __ballot_sync(0xffffffffu, u < hi && steps_before<TN, TREE>(a, s, u) <= inside);
-                lo += (31 - __clz(fits)) * width;
+                const long long n = steps_before<TN, TREE>(a, s, u);
+                const uint32_t fits = __ballot_sync(0xffffffffu, u < hi && n <= inside);
+                const int best = 31 - __clz(fits);
+                skip = __shfl_sync(0xffffffffu, n, best);
+                lo += best * width;
                 hi = min(hi, lo + width);
             }
-            inside -= steps_before<TN, TREE>(a, s, lo);
+            inside -= skip;
             int unit = lo;
             while (ok && at < end) {
                 const int tiles = tiles_of<TN>(a, s, unit), len = kSwitch + max(1, tiles);
@@ -740,7 +769,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                     const bool all = r0 == 0 && r1 == len - kSwitch;
                     s.slot = all ? -1 : 2 * (int)blockIdx.x + (r0 == 0);
                     if (r0 == 0 && !all)
-                        joint = {s.qRow, s.tok0, s.nq, s.head, (int)((first + (len - kSwitch) - 1) / share - first / share) + 1};
+                        joint = {s.qRow, s.tok0, s.nq, s.head, (int)(quotient(first + (len - kSwitch) - 1, share) - quotient(first, share)) + 1};
                     publish(s);
                 }
                 at += take;
