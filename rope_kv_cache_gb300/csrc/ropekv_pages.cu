@@ -80,73 +80,80 @@ struct AcceptArgs {
     int32_t numPages, M, tpp;
 };
 
-// One CTA per sequence: a thread owns one 16-byte column of a row (of either plane and
-// any head) and takes the entries in order, eight at a time: their sources are read
+// One CTA per sequence. Entries are taken in order, eight at a time: one warp finds their rows,
+// then a thread moves one 16-byte column (of either plane and any head), all sources read
 // before the first of the eight is written. Entry j's source is at least j, every
-// destination before it is smaller, so nothing is overwritten that is still to move.
-// Scales are further columns of 4 bytes. Bound by latency: lens and entries, page ids,
-// rows, one after the other.
+// destination before it is smaller, so nothing is overwritten that is still to move, and a
+// column has the same thread throughout. Scales are further columns of 4 bytes. Bound by
+// latency: lengths and entries, page ids, rows, one after the other.
 template <bool PAGED>
 __global__ void __launch_bounds__(512) accept_kernel(const __grid_constant__ AcceptArgs a)
 {
     constexpr int kBatch = 8;
+    // rows of the plane (paged: page * tpp + place), below 0 where nothing moves
+    __shared__ int rows[2][2][kBatch];
     dependency_sync();
     const int b = blockIdx.x;
     const int len = a.lens[b];
     const int n = max(0, min(a.acceptedLens[b], min(a.A, a.S)));
     const int64_t base = (int64_t)len - a.S;
-    const int32_t* acc = a.accepted + (size_t)b * a.A;
     const int vecs = 2 * a.Hkv * a.rowVecs;
     const int items = vecs + (PAGED && a.scales != nullptr ? 2 * a.Hkv : 0);
-    for (int item = threadIdx.x; item < items; item += blockDim.x) {
-        const bool scale = item >= vecs;
-        const int ph = scale ? item - vecs : item / a.rowVecs;      // plane * Hkv + head
-        const int vec = scale ? 0 : item - ph * a.rowVecs;
-        const int plane = ph / a.Hkv, h = ph - plane * a.Hkv;
-        const int32_t* table = PAGED ? a.pageTable + ((size_t)b * 2 + plane) * a.M : nullptr;
-        // address of this column at a position, NULL where there is none
-        auto at = [&](int64_t pos) -> uint8_t* {
-            if (pos < 0 || pos >= a.cap)
-                return nullptr;
-            if (!PAGED)
-                return a.cache + ((((size_t)b * 2 + plane) * a.Hkv + h) * a.cap + pos) * a.rowVecs * 16 + vec * 16;
-            const int lp = (int)pos / a.tpp, in = (int)pos - lp * a.tpp;
-            const int64_t id = table[lp];
-            if (id < (int64_t)plane * a.numPages || id >= (int64_t)(plane + 1) * a.numPages)
-                return nullptr;
-            if (scale)
-                return reinterpret_cast<uint8_t*>(a.scales + ((size_t)id * a.Hkv + h) * a.tpp + in);
-            return a.cache + (((size_t)id * a.tpp + in) * a.Hkv + h) * a.rowVecs * 16 + vec * 16;
-        };
-        for (int j0 = 0; j0 < n; j0 += kBatch) {
+    for (int j0 = 0; j0 < n; j0 += kBatch) {
+        if (threadIdx.x < 32) {
+            const int plane = threadIdx.x >> 4, to = (threadIdx.x >> 3) & 1, j = j0 + (threadIdx.x & 7);
+            const int node = j < n ? a.accepted[(size_t)b * a.A + j] : -1;
+            const int64_t src = base + node, dst = base + j, pos = to ? dst : src;
+            int row = node > j && node < a.S && dst >= 0 && src < a.cap ? (int)pos : -1;   // node == j stays where it is
+            if (PAGED && row >= 0) {
+                const int lp = row / a.tpp;
+                const int64_t id = (int64_t)a.pageTable[((size_t)b * 2 + plane) * a.M + lp] - (int64_t)plane * a.numPages;
+                row = id >= 0 && id < a.numPages ? (int)id * a.tpp + (row - lp * a.tpp) : -1;
+            }
+            // both or neither
+            if (__shfl_xor_sync(0xffffffffu, row, 8) < 0)
+                row = -1;
+            rows[plane][to][threadIdx.x & 7] = row;
+        }
+        __syncthreads();
+        for (int item = threadIdx.x; item < items; item += blockDim.x) {
+            const bool scale = item >= vecs;
+            const int ph = scale ? item - vecs : item / a.rowVecs;      // plane * Hkv + head
+            const int vec = scale ? 0 : item - ph * a.rowVecs;
+            const int plane = ph >= a.Hkv, h = ph - plane * a.Hkv;
+            auto at = [&](int row) -> uint8_t* {
+                if (!PAGED)
+                    return a.cache + ((((size_t)b * 2 + plane) * a.Hkv + h) * a.cap + row) * a.rowVecs * 16 + vec * 16;
+                if (scale) {
+                    const int page = row / a.tpp;
+                    return reinterpret_cast<uint8_t*>(
+                        a.scales + (((size_t)plane * a.numPages + page) * a.Hkv + h) * a.tpp + (row - page * a.tpp));
+                }
+                return a.cache + (((size_t)plane * a.numPages * a.tpp + row) * a.Hkv + h) * a.rowVecs * 16 + vec * 16;
+            };
             uint4 x[kBatch];
-            uint8_t* to[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                to[k] = nullptr;
-                const int j = j0 + k;
-                const int node = j < n ? acc[j] : 0;
-                if (j >= n || node <= j || node >= a.S)    // node == j stays where it is
-                    continue;
-                const uint8_t* from = at(base + node);
-                to[k] = from != nullptr ? at(base + j) : nullptr;
-                if (to[k] == nullptr)
+                const int row = rows[plane][0][k];
+                if (row < 0)
                     continue;
                 if (scale)
-                    x[k].x = *reinterpret_cast<const uint32_t*>(from);
+                    x[k].x = *reinterpret_cast<const uint32_t*>(at(row));
                 else
-                    x[k] = *reinterpret_cast<const uint4*>(from);
+                    x[k] = *reinterpret_cast<const uint4*>(at(row));
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                if (to[k] == nullptr)
+                const int row = rows[plane][1][k];
+                if (row < 0)
                     continue;
                 if (scale)
-                    *reinterpret_cast<uint32_t*>(to[k]) = x[k].x;
+                    *reinterpret_cast<uint32_t*>(at(row)) = x[k].x;
                 else
-                    *reinterpret_cast<uint4*>(to[k]) = x[k];
+                    *reinterpret_cast<uint4*>(at(row)) = x[k];
             }
         }
+        __syncthreads();
     }
     __syncthreads();   // lensOut may be lens
     if (threadIdx.x == 0 && a.lensOut != nullptr && len >= a.S)
@@ -225,7 +232,7 @@ struct ForkArgs {
     int32_t* refCounts;        // [P]
     const int32_t* parents;    // [N]
     const int32_t* children;
-    int32_t* rank;             // [N] workspace: rank among the forks that need a page, or one of the below
+    struct Fork* forks;        // [N] workspace: what the plan decided
     int32_t* found;            // [1] workspace: free pages found, at most the number needed
     int32_t* fresh;            // [N] workspace: the free pages, ascending
     int32_t N, B, numPages, M, tpp, Hkv, chunks;
@@ -233,6 +240,14 @@ struct ForkArgs {
 };
 
 constexpr int kNoPage = -1, kSkipped = -2;
+
+struct __align__(16) Fork {
+    int rank;                  // among the forks that need a page, or one of the above
+    int parent, child;
+    int length;                // of the parent
+    int tail;                  // its partly filled page
+};
+static_assert(sizeof(Fork) == 32, "workspace");
 
 __device__ __forceinline__ int fork_length(const ForkArgs& a, int parent)
 {
@@ -267,57 +282,19 @@ __device__ __forceinline__ int scan1024(int x, int& sum, int* shared)
 // One CTA decides for all forks, so that free pages go out in the order of the forks,
 // lowest first, without atomics whose order could change it. Sequences named as parent, as
 // child and as child twice are bits in shared memory. The reference counts are read 16
-// pages a thread until there are enough free ones.
+// pages a thread until there are enough free ones; those of the first round, and of the first
+// 1024 forks all that depends on memory alone, are on their way before the bits are known
+// (192 forks over 1000 pages: 5 us as a launch of its own, four loads after one another).
 __global__ void __launch_bounds__(1024) fork_plan_kernel(const __grid_constant__ ForkArgs a)
 {
     extern __shared__ uint32_t bits[];
     __shared__ int sums[32];
-    dependency_sync();
     const int words = (a.B + 31) / 32;
     uint32_t *isParent = bits, *isChild = bits + words, *isTwice = bits + 2 * words;
     for (int i = threadIdx.x; i < 3 * words; i += 1024)
         bits[i] = 0;
-    __syncthreads();
-    auto valid = [&](int i, int& p, int& c) {
-        p = c = -1;
-        if (i >= a.N)
-            return false;
-        p = a.parents[i];
-        c = a.children[i];
-        return p >= 0 && p < a.B && c >= 0 && c < a.B;
-    };
-    for (int i = threadIdx.x; i < a.N; i += 1024) {
-        int p, c;
-        if (!valid(i, p, c))
-            continue;
-        atomicOr(isParent + (p >> 5), 1u << (p & 31));
-        const uint32_t bit = 1u << (c & 31);
-        if (atomicOr(isChild + (c >> 5), bit) & bit)
-            atomicOr(isTwice + (c >> 5), bit);
-    }
-    __syncthreads();
-    int needed = 0;
-    for (int i0 = 0; i0 < a.N; i0 += 1024) {
-        const int i = i0 + threadIdx.x;
-        int p, c;
-        const bool ok = valid(i, p, c) && !(((isTwice[c >> 5] | isParent[c >> 5]) >> (c & 31)) & 1) && a.kvLens[c] <= 0;
-        bool part = false;
-        if (ok) {
-            const int n = fork_length(a, p), whole = n / a.tpp;
-            if (n - whole * a.tpp > 0) {
-                const int id = a.pageTable[(size_t)p * 2 * a.M + whole];
-                part = id >= 0 && id < a.numPages;
-            }
-        }
-        int sum;
-        const int before = scan1024(part, sum, sums);
-        if (i < a.N)
-            a.rank[i] = !ok ? kSkipped : part ? needed + before : kNoPage;
-        needed += sum;
-    }
-    int found = 0;
-    for (int p0 = 0; p0 < a.numPages && found < needed; p0 += 16 * 1024) {
-        const int p = p0 + 16 * threadIdx.x;
+    dependency_sync();
+    auto free_pages = [&](int p) -> uint32_t {
         uint32_t freeBits = 0;
         if (p + 16 <= a.numPages) {
 #pragma unroll
@@ -329,6 +306,62 @@ __global__ void __launch_bounds__(1024) fork_plan_kernel(const __grid_constant__
             for (int k = 0; k < 16 && p + k < a.numPages; ++k)
                 freeBits |= (uint32_t)(a.refCounts[p + k] <= 0) << k;
         }
+        return freeBits;
+    };
+    // a fork as far as memory says: rank kSkipped, kNoPage, or 0 where a page is needed
+    auto read_fork = [&](int i) -> Fork {
+        Fork f = {kSkipped, -1, -1, 0, -1};
+        if (i >= a.N)
+            return f;
+        f.parent = a.parents[i];
+        f.child = a.children[i];
+        if (f.parent < 0 || f.parent >= a.B || f.child < 0 || f.child >= a.B) {
+            f.parent = f.child = -1;
+            return f;
+        }
+        f.length = fork_length(a, f.parent);
+        if (a.kvLens[f.child] > 0)
+            return f;
+        f.rank = kNoPage;
+        const int whole = f.length / a.tpp;
+        if (f.length - whole * a.tpp > 0) {
+            f.tail = a.pageTable[(size_t)f.parent * 2 * a.M + whole];
+            if (f.tail >= 0 && f.tail < a.numPages)
+                f.rank = 0;
+        }
+        return f;
+    };
+    const Fork mine = read_fork(threadIdx.x);
+    const uint32_t firstFree = free_pages(16 * threadIdx.x);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.N; i += 1024) {
+        const Fork f = i < 1024 ? mine : read_fork(i);
+        if (f.child < 0)
+            continue;
+        atomicOr(isParent + (f.parent >> 5), 1u << (f.parent & 31));
+        const uint32_t bit = 1u << (f.child & 31);
+        if (atomicOr(isChild + (f.child >> 5), bit) & bit)
+            atomicOr(isTwice + (f.child >> 5), bit);
+    }
+    __syncthreads();
+    int needed = 0;
+    for (int i0 = 0; i0 < a.N; i0 += 1024) {
+        const int i = i0 + threadIdx.x;
+        Fork f = i0 == 0 ? mine : read_fork(i);
+        if (f.child >= 0 && (((isTwice[f.child >> 5] | isParent[f.child >> 5]) >> (f.child & 31)) & 1))
+            f.rank = kSkipped;
+        int sum;
+        const int before = scan1024(f.rank == 0, sum, sums);
+        if (f.rank == 0)
+            f.rank = needed + before;
+        if (i < a.N)
+            a.forks[i] = f;
+        needed += sum;
+    }
+    int found = 0;
+    for (int p0 = 0; p0 < a.numPages && found < needed; p0 += 16 * 1024) {
+        const int p = p0 + 16 * threadIdx.x;
+        uint32_t freeBits = p0 == 0 ? firstFree : free_pages(p);
         int sum;
         int at = found + scan1024(__popc(freeBits), sum, sums);
         for (; freeBits != 0 && at < needed; freeBits &= freeBits - 1, ++at)
@@ -347,15 +380,24 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ 
     dependency_sync();
     const uint64_t pol = stream_policy();
     const int chunk = blockIdx.x % a.chunks, i = blockIdx.x / a.chunks;
-    const int rank = a.rank[i];
-    if (rank == kSkipped)
+    const Fork f = a.forks[i];
+    if (f.rank == kSkipped)
         return;
-    const int p = a.parents[i], c = a.children[i];
-    const int fresh = rank >= 0 && rank < *a.found ? a.fresh[rank] : -1;
-    const int n = fork_length(a, p), whole = n / a.tpp, rest = n - whole * a.tpp;
-    const int32_t* from = a.pageTable + (size_t)p * 2 * a.M;
+    const int whole = f.length / a.tpp, rest = f.length - whole * a.tpp;
+    // the source's rows need not wait for the destination
+    const int64_t vecs = f.rank >= 0 ? (int64_t)rest * a.rowVecs : 0, page = (int64_t)a.tpp * a.rowVecs;
+    const int64_t v0 = (int64_t)chunk * blockDim.x * kCopyUnroll + threadIdx.x;
+    uint4 x[2][kCopyUnroll];
+#pragma unroll
+    for (int plane = 0; plane < 2; ++plane)
+#pragma unroll
+        for (int k = 0; k < kCopyUnroll; ++k)
+            if (v0 + k * blockDim.x < vecs)
+                x[plane][k] = load16(a.cache + (((int64_t)plane * a.numPages + f.tail) * page + v0 + k * blockDim.x) * 16, pol);
+    const int fresh = f.rank >= 0 && f.rank < *a.found ? a.fresh[f.rank] : -1;
     if (chunk == 0) {
-        int32_t* to = a.pageTable + (size_t)c * 2 * a.M;
+        const int32_t* from = a.pageTable + (size_t)f.parent * 2 * a.M;
+        int32_t* to = a.pageTable + (size_t)f.child * 2 * a.M;
         for (int k = threadIdx.x; k < a.M; k += blockDim.x) {
             const int id = k < whole ? from[k] : -1;
             const bool mapped = id >= 0 && id < a.numPages;
@@ -366,23 +408,13 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ 
             to[a.M + k] = mine >= 0 ? mine + a.numPages : -1;
         }
         if (threadIdx.x == 0) {
-            a.kvLens[c] = fresh >= 0 || rest == 0 ? n : whole * a.tpp;
+            a.kvLens[f.child] = fresh >= 0 || rest == 0 ? f.length : whole * a.tpp;
             if (fresh >= 0)
                 a.refCounts[fresh] = 1;
         }
     }
     if (fresh < 0)
         return;
-    const int tail = from[whole];
-    const int64_t vecs = (int64_t)rest * a.rowVecs, page = (int64_t)a.tpp * a.rowVecs;
-    const int64_t v0 = (int64_t)chunk * blockDim.x * kCopyUnroll + threadIdx.x;
-    uint4 x[2][kCopyUnroll];
-#pragma unroll
-    for (int plane = 0; plane < 2; ++plane)
-#pragma unroll
-        for (int k = 0; k < kCopyUnroll; ++k)
-            if (v0 + k * blockDim.x < vecs)
-                x[plane][k] = load16(a.cache + (((int64_t)plane * a.numPages + tail) * page + v0 + k * blockDim.x) * 16, pol);
 #pragma unroll
     for (int plane = 0; plane < 2; ++plane)
 #pragma unroll
@@ -394,7 +426,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ 
         for (int64_t k = (int64_t)chunk * blockDim.x + threadIdx.x; k < all; k += (int64_t)a.chunks * blockDim.x) {
             const int plane = k >= row, h = (int)((k - plane * row) / rest), t = (int)((k - plane * row) - (int64_t)h * rest);
             const size_t at = ((size_t)plane * a.numPages * a.Hkv + h) * a.tpp + t, step = (size_t)a.Hkv * a.tpp;
-            a.scales[at + fresh * step] = a.scales[at + tail * step];
+            a.scales[at + fresh * step] = a.scales[at + f.tail * step];
         }
     }
 }
@@ -546,7 +578,7 @@ int64_t paged_kv_fork_workspace_size(int32_t numForks, int32_t batch)
 {
     if (numForks < 0 || numForks > (1 << 20) || batch < 0 || batch > (1 << 18))
         return ROPEKV_ERR_SHAPE;
-    return 16 + 2 * up16(4LL * numForks);
+    return 16 + (int64_t)sizeof(Fork) * numForks + up16(4LL * numForks);
 }
 
 int paged_kv_fork(void* kvCache, float* kvScales, int32_t* pageTable, int32_t* kvLens,
@@ -576,7 +608,7 @@ int paged_kv_fork(void* kvCache, float* kvScales, int32_t* pageTable, int32_t* k
         return ROPEKV_ERR_CAPACITY;
     uint8_t* ws = (uint8_t*)workspace;
     ForkArgs a = {(uint8_t*)kvCache, f16 ? nullptr : kvScales, pageTable, kvLens, refCounts, parents, children,
-                  (int32_t*)(ws + 16), (int32_t*)ws, (int32_t*)(ws + 16 + up16(4LL * numForks)), numForks, batch,
+                  (Fork*)(ws + 16), (int32_t*)ws, (int32_t*)(ws + 16 + sizeof(Fork) * (size_t)numForks), numForks, batch,
                   numPages, maxPagesPerSeq, tokensPerPage, numKVHeads, 0,
                   (int64_t)numKVHeads * headDim / (f16 ? 8 : 16)};
     const int64_t vecs = tokensPerPage * a.rowVecs, chunks = (vecs + 256 * kCopyUnroll - 1) / (256 * kCopyUnroll);
