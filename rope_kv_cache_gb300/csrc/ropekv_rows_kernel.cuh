@@ -191,8 +191,8 @@ __device__ __forceinline__ uint32_t sees32(const RowsArgs& a, const int32_t* wor
     if (words != nullptr && t0 + 32 > base) {
         const int j = t0 - base;           // first new token of the 32
         const int w = j >> 5, sh = j & 31;
-        const uint32_t lo = w >= 0 && w < a.W ? (uint32_t)__ldg(words + w) : w < 0 ? 0xffffffffu : 0u;
-        const uint32_t hi = w + 1 >= 0 && w + 1 < a.W ? (uint32_t)__ldg(words + w + 1) : 0u;
+        const uint32_t lo = w >= 0 && w < a.W ? (uint32_t)words[w] : w < 0 ? 0xffffffffu : 0u;
+        const uint32_t hi = w + 1 >= 0 && w + 1 < a.W ? (uint32_t)words[w + 1] : 0u;
         bits &= __funnelshift_r(lo, hi, sh);
     }
     return bits;
