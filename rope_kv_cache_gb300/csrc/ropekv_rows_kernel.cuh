@@ -80,7 +80,7 @@ struct RowsArgs {
     int32_t tokens;            // tokens of a CTA's tiles: 128 MT / G
     int32_t tilesSeq;          // tree: units of a sequence and head group
     int32_t ctas;
-    int32_t whole;             // units are not split: each goes to the CTA in whose share it begins
+    int32_t whole;             // no unit can be long enough to be split: there is nothing to join
     int32_t leastShare;        // steps of a share, at least
     int32_t out32;             // out is a multiple of 32 bytes, not of 16 alone
     Divisor divG;
@@ -93,6 +93,16 @@ struct Joint {
 
 // Steps that changing from one unit to the next costs.
 constexpr int kSwitch = 3;
+
+// Splitting units costs about so many steps: their pieces are written, read and joined. So
+// units are left whole, and each goes to the CTA in whose share it begins, where the longest
+// takes no more than that above a share (or, where shares are longer than units, about that at
+// all). Whole against split, 32 query and 8 KV heads of 128: one prompt of 512 tokens 15.5
+// against 19.5 us, of 1024 21.8 against 25.9, 16 of 500 62.7 against 65.1; 8 of 1000 (not left
+// whole) 86.0 against 83.8; 64 decoding sequences of 100 to 200 tokens 27.4 against 29.6; one
+// tree of 26 drafts behind 900 tokens (not left whole) 13.5 against 10.7.
+template <int MT>
+constexpr int kSplit = MT == 2 ? 8 : 4;
 
 // A sequence as the kernel sees it.
 struct Sequence {
@@ -121,6 +131,7 @@ struct Start {
     long long perHead;         // steps of one of its head groups
     Sequence s;
     int found;                 // 0: no work
+    int whole;                 // units are not split: each goes to the CTA in whose share it begins
 };
 
 constexpr int kSegments = 4;   // that are known ahead
@@ -145,7 +156,7 @@ struct RowsConfig {
     static constexpr int kOffSegs = (kOffBar + kBars * 8 + 15) / 16 * 16;
     static constexpr int kOffStart = kOffSegs + kSegments * (int)sizeof(Segment);
     static constexpr int kOffSums = (kOffStart + (int)sizeof(Start) + 15) / 16 * 16;
-    static constexpr int kOffFlags = kOffSums + kThreads / 32 * 8;
+    static constexpr int kOffFlags = kOffSums + kThreads / 32 * 16;
     static constexpr int kSmem = kOffFlags + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kColO + MT * D <= kCols, "TMEM");
@@ -427,25 +438,34 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
         return a.heads * perHead;
     };
     long long mine = 0;
-    for (int b = b0; b < b1; ++b)
+    int longest = 0;
+    for (int b = b0; b < b1; ++b) {
         mine += work(b);
+        longest = max(longest, q.units > 0 ? q.nk : 0);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     long long sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, sum, d);
         sum += lane >= d ? y : 0;
     }
-    if (lane == 31)
-        sums[warp] = sum;
+    if (lane == 31) {
+        sums[2 * warp] = sum;
+        sums[2 * warp + 1] = longest;
+    }
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        before += w < warp ? sums[w] : 0;
-        total += sums[w];
+        before += w < warp ? sums[2 * w] : 0;
+        total += sums[2 * w];
+        longest = max(longest, (int)sums[2 * w + 1]);
     }
     before += sum - mine;
     const long long share = max((long long)a.leastShare, quotient(total + a.ctas - 1, a.ctas));
+    longest = (longest + TN - 1) / TN + kSwitch;
+    const int whole = a.whole || longest <= (share >= longest ? 2 : share) + kSplit<MT>;
     const long long at = share * blockIdx.x;
     if (threadIdx.x == 0 && at >= total)
         out->found = 0;
@@ -458,7 +478,7 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
                 n = work(++b);
             }
         }
-        *out = {at, min(total, at + share), share, at - before, perHead, q, 1};
+        *out = {at, min(total, at + share), share, at - before, perHead, q, 1, whole};
     }
 }
 
@@ -759,10 +779,10 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 const int tiles = tiles_of<TN>(a, s, unit), len = kSwitch + max(1, tiles);
                 const long long first = at - inside + kSwitch;       // of the unit's real steps, among all
                 long long take = min((long long)len - inside, end - at);
-                if (a.whole)
+                if (start.whole)
                     take = len - inside;                             // nothing of a unit that began before
                 const int r0 = max(0, (int)inside - kSwitch), r1 = max(0, (int)(inside + take) - kSwitch);
-                if (a.whole ? inside == 0 : r1 > r0) {
+                if (start.whole ? inside == 0 : r1 > r0) {
                     s.tok0 = unit * a.tokens;
                     s.j0 = min(r0, tiles);
                     s.j1 = min(r1, tiles);

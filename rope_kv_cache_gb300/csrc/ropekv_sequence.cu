@@ -127,7 +127,7 @@ Plan make_plan(bool tree, int64_t T, int B, int S, int Hq, int Hkv, int D, int64
     // at most so many units, of so many K/V tiles
     const int64_t units = (tree ? (int64_t)B * p.tilesSeq : T / p.tokens + std::min<int64_t>(B, T)) * p.heads;
     const int64_t tiles = std::max<int64_t>(1, (keys + (D == 256 ? 63 : 127)) / (D == 256 ? 64 : 128));
-    p.whole = tiles <= 2;
+    p.whole = tiles + ropekv_rows::kSwitch <= 2 + (p.mt == 2 ? ropekv_rows::kSplit<2> : ropekv_rows::kSplit<1>);
     p.leastShare = 4;
     p.ctas = (int)std::min<int64_t>(kSMs, p.whole ? units : units * ((tiles + ropekv_rows::kSwitch + p.leastShare - 1) / p.leastShare));
     return p;
@@ -283,7 +283,10 @@ int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k,
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(qStarts) || !aligned16(kvStarts) ||
         !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
         return ROPEKV_ERR_MISALIGNED;
-    if (overlap(q, (dims->numTokens - 1) * qTokenStride + Hq * D, out, dims->numTokens * Hq * D))
+    const int64_t size = dims->numTokens * Hq * D, last = std::max(0, dims->numKVTokens - 1);
+    if (overlap(q, (dims->numTokens - 1) * qTokenStride + Hq * D, out, size) ||
+        (dims->numKVTokens > 0 && (overlap(k, last * kTokenStride + Hkv * D, out, size) ||
+                                   overlap(v, last * vTokenStride + Hkv * D, out, size))))
         return ROPEKV_ERR_SHAPE;
     const Plan p = plan_of(dims);
     if (workspaceBytes < make_layout(p, dims->headDim).size)
@@ -338,12 +341,13 @@ int tree_attention(const uint16_t* q, const uint16_t* kvCache, const int32_t* kv
         !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
         return ROPEKV_ERR_MISALIGNED;
     const int64_t T = (int64_t)dims->batch * dims->seqLen, row = (int64_t)dims->numQHeads * dims->headDim;
-    if (overlap(q, T * row, out, T * row))
+    const int64_t cap = std::max(1, dims->kvCapacity), plane = cap * dims->numKVHeads * dims->headDim;
+    if (overlap(q, T * row, out, T * row) ||
+        (dims->kvCapacity > 0 && overlap(kvCache, 2 * dims->batch * plane, out, T * row)))
         return ROPEKV_ERR_SHAPE;
     const Plan p = plan_of(dims);
     if (workspaceBytes < make_layout(p, dims->headDim).size)
         return ROPEKV_ERR_CAPACITY;
-    const int64_t cap = std::max(1, dims->kvCapacity), plane = cap * dims->numKVHeads * dims->headDim;
     RowsArgs a = {};
     a.q = q;
     a.k = dims->kvCapacity > 0 ? kvCache : q;

@@ -210,6 +210,17 @@ def test_forks_without_free_pages():
         rk.paged_kv_fork(s.cache, *s.g, i32([0]), i32([1]), kv_scales=s.scales, workspace=ws[:16])
 
 
+def test_page_0_is_a_page_like_any_other():
+    """Page 0 is free and goes to the first fork; the forks behind it have no partly filled page."""
+    s = Pool(random.Random(2), 6, 3, 8, 16, 2, 64, "f16", [])
+    s.table[0], s.lens[0] = [[5, 2, -1], [13, 10, -1]], 20
+    s.table[1], s.lens[1] = [[7, -1, -1], [15, -1, -1]], 16
+    s.refs[:] = [0, 1, 1, 1, 1, 1, 0, 1]
+    s.g = [i32(s.table), i32(s.lens), i32(s.refs)]
+    s.fork([0, 1, 1, 0], [2, 3, 4, 5])
+    assert s.table[2][0] == [5, 0, -1] and s.table[5][0] == [5, 6, -1] and s.table[3][0] == [7, -1, -1]
+
+
 def test_many_forks_over_a_large_pool():
     """More forks than one scan takes, free pages far up among 70000."""
     import rope_kv_cache_gb300 as rk

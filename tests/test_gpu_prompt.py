@@ -93,7 +93,8 @@ def test_chunks_behind_a_context_and_queries_that_see_nothing(seqs, D):
     c.verify()
 
 
-@pytest.mark.parametrize("lens", [[3] * 200, [1] * 500, [0] * 40 + [9] + [0] * 70 + [130, 0], list(range(70))])
+@pytest.mark.parametrize("lens", [[3] * 200, [1] * 500, [0] * 40 + [9] + [0] * 70 + [130, 0], list(range(70)),
+                                  [(7 * b) % 4 for b in range(2000)], [0] * 900 + [300] + [0] * 900])
 def test_many_sequences(lens):
     c = Case(same(*lens), 4, 1, 64, seed=len(lens), lead=1, trail=1)
     c.run()

@@ -43,6 +43,7 @@ def pdims(**kw):
 def prompt(lib, ptrs=None, qs=48 * 128, ks=48 * 128, vs=48 * 128, size=1 << 40, scale=0.1, **kw):
     #          q  k  v  q_starts kv_starts out lse workspace
     p = ptrs or [A, A, A, A, A, FAR, A, A]
+    # (the inputs may lie over one another)
     return lib.prompt_attention(p[0], qs, p[1], ks, p[2], vs, *p[3:], size, ctypes.byref(pdims(**kw)), scale, NUL)
 
 
@@ -62,7 +63,9 @@ def test_prompt_refuses_bad_arguments(lib):
         if i not in (4, 6):                  # kv_starts and lse may be NULL
             assert prompt(lib, ptrs=ptrs) == NULL, i
     assert prompt(lib, ptrs=[A] * 8) == SHAPE                                   # out over q
-    assert prompt(lib, ptrs=[A, A, A, A, A, ctypes.c_void_p(0x10000 + 2 * (99 * 48 + 31) * 128), A, A]) == SHAPE
+    last = ctypes.c_void_p(0x10000 + 2 * (99 * 48 + 31) * 128)                  # over q's last head alone
+    assert prompt(lib, ptrs=[A, FAR, FAR, A, A, last, A, A]) == SHAPE
+    assert prompt(lib, ptrs=[FAR, A, FAR, A, A, A, A, A]) == SHAPE and prompt(lib, ptrs=[FAR, FAR, A, A, A, A, A, A]) == SHAPE
     need = lib.prompt_attention_workspace_size(ctypes.byref(pdims(numTokens=1000, numKVTokens=1000)))
     assert need > 0 and prompt(lib, numTokens=1000, numKVTokens=1000, size=need - 1) == CAPACITY
     assert prompt(lib, numTokens=0, ptrs=[NUL] * 8, size=0) == OK and prompt(lib, batch=0, ptrs=[NUL] * 8, size=0) == OK
@@ -95,7 +98,8 @@ def test_tree_refuses_bad_arguments(lib):
         ptrs[i] = NUL
         if i not in (3, 5):                  # tree_mask and lse may be NULL
             assert tree(lib, ptrs=ptrs) == NULL, i
-    assert tree(lib, ptrs=[A] * 7) == SHAPE                                     # out over q
+    assert tree(lib, ptrs=[A] * 7) == SHAPE and tree(lib, ptrs=[A, FAR, A, A, A, A, A]) == SHAPE     # out over q
+    assert tree(lib, ptrs=[FAR, A, A, A, A, A, A]) == SHAPE                     # out over the cache
     need = lib.tree_attention_workspace_size(ctypes.byref(tdims()))
     assert need > 0 and tree(lib, size=need - 1) == CAPACITY
     for kw in (dict(batch=0), dict(seqLen=0)):
