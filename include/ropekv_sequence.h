@@ -102,7 +102,8 @@ ROPEKV_API int64_t tree_attention_workspace_size(const ropekv_tree_dims* dims);
  * sequence, kvCacheEndLens[b] = 0, for one) gets a zero row and lse = -infinity. What
  * lies in slots that no token sees does not matter, whatever its bits.
  * Host errors: negative sizes, seqLen > 2^15, kvCapacity > 2^28, batch * seqLen * Hq >
- * 2^31 - 1, kvCapacity * Hkv * D > 2^37, smScale not finite, out overlapping q or
+ * 2^31 - 1, kvCapacity * Hkv * D > 2^37 or, times batch,
+ * 2^40, smScale not finite, out overlapping q or
  * kvCache -> ROPEKV_ERR_SHAPE; workspaceBytes too small -> ROPEKV_ERR_CAPACITY.
  */
 ROPEKV_API int tree_attention(const uint16_t* q, const uint16_t* kvCache,

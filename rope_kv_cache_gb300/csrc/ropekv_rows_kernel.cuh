@@ -136,17 +136,20 @@ struct Start {
 
 constexpr int kSegments = 4;   // that are known ahead
 
-template <int D, int MT>
+template <int D, int MT, int PER>
 struct RowsConfig {
     static constexpr int kTile = D == 256 ? 64 : 128;      // keys of a K/V tile
-    static constexpr int kSlots = MT == 2 ? 1 : D == 256 ? 4 : 2;   // of S per row tile
+    static constexpr int kPerSm = PER;                     // CTAs of an SM
+    static_assert(PER == 1 || (PER == 2 && MT == 1 && D <= 128), "TMEM and shared memory of a half");
+    static constexpr int kSlots = MT == 2 || kPerSm == 2 ? 1 : D == 256 ? 4 : 2;   // of S per row tile
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kQBytes = MT * 128 * D * 2;
-    static constexpr int kStages = (216 * 1024 - kQBytes) / kTileBytes > 8 ? 8 : (224 * 1024 - kQBytes) / kTileBytes;
+    static constexpr int kFit = ((kPerSm == 2 ? 108 : 224) * 1024 - kQBytes) / kTileBytes;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSoftmax = MT * 128;
     static constexpr int kThreads = kSoftmax + 128;
     static constexpr int kColO = MT * kSlots * kTile;
-    static constexpr int kCols = 512;
+    static constexpr int kCols = 512 / kPerSm;
     // barriers: full, empty of the stages; S full, the two halves of P, O done of the slots (a
     // wait tells only the last two phases of a barrier apart, and O(j - kSlots) is done when S(j)
     // is); Q full, Q free; full, free of the segments
@@ -158,7 +161,7 @@ struct RowsConfig {
     static constexpr int kOffSums = (kOffStart + (int)sizeof(Start) + 15) / 16 * 16;
     static constexpr int kOffFlags = kOffSums + kThreads / 32 * 16;
     static constexpr int kSmem = kOffFlags + 16;
-    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
     static_assert(kColO + MT * D <= kCols, "TMEM");
 };
 
@@ -281,7 +284,7 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* r, bool who
 template <int D, int MT>
 __device__ __noinline__ void plain_row(const RowsArgs& a, const Segment& s, int token, int at, int row, float m, float l)
 {
-    constexpr int TN = RowsConfig<D, MT>::kTile;
+    constexpr int TN = RowsConfig<D, MT, 1>::kTile;
     const int kvHead = s.head / a.headsPerKv;
     const int limit = min(row_limit(a, s, token), s.j1 * TN);
     const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)s.b * a.S + token) * a.W : nullptr;
@@ -407,11 +410,11 @@ __device__ __forceinline__ long long steps_before(const RowsArgs& a, const Seque
     if (n <= 0)
         return sum;
     const long long first = (long long)s.base + a.tokens + TN - 1;        // floor(first / TN) tiles of unit 0
-    int ones = first >= 2 * TN ? 0 : (int)min((long long)n, (2 * TN - first + a.tokens - 1) / a.tokens);
+    int ones = first >= 2 * TN ? 0 : min(n, ((int)(2 * TN - first) + a.tokens - 1) / a.tokens);
     // a tree's units behind the cache's end see nk
     int full = n;
     if (TREE && (long long)s.base + (long long)n * a.tokens > s.nk) {
-        full = s.nk <= s.base ? 0 : (int)min((long long)n, ((long long)s.nk - s.base) / a.tokens);
+        full = s.nk <= s.base ? 0 : min(n, (s.nk - s.base) / a.tokens);
         ones = min(ones, full);
         sum += (long long)(n - full) * max(1, (s.nk + TN - 1) / TN);
     }
@@ -424,10 +427,10 @@ __device__ __forceinline__ long long steps_before(const RowsArgs& a, const Seque
     return sum + ones + floor_sum<uint64_t>(rest, TN, a.tokens, from);
 }
 
-template <int D, int MT, bool TREE>
+template <int D, int MT, int PER, bool TREE>
 __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, Start* out)
 {
-    constexpr int TN = RowsConfig<D, MT>::kTile, kThreads = RowsConfig<D, MT>::kThreads, kWarps = kThreads / 32;
+    constexpr int TN = RowsConfig<D, MT, PER>::kTile, kThreads = RowsConfig<D, MT, PER>::kThreads, kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
     Sequence q;
@@ -483,19 +486,24 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
 }
 
 // The softmax warps, which hold kTile scores a thread, take registers of the others: 256 x 208 +
-// 128 x 88 are the 384 x 168 of the launch with two row tiles.
-template <int MT>
+// 128 x 88 are the 384 x 168 of the launch with two row tiles, 128 x 184 + 128 x 72 the 256 x 128
+// of one of two CTAs on an SM.
+template <typename C>
 __device__ __forceinline__ void few_registers()
 {
-    if constexpr (MT == 2)
+    if constexpr (C::kThreads == 384)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else if constexpr (C::kPerSm == 2)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 }
 
-template <int MT>
+template <typename C>
 __device__ __forceinline__ void more_registers()
 {
-    if constexpr (MT == 2)
+    if constexpr (C::kThreads == 384)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else if constexpr (C::kPerSm == 2)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -520,12 +528,12 @@ __device__ __forceinline__ uint32_t half2_sat(float lo, float hi)
     return d;
 }
 
-template <int D, int MT, bool TREE>
-__global__ void __launch_bounds__(RowsConfig<D, MT>::kThreads, 1)
+template <int D, int MT, int PER, bool TREE>
+__global__ void __launch_bounds__(RowsConfig<D, MT, PER>::kThreads, RowsConfig<D, MT, PER>::kPerSm)
 rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap mapQ,
             const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV)
 {
-    using C = RowsConfig<D, MT>;
+    using C = RowsConfig<D, MT, PER>;
     constexpr int TN = C::kTile, NS = C::kStages, SL = C::kSlots, LA = SL;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
@@ -571,7 +579,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    find_start<D, MT, TREE>(a, reinterpret_cast<long long*>(smem + C::kOffSums), &start);
+    find_start<D, MT, PER, TREE>(a, reinterpret_cast<long long*>(smem + C::kOffSums), &start);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -592,7 +600,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
 
     if (warp == kLoad) {
         // --------------------------------------------------------------- TMA
-        few_registers<MT>();
+        few_registers<C>();
         bool ok = true;
         int n = 0, nq = 0;                          // loads of K and V, of Q so far
         Segment seg;
@@ -637,7 +645,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             mbar_drain(full + 8 * (i % NS), (i / NS) & 1);
     } else if (warp == kMma) {
         // ---------------------------------------------------------- products
-        few_registers<MT>();
+        few_registers<C>();
         // a negative smScale: -Q K^T (bit 13 negates A), scaled by |smScale|
         const uint32_t kindS = mma_desc(TN, false) | (a.scaleLog2 < 0.0f ? 1u << 13 : 0u);
         constexpr uint32_t kindO = mma_desc(D, true);
@@ -740,7 +748,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             mbar_wait_warp(qFree, (nq - 1) & 1, failed);
     } else if (warp == kAlloc) {
         // ---------------------------------------------------------- segments
-        few_registers<MT>();
+        few_registers<C>();
         bool ok = true;
         int n = 0;
         auto publish = [&](const Segment& s) {
@@ -816,7 +824,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             a.joints[blockIdx.x] = joint;
     } else if (warp < 4 * MT) {
         // ----------------------------------------------------------- softmax
-        more_registers<MT>();
+        more_registers<C>();
         const int tile = warp >> 2;
         const int row = (int)threadIdx.x;                       // of the CTA's tiles
         const uint32_t laneBase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -1007,7 +1015,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 mbar_arrive(segFree + 8 * at4);
         }
     } else {
-        few_registers<MT>();
+        few_registers<C>();
     }
     // the join may start; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

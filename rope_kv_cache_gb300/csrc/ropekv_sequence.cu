@@ -99,6 +99,7 @@ bool make_map(CUtensorMap* map, const uint16_t* p, int D, int64_t d1, int64_t s1
 // How a call is cut, from its sizes alone (the shares follow from the lengths, on the device).
 struct Plan {
     int mt;                   // row tiles of a CTA
+    int perSm;                // CTAs of an SM
     int G, heads, tokens;     // heads of a tile, head groups, tokens of a CTA's tiles
     int tilesSeq;             // tree: CTA tiles of a sequence
     int ctas;
@@ -121,6 +122,9 @@ Plan make_plan(bool tree, int64_t T, int B, int S, int Hq, int Hkv, int D, int64
     p.G = group_of(Hq, Hkv);
     p.heads = Hq / p.G;
     const int64_t rows = (tree ? S : (T + B - 1) / std::max(1, B)) * (int64_t)p.G;     // of a sequence, in mean
+    // Two row tiles share K and V and alternate. One tile and two CTAs of an SM in their place, D =
+    // 128: 32 prompts of 300 tokens 78 us instead of 68, one of 8000 385 instead of 340; at 100
+    // tokens 46 instead of 41.
     p.mt = D != 256 && rows > 128 ? 2 : 1;
     p.tokens = 128 * p.mt / p.G;
     p.tilesSeq = (S + p.tokens - 1) / p.tokens;
@@ -129,7 +133,15 @@ Plan make_plan(bool tree, int64_t T, int B, int S, int Hq, int Hkv, int D, int64
     const int64_t tiles = std::max<int64_t>(1, (keys + (D == 256 ? 63 : 127)) / (D == 256 ? 64 : 128));
     p.whole = tiles + ropekv_rows::kSwitch <= 2 + (p.mt == 2 ? ropekv_rows::kSplit<2> : ropekv_rows::kSplit<1>);
     p.leastShare = 4;
-    p.ctas = (int)std::min<int64_t>(kSMs, p.whole ? units : units * ((tiles + ropekv_rows::kSwitch + p.leastShare - 1) / p.leastShare));
+    // One row tile: two CTAs of an SM overlap what a step and a change of units wait for, at the
+    // cost of scores looked ahead and of stages in flight, which few units, and long ones of
+    // 128 dims, need more. One against two, 32 query and 8 KV heads: 200 prompts of 30 tokens 52
+    // against 42 us (D = 128), 47 against 29 (D = 64); 64 decoding sequences of 100 to 200 tokens 27
+    // against 19; 128 of 2000 to 4000, D = 64, 151 against 132; 16 trees of 26 drafts behind 2000
+    // to 4000, D = 128, 49 against 52; one decoding sequence of 16000, D = 64, 17.3 against 18.7.
+    const int64_t mean = tree ? tiles : (tiles + B - 1) / std::max(1, B);
+    p.perSm = p.mt == 1 && D != 256 && units >= kSMs / 2 && (D == 64 || mean <= 8) ? 2 : 1;
+    p.ctas = (int)std::min<int64_t>(kSMs * p.perSm, p.whole ? units : units * ((tiles + ropekv_rows::kSwitch + p.leastShare - 1) / p.leastShare));
     return p;
 }
 
@@ -151,12 +163,12 @@ Layout make_layout(const Plan& p, int D)
     return w;
 }
 
-template <int D, int MT, bool TREE>
+template <int D, int MT, int PER, bool TREE>
 int launch_rows(const RowsArgs& a, const Plan& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                 cudaStream_t st)
 {
-    constexpr auto kern = ropekv_rows::rows_kernel<D, MT, TREE>;
-    using C = RowsConfig<D, MT>;
+    constexpr auto kern = ropekv_rows::rows_kernel<D, MT, PER, TREE>;
+    using C = RowsConfig<D, MT, PER>;
     if (!raise_smem<kern>(C::kSmem))
         return ROPEKV_ERR_LAUNCH;
     const int rc = launch(kern, p.ctas, C::kThreads, C::kSmem, true, st, a, q, k, v);
@@ -190,9 +202,13 @@ int run(RowsArgs& a, const Plan& p, int D, int Hkv, int64_t kvTokens, int64_t kv
         !make_map(&v, a.v, D, kvTokens, a.vTok, Hkv, a.kvHead, kvBatches, batchStride, tile, 1))
         return ROPEKV_ERR_LAUNCH;
     switch (D) {
-    case 64: return p.mt == 2 ? launch_rows<64, 2, TREE>(a, p, q, k, v, st) : launch_rows<64, 1, TREE>(a, p, q, k, v, st);
-    case 128: return p.mt == 2 ? launch_rows<128, 2, TREE>(a, p, q, k, v, st) : launch_rows<128, 1, TREE>(a, p, q, k, v, st);
-    default: return launch_rows<256, 1, TREE>(a, p, q, k, v, st);
+    case 64:
+        return p.mt == 2 ? launch_rows<64, 2, 1, TREE>(a, p, q, k, v, st)
+             : p.perSm == 2 ? launch_rows<64, 1, 2, TREE>(a, p, q, k, v, st) : launch_rows<64, 1, 1, TREE>(a, p, q, k, v, st);
+    case 128:
+        return p.mt == 2 ? launch_rows<128, 2, 1, TREE>(a, p, q, k, v, st)
+             : p.perSm == 2 ? launch_rows<128, 1, 2, TREE>(a, p, q, k, v, st) : launch_rows<128, 1, 1, TREE>(a, p, q, k, v, st);
+    default: return launch_rows<256, 1, 1, TREE>(a, p, q, k, v, st);
     }
 }
 
@@ -232,7 +248,8 @@ int check_tree(const ropekv_tree_dims* d)
         return rc;
     if (d->batch < 0 || d->seqLen < 0 || d->seqLen > (1 << 15) || d->kvCapacity < 0 || d->kvCapacity > (1 << 28) ||
         (long long)d->batch * d->seqLen > 0x7FFFFFFFLL / d->numQHeads ||
-        (long long)d->kvCapacity * d->numKVHeads > (1LL << 37) / d->headDim)
+        (long long)d->kvCapacity * d->numKVHeads > (1LL << 37) / d->headDim ||
+        (long long)d->kvCapacity * d->numKVHeads * d->headDim > (1LL << 40) / std::max(1, d->batch))
         return ROPEKV_ERR_SHAPE;
     return ROPEKV_OK;
 }
@@ -343,7 +360,7 @@ int tree_attention(const uint16_t* q, const uint16_t* kvCache, const int32_t* kv
     const int64_t T = (int64_t)dims->batch * dims->seqLen, row = (int64_t)dims->numQHeads * dims->headDim;
     const int64_t cap = std::max(1, dims->kvCapacity), plane = cap * dims->numKVHeads * dims->headDim;
     if (overlap(q, T * row, out, T * row) ||
-        (dims->kvCapacity > 0 && overlap(kvCache, 2 * dims->batch * plane, out, T * row)))
+        (dims->kvCapacity > 0 && overlap(kvCache, 2LL * dims->batch * plane, out, T * row)))
         return ROPEKV_ERR_SHAPE;
     const Plan p = plan_of(dims);
     if (workspaceBytes < make_layout(p, dims->headDim).size)

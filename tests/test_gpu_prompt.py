@@ -95,8 +95,9 @@ def test_chunks_behind_a_context_and_queries_that_see_nothing(seqs, D):
 
 @pytest.mark.parametrize("lens", [[3] * 200, [1] * 500, [0] * 40 + [9] + [0] * 70 + [130, 0], list(range(70)),
                                   [(7 * b) % 4 for b in range(2000)], [0] * 900 + [300] + [0] * 900])
-def test_many_sequences(lens):
-    c = Case(same(*lens), 4, 1, 64, seed=len(lens), lead=1, trail=1)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_sequences(lens, D):
+    c = Case(same(*lens), 4, 1, D, seed=len(lens), lead=1, trail=1)
     c.run()
     c.verify()
 
@@ -138,6 +139,16 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(D, where):
     c.v[1 + where, 0, 5] = float("inf")
     c.v[1 + where, 1, D - 1] = float("nan")
     c.v[1 + 300 + min(where, 259), 0, 7] = float("-inf")
+    c.run()
+    c.verify()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_that_are_not_finite_in_many_short_sequences(D):
+    c = Case([(20, 20 + 60 * (b % 3)) for b in range(50)], 8, 2, D, seed=D, lead=1, trail=2)
+    for b in range(0, 50, 7):
+        at = c.ks[b].item() + c.seqs[b][1] - 10
+        c.v[at, b % 2, 3 * b % D] = [float("inf"), float("nan"), float("-inf")][b % 3]
     c.run()
     c.verify()
 

@@ -133,7 +133,8 @@ def test_large_values_and_growing_scores():
 
 
 @pytest.mark.parametrize("B,S,cap,D", [(1, 1, 9000, 128), (2, 1, 40000, 64), (1, 61, 20000, 128), (3, 4, 7000, 256),
-                                       (40, 1, 3000, 128), (200, 1, 260, 64)])
+                                       (40, 1, 3000, 128), (200, 1, 260, 64), (200, 1, 260, 128), (60, 9, 400, 128),
+                                       (60, 9, 2000, 64), (30, 26, 700, 64)])
 def test_long_and_many(B, S, cap, D):
     ends = [cap if b == 0 else S + (b * 7919) % (cap - S) for b in range(B)]
     c = Case(ends, S, 8, 2, D, cap, S > 1, seed=B)

@@ -89,7 +89,7 @@ def tree(lib, ptrs=None, size=1 << 40, scale=0.1, **kw):
 def test_tree_refuses_bad_arguments(lib):
     assert tree(lib, headDim=80) == HEAD_DIM and tree(lib, numQHeads=31) == HEADS and tree(lib, numQHeads=0) == HEADS
     for kw in (dict(batch=-1), dict(seqLen=-1), dict(seqLen=(1 << 15) + 1), dict(kvCapacity=-1), dict(kvCapacity=(1 << 28) + 1),
-               dict(batch=1 << 20, seqLen=1 << 10), dict(kvCapacity=1 << 28, numKVHeads=8), dict(scale=float("nan"))):
+               dict(batch=1 << 20, seqLen=1 << 10), dict(kvCapacity=1 << 28, numKVHeads=8), dict(batch=1 << 20, seqLen=1, kvCapacity=1 << 20), dict(scale=float("nan"))):
         assert tree(lib, **kw) == SHAPE, kw
     for i in range(7):
         ptrs = [A, A, A, A, FAR, A, A]
