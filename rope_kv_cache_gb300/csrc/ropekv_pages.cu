@@ -85,7 +85,9 @@ struct AcceptArgs {
 // before the first of the eight is written. Entry j's source is at least j, every
 // destination before it is smaller, so nothing is overwritten that is still to move, and a
 // column has the same thread throughout. Scales are further columns of 4 bytes. Bound by
-// latency: lengths and entries, page ids, rows, one after the other.
+// latency: lengths and entries, page ids, rows, one after the other (128 sequences, up to 8 of 61
+// drafts, INT8: 3.9 us, 5.7 with every thread looking its rows up itself; 4 sequences of a
+// contiguous cache 2.5 us, about what any dependent launch takes).
 template <bool PAGED>
 __global__ void __launch_bounds__(512) accept_kernel(const __grid_constant__ AcceptArgs a)
 {
@@ -192,7 +194,8 @@ struct CopyArgs {
 constexpr int kCopyUnroll = 4;
 
 // A CTA copies one run of one plane of one pair: four vectors a thread, all loaded before
-// the first is stored; the first run's CTA takes the page's scales along.
+// the first is stored; the first run's CTA takes the page's scales along. 1200 pages of 32 tokens x 8
+// heads of 128, FP16: 47.5 us, 6.6 TB/s read and written, 97 % of a plain copy; 6 small pages 2.9 us.
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ CopyArgs a)
 {
     dependency_sync();
@@ -374,7 +377,9 @@ __global__ void __launch_bounds__(1024) fork_plan_kernel(const __grid_constant__
 
 // CTAs of one fork: runs of the partly filled page's rows (four vectors a thread); the
 // first also writes the child's row of the table, the counts and the length. Children
-// are no parents, so nothing that is read here is written here.
+// are no parents, so nothing that is read here is written here. 192 children given up and forked
+// anew from 64 sequences of up to 2000 tokens (pages of 64, 8 heads of 128, FP16; 50 MB): 14.6 us in three
+// launches, of which the copy takes about 8; four children 8.7 us.
 __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ ForkArgs a)
 {
     dependency_sync();
