@@ -17,8 +17,8 @@
  * from the sizes and lengths alone, so equal calls give equal bits. Scores, sums and
  * partial results are FP32; the weights of V are rounded to FP16 once. A value that is
  * not finite reaches only the rows that see its token; in V one costs such rows, and
- * those of the same tile that do not see it, a slower path. Waits inside the kernels
- * are bounded; should one run out, which no argument makes it do, the rows concerned
+ * those of the same tile that do not see it, a much slower path. Waits inside the
+ * kernels are bounded; should one run out, which no argument makes it do, the rows concerned
  * are NaN in out and lse.
  */
 #ifndef ROPEKV_SEQUENCE_H

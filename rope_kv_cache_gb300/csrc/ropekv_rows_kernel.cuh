@@ -42,8 +42,13 @@
 //
 // Masked scores become -infinity by selection, whatever they were. A V that is not finite
 // and that some rows of a tile see and others do not (a weight of 0 times infinity) shows
-// as a row of O that is not finite although its sum is: such a row is computed again
-// from the tokens it sees alone.
+// as a row of O that is not finite although its sum is. Which of its elements a value that it
+// does not see has spoilt is then looked up in V, and those are computed again from the keys
+// that it sees, a row by a warp, in FP32. A prompt of 6000 tokens (220 us) takes 3.9 ms if all
+// of V is NaN, 13 ms with one NaN or infinity in the middle and 49 ms with it at the end, where
+// the rows just before it are long (a thread a row, each row in full: 68 to 100 ms). Looking for
+// such values in shared memory and taking them out before the product makes that 0.5 to 2 ms, but
+// costs prompts of 300 tokens 10 % (68 -> 75 us) when there are none.
 //
 // Bounds and figures (32 query and 8 KV heads of 128). A step of two row tiles is 2048 cycles of
 // products at the tensor cores' rate, 2300 as they come here: both operands of S lie in shared
@@ -294,63 +299,174 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* r, bool who
     }
 }
 
-// A row of O / l from the segment's tokens that the row sees, in FP32 throughout, in place of
-// what the products made of it.
-template <int D, int MT>
-__device__ __noinline__ void plain_row(const RowsArgs& a, const Segment& s, int token, int at, int row, float m, float l)
+// Halves of a word that are infinities or NaN, and those that are NaN alone: bits 0 and 1.
+__device__ __forceinline__ uint32_t strange2(uint32_t w, uint32_t least)
 {
-    constexpr int TN = RowsConfig<D, MT, 1>::kTile;
-    const int kvHead = s.head / a.headsPerKv;
-    const int limit = min(row_limit(a, s, token), s.j1 * TN);
-    const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)s.b * a.S + token) * a.W : nullptr;
-    const uint16_t* q = a.q + (size_t)(s.qRow + token) * a.qStride + (size_t)(at % a.Hq) * D;
-    const uint16_t* kBase = a.k + (size_t)s.b * a.kvBatch + (size_t)kvHead * a.kvHead;
-    const uint16_t* vBase = a.v + (size_t)s.b * a.kvBatch + (size_t)kvHead * a.kvHead;
-    float o[D];
-#pragma unroll 1
-    for (int d = 0; d < D; ++d)
-        o[d] = 0.0f;
-#pragma unroll 1
-    for (int t = s.j0 * TN; t < limit; ++t) {
-        if (words != nullptr && !(sees32(a, words, s.base, limit, t) & 1))
-            continue;
-        const uint4* kr = reinterpret_cast<const uint4*>(kBase + (size_t)(s.kvRow + t) * a.kTok);
-        const uint4* qr = reinterpret_cast<const uint4*>(q);
-        float dot = 0.0f;
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) {
-            uint4 kw = kr[x], qw = qr[x];
-            const __half2* kh = reinterpret_cast<const __half2*>(&kw);
-            const __half2* qh = reinterpret_cast<const __half2*>(&qw);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float2 f = __half22float2(kh[y]), g = __half22float2(qh[y]);
-                dot = fmaf(f.x, g.x, fmaf(f.y, g.y, dot));
-            }
-        }
-        const float p = exp2_fast(dot * a.scaleLog2 - m) / l;
-        const uint4* vr = reinterpret_cast<const uint4*>(vBase + (size_t)(s.kvRow + t) * a.vTok);
-#pragma unroll 1
-        for (int x = 0; x < D / 8; ++x) {
-            uint4 vw = vr[x];
-            const __half2* vh = reinterpret_cast<const __half2*>(&vw);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float2 f = __half22float2(vh[y]);
-                o[8 * x + 2 * y] += p * f.x;
-                o[8 * x + 2 * y + 1] += p * f.y;
-            }
-        }
-    }
-    if (s.slot >= 0) {
-#pragma unroll 1
-        for (int d = 0; d < D; ++d)
-            a.partO[(((size_t)s.slot * (D / 4) + d / 4) * (MT * 128) + row) * 4 + d % 4] = o[d];
+    return ((w & 0x7fffu) >= least ? 1u : 0u) | ((w >> 16 & 0x7fffu) >= least ? 2u : 0u);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, const uint16_t* p)
+{
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x, w[1] = x.y;
     } else {
-#pragma unroll 1
-        for (int d = 0; d < D; d += 2)
-            *reinterpret_cast<uint32_t*>(a.out + (size_t)at * D + d) = half2_bits(within_half(o[d]), within_half(o[d + 1]));
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
+}
+
+// Rows (`mine`, one a lane) of which an element of O / l is not finite although the sum is. Out has
+// held infinities as +-65504: it gets them. Then, row by row with the whole warp, an element whose
+// column has a value that is not finite in a key of the segment that the row does not see (its
+// weight of 0 made it NaN), and no NaN in one that it sees, is computed again from the latter alone.
+template <int D, int MT>
+__device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint32_t oAddr, bool mine, int token, int at,
+                                       int row, float m, float l)
+{
+    constexpr int TN = RowsConfig<D, MT, 1>::kTile, kWords = D / 64;
+    constexpr int kLanes = D / 8, kKeys = 32 / kLanes;         // a key of K by kLanes lanes, a row of V by all
+    constexpr int kBatch = D == 256 ? 16 : 32;                 // rows of V on their way at once
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int k = 0; s.slot < 0 && k < D; k += 16) {
+        float o[16];
+        tmem_load16(o, oAddr + k);
+        tmem_wait_load();
+        pin<16>(o);
+#pragma unroll
+        for (int x = 0; x < 16; x += 2)
+            if (mine)
+                *reinterpret_cast<uint32_t*>(a.out + (size_t)at * D + k + x) =
+                    half2_bits(within_half(o[x] / l), within_half(o[x + 1] / l));
+    }
+    tmem_fence_before();
+    __syncwarp();
+    const size_t kv = (size_t)s.b * a.kvBatch + (size_t)(s.head / a.headsPerKv) * a.kvHead;
+    const uint16_t* kBase = a.k + kv + (size_t)s.kvRow * a.kTok + (lane % kLanes) * 8;
+    const uint16_t* vBase = a.v + kv + (size_t)s.kvRow * a.vTok + lane * (2 * kWords);
+    const int first = s.j0 * TN, end = min(s.nk, s.j1 * TN);
+#pragma unroll 1
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine); left != 0; left &= left - 1) {
+        const int src = __ffs(left) - 1;
+        const int tok = __shfl_sync(0xffffffffu, token, src), atRow = __shfl_sync(0xffffffffu, at, src);
+        const int partRow = __shfl_sync(0xffffffffu, row, src);
+        const float mRow = __shfl_sync(0xffffffffu, m, src), lRow = __shfl_sync(0xffffffffu, l, src);
+        const int limit = min(row_limit(a, s, tok), end);
+        const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)s.b * a.S + tok) * a.W : nullptr;
+        // columns of the lane, a bit each: of the values that the row does not see ..
+        uint32_t spoiled = 0, known = 0;
+#pragma unroll 1
+        for (int t0 = max(first, (words != nullptr ? s.base : limit) & ~31); t0 < end; t0 += 32) {
+            const uint32_t hidden = ~sees32(a, words, s.base, limit, t0);
+#pragma unroll 1
+            for (int y0 = 0; y0 < 32; y0 += kBatch) {
+                uint32_t w[kBatch][kWords];
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y)
+                    load_words<kWords>(w[y], vBase + (size_t)min(t0 + y0 + y, end - 1) * a.vTok);
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y)
+#pragma unroll
+                    for (int x = 0; x < kWords; ++x)
+                        spoiled |= t0 + y0 + y < end && hidden >> (y0 + y) & 1 ? strange2(w[y][x], 0x7c00u) << 2 * x : 0u;
+            }
+        }
+        // .. and of those that it sees
+#pragma unroll 1
+        for (int t0 = first; t0 < limit && __any_sync(0xffffffffu, spoiled & ~known); t0 += 32) {
+            const uint32_t seen = sees32(a, words, s.base, limit, t0);
+#pragma unroll 1
+            for (int y0 = 0; y0 < 32; y0 += kBatch) {
+                uint32_t w[kBatch][kWords];
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y)
+                    load_words<kWords>(w[y], vBase + (size_t)min(t0 + y0 + y, end - 1) * a.vTok);
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y)
+#pragma unroll
+                    for (int x = 0; x < kWords; ++x)
+                        known |= seen >> (y0 + y) & 1 ? strange2(w[y][x], 0x7c01u) << 2 * x : 0u;
+            }
+        }
+        const uint32_t again = spoiled & ~known;
+        if (!__any_sync(0xffffffffu, again))
+            continue;
+        float q[8], o[2 * kWords];
+        const uint4 qw = *reinterpret_cast<const uint4*>(
+            a.q + (size_t)(s.qRow + tok) * a.qStride + (size_t)(atRow % a.Hq) * D + (lane % kLanes) * 8);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float2 f = __half22float2(reinterpret_cast<const __half2*>(&qw)[x]);
+            q[2 * x] = f.x, q[2 * x + 1] = f.y;
+        }
+#pragma unroll
+        for (int x = 0; x < 2 * kWords; ++x)
+            o[x] = 0.0f;
+#pragma unroll 1
+        for (int t0 = first; t0 < limit; t0 += 32) {
+            const uint32_t seen = sees32(a, words, s.base, limit, t0);
+            if (seen == 0)
+                continue;
+            float score = 0.0f;
+#pragma unroll 1
+            for (int x0 = 0; x0 < kLanes; x0 += 8) {
+                uint4 kw[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    kw[x] = *reinterpret_cast<const uint4*>(
+                        kBase + (size_t)min(t0 + (x0 + x) * kKeys + lane / kLanes, end - 1) * a.kTok);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float2 f = __half22float2(reinterpret_cast<const __half2*>(kw + x)[y]);
+                        dot = fmaf(f.x, q[2 * y], fmaf(f.y, q[2 * y + 1], dot));
+                    }
+#pragma unroll
+                    for (int y = 1; y < kLanes; y *= 2)
+                        dot += __shfl_xor_sync(0xffffffffu, dot, y);
+                    dot = __shfl_sync(0xffffffffu, dot, lane % kKeys * kLanes);
+                    score = lane / kKeys == x0 + x ? dot : score;
+                }
+            }
+            const float p = seen >> lane & 1 ? exp2_fast(score * a.scaleLog2 - mRow) / lRow : 0.0f;
+#pragma unroll 1
+            for (int y0 = 0; y0 < 32; y0 += kBatch) {
+                uint32_t w[kBatch][kWords];
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y)
+                    load_words<kWords>(w[y], vBase + (size_t)min(t0 + y0 + y, end - 1) * a.vTok);
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) {
+                    const float weight = __shfl_sync(0xffffffffu, p, y0 + y);
+                    const uint32_t keep = seen >> (y0 + y) & 1 ? 0xffffffffu : 0u;
+#pragma unroll
+                    for (int x = 0; x < kWords; ++x) {
+                        const uint32_t bits = w[y][x] & keep;
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bits));
+                        o[2 * x] = fmaf(weight, f.x, o[2 * x]);
+                        o[2 * x + 1] = fmaf(weight, f.y, o[2 * x + 1]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2 * kWords; ++x) {
+            const int d = lane * (2 * kWords) + x;
+            if (again >> x & 1) {
+                if (s.slot >= 0)
+                    a.partO[(((size_t)s.slot * (D / 4) + d / 4) * (MT * 128) + partRow) * 4 + d % 4] = o[x];
+                else
+                    a.out[(size_t)atRow * D + d] = (uint16_t)half2_bits(within_half(o[x]), 0.0f);
+            }
+        }
+    }
+    __syncwarp();
 }
 
 template <bool TREE>
@@ -1021,9 +1137,8 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             }
             const bool strange = live && !none && !wrong && fabsf(l) < INFINITY && !(nan0 + nan1 == 0.0f);
             if (__any_sync(0xffffffffu, strange)) {
-                __syncwarp();          // other lanes have written of the row
-                if (strange)
-                    plain_row<D, MT>(a, seg, token, at, row, M, l);
+                __syncwarp();
+                mend_rows<D, MT>(a, seg, oAddr, strange, token, at, row, M, l);
             }
             __syncwarp();
             if (lane == 0)

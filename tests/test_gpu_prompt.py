@@ -154,6 +154,19 @@ def test_values_that_are_not_finite_in_many_short_sequences(D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seqs", [same(400, 131), [(30, 90)] * 40, [(5, 1200)]])
+def test_values_that_are_not_finite_in_many_places(D, seqs):
+    # in one column: of a row, seen ones and others; weights are far above FP16's least
+    c = Case(seqs, 8, 2, D, seed=D, lead=1, trail=2, q_scale=1.0)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    at = torch.rand(c.v.shape, generator=g, device=DEV)
+    for x, bad in enumerate(["nan", "inf", "-inf"]):
+        c.v[(at > x * 1e-3) & (at < x * 1e-3 + 5e-4)] = float(bad)
+    c.run()
+    c.verify()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_keys_that_are_not_finite_do_not_reach_rows_before_them(D, bad):
     c = Case(same(200, 150), 4, 2, D, seed=1)

@@ -115,6 +115,18 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(S, D):
     c.verify()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("S", [1, 12, 70])
+def test_values_that_are_not_finite_in_many_places(S, D):
+    c = Case([S + 900, S + 3, 300], S, 8, 2, D, 1000, True, seed=S, q_scale=1.0)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    at = torch.rand(c.cache[:, 1].shape, generator=g, device=DEV)
+    for x, bad in enumerate(["nan", "inf", "-inf"]):
+        c.cache[:, 1][(at > x * 1e-3) & (at < x * 1e-3 + 5e-4)] = float(bad)
+    c.run()
+    c.verify()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
 def test_scales(scale):
     c = Case([300, 44], 7, 4, 2, 128, 300, True, seed=2, q_scale=1.0)
