@@ -197,6 +197,26 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
 
+// Wait of at most 2^20 polls, each of which the hardware may suspend for a time of its own choosing;
+// while rows are mended (failed[1]), which ends by itself but takes long, they start anew. False, for
+// the whole CTA, if it runs out.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, int parity, volatile int* failed)
+{
+    bool done = mbar_try(bar, parity);
+    for (int i = 0; !done && i < (1 << 20); ++i) {
+        done = mbar_try(bar, parity);
+        if ((i & 255) == 255) {
+            if (*failed)
+                break;
+            if (failed[1])
+                i = 0;
+        }
+    }
+    if (!done)
+        *failed = 1;
+    return __all_sync(0xffffffffu, done);
+}
+
 // Wait for a copy of the role's own, whatever has failed: nothing may land in shared memory
 // after the CTA has ended.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, int parity)
@@ -419,19 +439,25 @@ __device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint
                 for (int x = 0; x < 8; ++x)
                     kw[x] = *reinterpret_cast<const uint4*>(
                         kBase + (size_t)min(t0 + (x0 + x) * kKeys + lane / kLanes, end - 1) * a.kTok);
+                float dot[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    float dot = 0.0f;
+                    dot[x] = 0.0f;
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         const float2 f = __half22float2(reinterpret_cast<const __half2*>(kw + x)[y]);
-                        dot = fmaf(f.x, q[2 * y], fmaf(f.y, q[2 * y + 1], dot));
+                        dot[x] = fmaf(f.x, q[2 * y], fmaf(f.y, q[2 * y + 1], dot[x]));
                     }
+                }
 #pragma unroll
-                    for (int y = 1; y < kLanes; y *= 2)
-                        dot += __shfl_xor_sync(0xffffffffu, dot, y);
-                    dot = __shfl_sync(0xffffffffu, dot, lane % kKeys * kLanes);
-                    score = lane / kKeys == x0 + x ? dot : score;
+                for (int y = 1; y < kLanes; y *= 2)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        dot[x] += __shfl_xor_sync(0xffffffffu, dot[x], y);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float d = __shfl_sync(0xffffffffu, dot[x], lane % kKeys * kLanes);
+                    score = lane / kKeys == x0 + x ? d : score;
                 }
             }
             const float p = seen >> lane & 1 ? exp2_fast(score * a.scaleLog2 - mRow) / lRow : 0.0f;
@@ -698,6 +724,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             mbar_init(segFree + 8 * i, 4 * MT + 2);
         }
         *failed = base & 1023;      // tiles of 1024 bytes: 0
+        failed[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kLoad && lane < 3) {
@@ -719,7 +746,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     int segments = 0;
     auto next = [&](Segment& s) -> bool {
         const int i = segments % kSegments;
-        if (!mbar_wait_warp(segFull + 8 * i, (segments / kSegments) & 1, failed))
+        if (!wait_warp(segFull + 8 * i, (segments / kSegments) & 1, failed))
             return false;
         s = ring[i];
         __syncwarp();
@@ -741,7 +768,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 continue;
             auto load = [&](const CUtensorMap* map, int j) {
                 const int st = n % NS;
-                ok = ok && (n < NS || mbar_wait_warp(empty + 8 * st, (n / NS - 1) & 1, failed));
+                ok = ok && (n < NS || wait_warp(empty + 8 * st, (n / NS - 1) & 1, failed));
                 if (ok && elect_one()) {
                     mbar_expect(full + 8 * st, C::kTileBytes);
 #pragma unroll
@@ -753,7 +780,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 n += ok;
             };
             // the scores of the segment before have read its Q
-            ok = nq == 0 || mbar_wait_warp(qFree, (nq - 1) & 1, failed);
+            ok = nq == 0 || wait_warp(qFree, (nq - 1) & 1, failed);
             if (ok && elect_one()) {
                 mbar_expect(qFull, (uint32_t)(a.G * a.tokens * D * 2));
 #pragma unroll
@@ -784,7 +811,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         int n = 0, nq = 0, items = 0;               // loads taken, Q taken, items of a row tile before this segment
         auto acquire = [&]() -> int {
             const int st = n % NS;
-            ok = ok && mbar_wait_warp(full + 8 * st, (n / NS) & 1, failed);
+            ok = ok && wait_warp(full + 8 * st, (n / NS) & 1, failed);
             ++n;
             return st;
         };
@@ -813,7 +840,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             const int J = seg.j1 - seg.j0, look = min(LA, J);
             if (J == 0)
                 continue;
-            ok = mbar_wait_warp(qFull, nq & 1, failed);
+            ok = wait_warp(qFull, nq & 1, failed);
             ++nq;
             for (int j = 0; ok && j < look; ++j) {
                 const int st = acquire();
@@ -845,7 +872,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                     const uint32_t to = tmem + C::kColO + tile * D, from = tmem + slot * TN;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        ok = ok && mbar_wait_warp(pFull + 16 * slot + 8 * h, (item / SL) & 1, failed);
+                        ok = ok && wait_warp(pFull + 16 * slot + 8 * h, (item / SL) & 1, failed);
                         if (ok && elect_one()) {
                             tmem_fence_after();
 #pragma unroll
@@ -874,9 +901,9 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         }
         // the last products' arrivals
         for (int i = n > NS ? n - NS : 0; i < n; ++i)
-            mbar_wait_warp(empty + 8 * (i % NS), (i / NS) & 1, failed);
+            wait_warp(empty + 8 * (i % NS), (i / NS) & 1, failed);
         if (nq > 0)
-            mbar_wait_warp(qFree, (nq - 1) & 1, failed);
+            wait_warp(qFree, (nq - 1) & 1, failed);
     } else if (warp == kAlloc) {
         // ---------------------------------------------------------- segments
         few_registers<C>();
@@ -884,7 +911,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         int n = 0;
         auto publish = [&](const Segment& s) {
             const int i = n % kSegments;
-            ok = ok && (n < kSegments || mbar_wait_warp(segFree + 8 * i, (n / kSegments - 1) & 1, failed));
+            ok = ok && (n < kSegments || wait_warp(segFree + 8 * i, (n / kSegments - 1) & 1, failed));
             if (ok && lane == 0) {
                 ring[i] = s;
                 mbar_arrive(segFull + 8 * i);
@@ -967,7 +994,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         int items = 0;
         for (; ok; ++segments) {
             const int at4 = segments % kSegments;
-            ok = mbar_wait_warp(segFull + 8 * at4, (segments / kSegments) & 1, failed);
+            ok = wait_warp(segFull + 8 * at4, (segments / kSegments) & 1, failed);
             const Segment& seg = ring[at4];                     // given back when its rows have left
             if (!ok || seg.head < 0)
                 break;
@@ -984,7 +1011,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             for (int j = 0; ok && j < J; ++j) {
                 const int item = items + j, slot = tile * SL + item % SL;
                 const uint32_t sAddr = laneBase + slot * TN;
-                ok = mbar_wait_warp(sFull + 8 * slot, (item / SL) & 1, failed);
+                ok = wait_warp(sFull + 8 * slot, (item / SL) & 1, failed);
                 if (!ok)
                     break;
                 if (!warpLive) {
@@ -1027,7 +1054,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                     l *= f;
                     if (j > 0) {
                         // O of this row tile is at rest: its last product has finished
-                        ok = mbar_wait_warp(oDone + 8 * (tile * SL + (item - 1) % SL), ((item - 1) / SL) & 1, failed);
+                        ok = wait_warp(oDone + 8 * (tile * SL + (item - 1) % SL), ((item - 1) / SL) & 1, failed);
                         if (!ok)
                             break;
                         tmem_fence_after();
@@ -1076,7 +1103,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             }
             items += J;
             if (J > 0 && ok)
-                ok = mbar_wait_warp(oDone + 8 * (tile * SL + (items - 1) % SL), ((items - 1) / SL) & 1, failed);
+                ok = wait_warp(oDone + 8 * (tile * SL + (items - 1) % SL), ((items - 1) / SL) & 1, failed);
             if (!warpLive) {
                 if (lane == 0)
                     mbar_arrive(segFree + 8 * at4);
@@ -1138,7 +1165,11 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             const bool strange = live && !none && !wrong && fabsf(l) < INFINITY && !(nan0 + nan1 == 0.0f);
             if (__any_sync(0xffffffffu, strange)) {
                 __syncwarp();
+                if (lane == 0)
+                    atomicAdd(const_cast<int*>(failed) + 1, 1);
                 mend_rows<D, MT>(a, seg, oAddr, strange, token, at, row, M, l);
+                if (lane == 0)
+                    atomicSub(const_cast<int*>(failed) + 1, 1);
             }
             __syncwarp();
             if (lane == 0)
