@@ -344,13 +344,14 @@ __device__ __forceinline__ void load_words(uint32_t* w, const uint16_t* p)
 // column has a value that is not finite in a key of the segment that the row does not see (its
 // weight of 0 made it NaN), and no NaN in one that it sees, is computed again from the latter alone.
 template <int D, int MT>
-__device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint32_t oAddr, bool mine, int token, int at,
-                                       int row, float m, float l)
+__device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint32_t oAddr, bool mine, float m, float l)
 {
     constexpr int TN = RowsConfig<D, MT, 1>::kTile, kWords = D / 64;
     constexpr int kLanes = D / 8, kKeys = 32 / kLanes;         // a key of K by kLanes lanes, a row of V by all
     constexpr int kBatch = D == 256 ? 16 : 32;                 // rows of V on their way at once
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, row = threadIdx.x;
+    const int rowTok = divide(row, a.divG), token = s.tok0 + rowTok;
+    const int at = (s.qRow + token) * a.Hq + s.head * a.G + row - rowTok * a.G;
 #pragma unroll 1
     for (int k = 0; s.slot < 0 && k < D; k += 16) {
         float o[16];
@@ -643,7 +644,7 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
 }
 
 // The softmax warps, which hold kTile scores a thread, take registers of the others: 256 x 208 +
-// 128 x 88 are the 384 x 168 of the launch with two row tiles, 128 x 184 + 128 x 72 the 256 x 128
+// 128 x 88 are the 384 x 168 of the launch with two row tiles, 128 x 200 + 128 x 56 the 256 x 128
 // of one of two CTAs on an SM.
 template <typename C>
 __device__ __forceinline__ void few_registers()
@@ -651,7 +652,7 @@ __device__ __forceinline__ void few_registers()
     if constexpr (C::kThreads == 384)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else if constexpr (C::kPerSm == 2)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 
 template <typename C>
@@ -660,7 +661,7 @@ __device__ __forceinline__ void more_registers()
     if constexpr (C::kThreads == 384)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     else if constexpr (C::kPerSm == 2)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -1167,7 +1168,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 __syncwarp();
                 if (lane == 0)
                     atomicAdd(const_cast<int*>(failed) + 1, 1);
-                mend_rows<D, MT>(a, seg, oAddr, strange, token, at, row, M, l);
+                mend_rows<D, MT>(a, seg, oAddr, strange, M, l);
                 if (lane == 0)
                     atomicSub(const_cast<int*>(failed) + 1, 1);
             }
