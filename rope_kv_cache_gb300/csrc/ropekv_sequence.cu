@@ -122,9 +122,8 @@ Plan make_plan(bool tree, int64_t T, int B, int S, int Hq, int Hkv, int D, int64
     p.G = group_of(Hq, Hkv);
     p.heads = Hq / p.G;
     const int64_t rows = (tree ? S : (T + B - 1) / std::max(1, B)) * (int64_t)p.G;     // of a sequence, in mean
-    // Two row tiles share K and V and alternate. One tile and two CTAs of an SM in their place, D =
-    // 128: 32 prompts of 300 tokens 78 us instead of 68, one of 8000 385 instead of 340; at 100
-    // tokens 46 instead of 41.
+    // Two row tiles share K and V and alternate. One tile in their place, D = 128: 32 prompts of
+    // 300 tokens 77 us instead of 62, one of 8000 460 instead of 345; 64 of 100 tokens 50 instead of 39.
     p.mt = D != 256 && rows > 128 ? 2 : 1;
     p.tokens = 128 * p.mt / p.G;
     p.tilesSeq = (S + p.tokens - 1) / p.tokens;
@@ -135,10 +134,10 @@ Plan make_plan(bool tree, int64_t T, int B, int S, int Hq, int Hkv, int D, int64
     p.leastShare = 4;
     // One row tile: two CTAs of an SM overlap what a step and a change of units wait for, at the
     // cost of scores looked ahead and of stages in flight, which few units, and long ones of
-    // 128 dims, need more. One against two, 32 query and 8 KV heads: 200 prompts of 30 tokens 52
-    // against 42 us (D = 128), 47 against 29 (D = 64); 64 decoding sequences of 100 to 200 tokens 27
-    // against 19; 128 of 2000 to 4000, D = 64, 151 against 132; 16 trees of 26 drafts behind 2000
-    // to 4000, D = 128, 49 against 52; one decoding sequence of 16000, D = 64, 17.3 against 18.7.
+    // 128 dims, need more. One against two, 32 query and 8 KV heads: 200 prompts of 30 tokens 50
+    // against 38 us (D = 128), 44 against 27 (D = 64); 64 decoding sequences of 100 to 200 tokens 27
+    // against 18; 128 of 2000 to 4000, D = 64, 152 against 130; 16 trees of 26 drafts behind 2000
+    // to 4000, D = 128, 48 against 53; one decoding sequence of 16000, D = 64, 17 against 19.
     const int64_t mean = tree ? tiles : (tiles + B - 1) / std::max(1, B);
     p.perSm = p.mt == 1 && D != 256 && units >= kSMs / 2 && (D == 64 || mean <= 8) ? 2 : 1;
     p.ctas = (int)std::min<int64_t>(kSMs * p.perSm, p.whole ? units : units * ((tiles + ropekv_rows::kSwitch + p.leastShare - 1) / p.leastShare));
