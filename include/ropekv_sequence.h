@@ -17,9 +17,9 @@
  * from the sizes and lengths alone, so equal calls give equal bits. Scores, sums and
  * partial results are FP32; the weights of V are rounded to FP16 once. A value that is
  * not finite reaches only the rows that see its token; in V one costs such rows, and
- * those of the same tile that do not see it, a much slower path. Waits inside the
- * kernels are bounded; should one run out, which no argument makes it do, the rows concerned
- * are NaN in out and lse.
+ * those of the same tile that do not see it, a much slower path. Waits inside the kernels
+ * are bounded; should one run out, which no argument makes it do, the rows concerned are
+ * NaN in out and lse.
  */
 #ifndef ROPEKV_SEQUENCE_H
 #define ROPEKV_SEQUENCE_H
@@ -63,7 +63,8 @@ ROPEKV_API int64_t prompt_attention_workspace_size(const ropekv_prompt_dims* dim
  * nothing (nk < nq) gets a zero row and lse = -infinity.
  * Host errors: negative sizes, numTokens or numKVTokens > 2^28, batch > 2^20,
  * strides too small, not multiples of 8 or > 2^36, numTokens * Hq > 2^31 - 1, smScale
- * not finite, out overlapping q, k or v -> ROPEKV_ERR_SHAPE; workspaceBytes too small -> ROPEKV_ERR_CAPACITY.
+ * not finite, out overlapping q, k or v -> ROPEKV_ERR_SHAPE; workspaceBytes too small ->
+ * ROPEKV_ERR_CAPACITY.
  */
 ROPEKV_API int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k,
                                 int64_t kTokenStride, const uint16_t* v, int64_t vTokenStride,
@@ -102,9 +103,9 @@ ROPEKV_API int64_t tree_attention_workspace_size(const ropekv_tree_dims* dims);
  * sequence, kvCacheEndLens[b] = 0, for one) gets a zero row and lse = -infinity. What
  * lies in slots that no token sees does not matter, whatever its bits.
  * Host errors: negative sizes, seqLen > 2^15, kvCapacity > 2^28, batch * seqLen * Hq >
- * 2^31 - 1, kvCapacity * Hkv * D > 2^37 or, times batch,
- * 2^40, smScale not finite, out overlapping q or
- * kvCache -> ROPEKV_ERR_SHAPE; workspaceBytes too small -> ROPEKV_ERR_CAPACITY.
+ * 2^31 - 1, kvCapacity * Hkv * D > 2^37 or, times batch, 2^40, smScale not finite, out
+ * overlapping q or kvCache -> ROPEKV_ERR_SHAPE; workspaceBytes too small ->
+ * ROPEKV_ERR_CAPACITY.
  */
 ROPEKV_API int tree_attention(const uint16_t* q, const uint16_t* kvCache,
                               const int32_t* kvCacheEndLens, const int32_t* treeMask, uint16_t* out,
