@@ -65,8 +65,10 @@
 // quarter's exponentials before the maximum is known, exponentials in two stages, scores read in
 // halves (no gain), rows exchanged between lanes on their way out (no gain).
 //
-// Every wait on an mbarrier is bounded. One that runs out ends its role's loop and,
-// through a flag, those of the others, and the CTA writes NaN.
+// Every wait on an mbarrier is bounded. One that runs out ends its role's loop and, through a flag,
+// those of the others; what is in flight is waited for, and each softmax thread that has not come to the
+// end of the CTA's share writes NaN to its rows in all of it: to out and lse of whole units, and to the
+// sums of pieces, from where the join spreads it.
 #pragma once
 
 #include <cuda.h>
@@ -103,6 +105,7 @@ struct RowsArgs {
     int32_t whole;             // no unit can be long enough to be split: there is nothing to join
     int32_t leastShare;        // steps of a share, at least
     int32_t out32;             // out is a multiple of 32 bytes, not of 16 alone
+    int32_t fail;              // as if a wait had run out before the first (tests)
     Divisor divG;
 };
 
@@ -172,8 +175,8 @@ struct RowsConfig {
     static constexpr int kCols = 512 / kPerSm;
     // barriers: full, empty of the stages; S full, the two halves of P, O done of the slots (a
     // wait tells only the last two phases of a barrier apart, and O(j - kSlots) is done when S(j)
-    // is); Q full, Q free; full, free of the segments
-    static constexpr int kBars = 2 * kStages + 4 * MT * kSlots + 2 + 2 * kSegments;
+    // is); Q full, Q free; full, free of the segments; all products done, after a failure
+    static constexpr int kBars = 2 * kStages + 4 * MT * kSlots + 2 + 2 * kSegments + 1;
     static constexpr int kOffRing = kQBytes;
     static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
     static constexpr int kOffSegs = (kOffBar + kBars * 8 + 15) / 16 * 16;
@@ -218,8 +221,8 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, int parity, volatile int
     return __all_sync(0xffffffffu, done);
 }
 
-// Wait for a copy of the role's own, whatever has failed: nothing may land in shared memory
-// after the CTA has ended.
+// Wait for copies and products of the role's own, whatever has failed: nothing may land in shared
+// memory or TMEM after the CTA has ended.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, int parity)
 {
     for (int i = 0; i < (1 << 20) && !mbar_try(bar, parity); ++i) {
@@ -644,6 +647,95 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
     }
 }
 
+// The segments of a CTA's share, in order, each given to f. Returns the unit that the share begins
+// and others end, if there is one. For a whole warp.
+template <int TN, bool TREE, typename F>
+__device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& start, F&& f)
+{
+    Joint joint = {};
+    if (!start.found)
+        return joint;
+    const int lane = threadIdx.x & 31;
+    Segment s;
+    long long at = start.at;
+    const long long end = start.end, share = start.share;
+    static_cast<Sequence&>(s) = start.s;
+    s.head = (int)quotient(start.inside, start.perHead);
+    long long inside = start.inside - s.head * start.perHead;      // steps of the head group before `at`
+    // the unit: the last with no more steps before it, by 32 guesses at a time
+    int lo = 0, hi = s.units;
+    long long skip = 0;
+    while (hi - lo > 1) {
+        const int width = (hi - lo + 31) / 32, u = min(hi, lo + lane * width);
+        const long long n = steps_before<TN, TREE>(a, s, u);
+        const uint32_t fits = __ballot_sync(0xffffffffu, u < hi && n <= inside);
+        const int best = 31 - __clz(fits);
+        skip = __shfl_sync(0xffffffffu, n, best);
+        lo += best * width;
+        hi = min(hi, lo + width);
+    }
+    inside -= skip;
+    int unit = lo;
+    while (at < end) {
+        const int tiles = tiles_of<TN>(a, s, unit), len = kSwitch + max(1, tiles);
+        const long long first = at - inside + kSwitch;       // of the unit's real steps, among all
+        long long take = min((long long)len - inside, end - at);
+        if (start.whole)
+            take = len - inside;                             // nothing of a unit that began before
+        const int r0 = max(0, (int)inside - kSwitch), r1 = max(0, (int)(inside + take) - kSwitch);
+        if (start.whole ? inside == 0 : r1 > r0) {
+            s.tok0 = unit * a.tokens;
+            s.j0 = min(r0, tiles);
+            s.j1 = min(r1, tiles);
+            const bool all = r0 == 0 && r1 == len - kSwitch;
+            s.slot = all ? -1 : 2 * (int)blockIdx.x + (r0 == 0);
+            if (r0 == 0 && !all)
+                joint = {s.qRow, s.tok0, s.nq, s.head, (int)(quotient(first + (len - kSwitch) - 1, share) - quotient(first, share)) + 1};
+            f(s);
+        }
+        at += take;
+        inside = 0;
+        if (++unit == s.units) {
+            unit = 0;
+            if (++s.head == a.heads) {
+                s.head = 0;
+                do {
+                    const int b = s.b + 1;
+                    if (b == a.B) {
+                        at = end;
+                        break;
+                    }
+                    static_cast<Sequence&>(s) = sequence<TREE>(a, b);
+                } while (s.units == 0);
+            }
+        }
+    }
+    return joint;
+}
+
+// A wait has run out: the thread's rows in every segment of the share become NaN, those too that had
+// been finished.
+template <int D, int MT, int PER, bool TREE>
+__device__ __noinline__ void spoil_rows(const RowsArgs& a, const Start& start)
+{
+    const int row = threadIdx.x, rowTok = divide(row, a.divG);
+    const float nan = __int_as_float(0x7fc00000);
+    each_segment<RowsConfig<D, MT, PER>::kTile, TREE>(a, start, [&](const Segment& s) {
+        if (rowTok >= a.tokens || s.tok0 + rowTok >= s.nq)
+            return;
+        if (s.slot >= 0) {
+            a.partL[(size_t)s.slot * (MT * 128) + row] = nan;
+            return;
+        }
+        const int at = (s.qRow + s.tok0 + rowTok) * a.Hq + s.head * a.G + row - rowTok * a.G;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 8)
+            *reinterpret_cast<uint4*>(a.out + (size_t)at * D + d) = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+        if (a.lse != nullptr)
+            a.lse[at] = nan;
+    });
+}
+
 // The softmax warps, which hold kTile scores a thread, take registers of the others: 256 x 208 +
 // 128 x 88 are the 384 x 168 of the launch with two row tiles, 128 x 200 + 128 x 56 the 256 x 128
 // of one of two CTAs on an SM (200 and 56 spill nothing, 184 and 72 60 words a thread: 200 prompts of 30
@@ -705,7 +797,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     const uint32_t bars = base + C::kOffBar;
     const uint32_t full = bars, empty = full + NS * 8, sFull = empty + NS * 8, pFull = sFull + MT * SL * 8,
                    oDone = pFull + 2 * MT * SL * 8, qFull = oDone + MT * SL * 8, qFree = qFull + 8, segFull = qFree + 8,
-                   segFree = segFull + kSegments * 8;
+                   segFree = segFull + kSegments * 8, drained = segFree + kSegments * 8;
     volatile int* failed = reinterpret_cast<volatile int*>(smem + C::kOffFlags);
     uint32_t* tmemSlot = reinterpret_cast<uint32_t*>(smem + C::kOffFlags + 8);
 
@@ -726,7 +818,8 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             mbar_init(segFull + 8 * i, 1);
             mbar_init(segFree + 8 * i, 4 * MT + 2);
         }
-        *failed = base & 1023;      // tiles of 1024 bytes: 0
+        mbar_init(drained, 1);
+        *failed = (base & 1023) | a.fail;      // tiles of 1024 bytes: 0
         failed[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -745,6 +838,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = *tmemSlot;
+    bool ok = true;
     // The segments, in order, for every warp that works on them; false at the end.
     int segments = 0;
     auto next = [&](Segment& s) -> bool {
@@ -762,7 +856,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     if (warp == kLoad) {
         // --------------------------------------------------------------- TMA
         few_registers<C>();
-        bool ok = true;
         int n = 0, nq = 0;                          // loads of K and V, of Q so far
         Segment seg;
         while (ok && next(seg)) {
@@ -810,7 +903,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         // a negative smScale: -Q K^T (bit 13 negates A), scaled by |smScale|
         const uint32_t kindS = mma_desc(TN, false) | (a.scaleLog2 < 0.0f ? 1u << 13 : 0u);
         constexpr uint32_t kindO = mma_desc(D, true);
-        bool ok = true;
         int n = 0, nq = 0, items = 0;               // loads taken, Q taken, items of a row tile before this segment
         auto acquire = [&]() -> int {
             const int st = n % NS;
@@ -903,14 +995,19 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             items += J;
         }
         // the last products' arrivals
-        for (int i = n > NS ? n - NS : 0; i < n; ++i)
-            wait_warp(empty + 8 * (i % NS), (i / NS) & 1, failed);
-        if (nq > 0)
-            wait_warp(qFree, (nq - 1) & 1, failed);
+        for (int i = n > NS ? n - NS : 0; ok && i < n; ++i)
+            ok = wait_warp(empty + 8 * (i % NS), (i / NS) & 1, failed);
+        ok = ok && (nq == 0 || wait_warp(qFree, (nq - 1) & 1, failed));
+        if (!ok) {
+            if (elect_one())
+                mma_commit(drained);
+            __syncwarp();
+            mbar_drain(drained, 0);
+        }
     } else if (warp == kAlloc) {
         // ---------------------------------------------------------- segments
         few_registers<C>();
-        bool ok = true;
+        ok = a.fail == 0;                           // without segments nothing begins
         int n = 0;
         auto publish = [&](const Segment& s) {
             const int i = n % kSegments;
@@ -922,63 +1019,8 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             __syncwarp();
             ++n;
         };
+        const Joint joint = each_segment<TN, TREE>(a, start, publish);
         Segment s;
-        Joint joint = {};
-        long long at = start.at;
-        const long long end = start.end, share = start.share;
-        if (start.found) {
-            static_cast<Sequence&>(s) = start.s;
-            s.head = (int)quotient(start.inside, start.perHead);
-            long long inside = start.inside - s.head * start.perHead;      // steps of the head group before `at`
-            // the unit: the last with no more steps before it, by 32 guesses at a time
-            int lo = 0, hi = s.units;
-            long long skip = 0;
-            while (hi - lo > 1) {
-                const int width = (hi - lo + 31) / 32, u = min(hi, lo + lane * width);
-                const long long n = steps_before<TN, TREE>(a, s, u);
-                const uint32_t fits = __ballot_sync(0xffffffffu, u < hi && n <= inside);
-                const int best = 31 - __clz(fits);
-                skip = __shfl_sync(0xffffffffu, n, best);
-                lo += best * width;
-                hi = min(hi, lo + width);
-            }
-            inside -= skip;
-            int unit = lo;
-            while (ok && at < end) {
-                const int tiles = tiles_of<TN>(a, s, unit), len = kSwitch + max(1, tiles);
-                const long long first = at - inside + kSwitch;       // of the unit's real steps, among all
-                long long take = min((long long)len - inside, end - at);
-                if (start.whole)
-                    take = len - inside;                             // nothing of a unit that began before
-                const int r0 = max(0, (int)inside - kSwitch), r1 = max(0, (int)(inside + take) - kSwitch);
-                if (start.whole ? inside == 0 : r1 > r0) {
-                    s.tok0 = unit * a.tokens;
-                    s.j0 = min(r0, tiles);
-                    s.j1 = min(r1, tiles);
-                    const bool all = r0 == 0 && r1 == len - kSwitch;
-                    s.slot = all ? -1 : 2 * (int)blockIdx.x + (r0 == 0);
-                    if (r0 == 0 && !all)
-                        joint = {s.qRow, s.tok0, s.nq, s.head, (int)(quotient(first + (len - kSwitch) - 1, share) - quotient(first, share)) + 1};
-                    publish(s);
-                }
-                at += take;
-                inside = 0;
-                if (++unit == s.units) {
-                    unit = 0;
-                    if (++s.head == a.heads) {
-                        s.head = 0;
-                        do {
-                            const int b = s.b + 1;
-                            if (b == a.B) {
-                                at = end;
-                                break;
-                            }
-                            static_cast<Sequence&>(s) = sequence<TREE>(a, b);
-                        } while (s.units == 0);
-                    }
-                }
-            }
-        }
         s.head = -1;
         publish(s);
         if (lane == 0 && !a.whole)
@@ -993,7 +1035,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         const int rowTok = divide(row, a.divG), g = row - rowTok * a.G;
         // |c|, kept above 0 so that a masked -infinity stays one (c = 0: all scores are 0)
         const float scale = fmaxf(fabsf(a.scaleLog2), 1e-30f);
-        bool ok = true;
         int items = 0;
         for (; ok; ++segments) {
             const int at4 = segments % kSegments;
@@ -1104,20 +1145,24 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
+            if (!ok)
+                break;
             items += J;
-            if (J > 0 && ok)
+            if (J > 0)
                 ok = wait_warp(oDone + 8 * (tile * SL + (items - 1) % SL), ((items - 1) / SL) & 1, failed);
+            if (!ok)
+                break;
             if (!warpLive) {
                 if (lane == 0)
                     mbar_arrive(segFree + 8 * at4);
                 continue;
             }
             tmem_fence_after();
-            const bool none = J == 0 || l == 0.0f, wrong = *failed != 0;
+            const bool none = J == 0 || l == 0.0f;
             const float inv = none ? 0.0f : 1.0f / l;
             const int at = (seg.qRow + token) * a.Hq + seg.head * a.G + g;      // row of out
             const int slot = seg.slot;
-            const bool plain = __all_sync(0xffffffffu, !none && !wrong);
+            const bool plain = __all_sync(0xffffffffu, !none);
             float nan0 = 0.0f, nan1 = 0.0f;                                     // NaN if an element is not finite
 #pragma unroll 1
             for (int k = 0; k < D; k += 32) {
@@ -1130,7 +1175,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 if (!plain) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
-                        o[x] = wrong ? __int_as_float(0x7fc00000) : none ? 0.0f : o[x];
+                        o[x] = none ? 0.0f : o[x];
                 }
 #pragma unroll
                 for (int x = 0; x < 32; x += 2) {
@@ -1159,13 +1204,12 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             }
             tmem_fence_before();
             if (live) {
-                const float bad = wrong ? __int_as_float(0x7fc00000) : 0.0f;
                 if (slot >= 0)
-                    a.partL[(size_t)slot * (MT * 128) + row] = none ? -INFINITY + bad : M + log2f(l) + bad;
+                    a.partL[(size_t)slot * (MT * 128) + row] = none ? -INFINITY : M + log2f(l);
                 else if (a.lse != nullptr)
-                    a.lse[at] = none ? -INFINITY + bad : kLn2 * (M + log2f(l)) + bad;
+                    a.lse[at] = none ? -INFINITY : kLn2 * (M + log2f(l));
             }
-            const bool strange = live && !none && !wrong && fabsf(l) < INFINITY && !(nan0 + nan1 == 0.0f);
+            const bool strange = live && !none && fabsf(l) < INFINITY && !(nan0 + nan1 == 0.0f);
             if (__any_sync(0xffffffffu, strange)) {
                 __syncwarp();
                 if (lane == 0)
@@ -1178,6 +1222,8 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             if (lane == 0)
                 mbar_arrive(segFree + 8 * at4);
         }
+        if (__any_sync(0xffffffffu, !ok || *failed != 0))
+            spoil_rows<D, MT, PER, TREE>(a, start);
     } else {
         few_registers<C>();
     }

@@ -20,6 +20,8 @@ using ropekv_rows::RowsConfig;
 
 constexpr int kSMs = 152;
 
+std::atomic<int> failing{0};      // ropekv_sequence_fail
+
 bool aligned16(const void* p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
@@ -188,6 +190,7 @@ int run(RowsArgs& a, const Plan& p, int D, int Hkv, int64_t kvTokens, int64_t kv
     a.whole = p.whole;
     a.leastShare = p.leastShare;
     a.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+    a.fail = failing.load(std::memory_order_relaxed);
     a.divG = make_divisor(p.G);
     const Layout at = make_layout(p, D);
     a.joints = (ropekv_rows::Joint*)workspace;
@@ -268,6 +271,13 @@ bool overlap(const uint16_t* p, int64_t n, const uint16_t* q, int64_t m)
 }  // namespace
 
 extern "C" {
+
+// Not part of the interface, for tests of what a wait that runs out leaves: with `on`, the attention
+// calls from now on end as if one had done so before anything is in flight. Returns what was set.
+ROPEKV_API int ropekv_sequence_fail(int on)
+{
+    return failing.exchange(on != 0, std::memory_order_relaxed);
+}
 
 int64_t prompt_attention_workspace_size(const ropekv_prompt_dims* dims)
 {

@@ -1,0 +1,93 @@
+"""The operators on whole sequences where they are easily wrong: weights far below the largest,
+infinities behind them, waits that give up, children whose rows still name pages, large batches."""
+import pytest
+
+import sequence_plain as sp
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from rope_kv_cache_gb300 import build
+    build.build_library()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def prompt(q, k, v, nq, nk, **kw):
+    """One sequence of nq queries that are the last of nk tokens: (out, lse)."""
+    import rope_kv_cache_gb300 as rk
+    out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device=DEV)
+    rk.prompt_attention(q, k, v, i32([0, nq]), out, kv_starts=i32([0, nk]), lse=lse, **kw)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def decode(q, k, v, **kw):
+    """The same call of tree_attention: the keys lie in a contiguous cache."""
+    import rope_kv_cache_gb300 as rk
+    cache = torch.stack([k.transpose(0, 1), v.transpose(0, 1)])[None].contiguous()
+    out, lse = torch.full_like(q, float("nan"))[None], torch.full(q.shape[:2], float("nan"), device=DEV)[None]
+    rk.tree_attention(q[None].contiguous(), cache, i32([k.shape[0]]), out, lse=lse, **kw)
+    torch.cuda.synchronize()
+    return out[0], lse[0]
+
+
+def test_waits_that_run_out_leave_nan_in_every_row():
+    """Calls that end as if a wait inside the kernel had run out at once. Nothing of an earlier call's rows
+    or pieces may be left then: whole units, cut ones and their joins are all NaN."""
+    import ctypes
+
+    import rope_kv_cache_gb300 as rk
+    fail = rk.load_serving_library().ropekv_sequence_fail
+    fail.argtypes, fail.restype = [ctypes.c_int], ctypes.c_int
+    g = torch.Generator(device=DEV).manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).half()
+    for D, Hq, Hkv, seqs in [(64, 8, 2, [(1, 1)]), (64, 8, 2, [(30, 30)] * 200), (128, 8, 2, [(3, 4000), (700, 900), (0, 9), (5, 2)]),
+                             (128, 32, 8, [(300, 300)] * 32), (128, 6, 2, [(1, 30000)]), (256, 8, 1, [(70, 2000), (1, 9000), (129, 129)])]:
+        nq, nk = sum(s[0] for s in seqs), sum(s[1] for s in seqs)
+        start = lambda i: torch.tensor([1] + [s[i] for s in seqs], device=DEV).cumsum(0).int()
+        q, k, v, qs, ks = r(nq + 2, Hq, D), r(nk + 2, Hkv, D), r(nk + 2, Hkv, D), start(0), start(1)
+        ws = torch.zeros(rk.prompt_attention_workspace_size(q, k, v, qs, ks), dtype=torch.uint8, device=DEV)
+        out, lse = torch.zeros_like(q), torch.zeros(nq + 2, Hq, device=DEV)
+        call = lambda: rk.prompt_attention(q, k, v, qs, out, kv_starts=ks, lse=lse, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        want, wl = out.clone(), lse.clone()
+        assert want.isfinite().all() and not wl.isnan().any()
+        assert fail(1) == 0
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            assert fail(0) == 1
+        assert out[1:-1].isnan().all() and lse[1:-1].isnan().all(), (D, seqs[:3])
+        assert (out[[0, -1]] == 0).all() and (lse[[0, -1]] == 0).all()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    for D, S, cap, ends in [(64, 1, 260, [100 + b for b in range(100)]), (128, 26, 3000, [3000, 26, 1000, 0]), (256, 9, 5000, [5000])]:
+        q, cache, lens = r(len(ends), S, 8, D), r(len(ends), 2, 2, cap, D), i32(ends)
+        ws = torch.zeros(rk.tree_attention_workspace_size(q, cache), dtype=torch.uint8, device=DEV)
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device=DEV)
+        call = lambda: rk.tree_attention(q, cache, lens, out, lse=lse, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        want, wl = out.clone(), lse.clone()
+        assert fail(1) == 0
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            fail(0)
+        assert out.isnan().all() and lse.isnan().all()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
