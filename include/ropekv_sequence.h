@@ -18,8 +18,9 @@
  * partial results are FP32; the weights of V are rounded to FP16 once. A value that is
  * not finite reaches only the rows that see its token; in V one costs such rows, and
  * those of the same tile that do not see it, a much slower path. Waits inside the kernels
- * are bounded; should one run out, all rows that a CTA had taken on, and all rows of units
- * that it shares with others, are NaN in out and lse, but for such as it had finished.
+ * are bounded while nothing comes on; should one run out, all rows that a CTA had taken on, and
+ * all rows of units that it shares with others, are NaN in out and lse, but for such as it had
+ * finished.
  */
 #ifndef ROPEKV_SEQUENCE_H
 #define ROPEKV_SEQUENCE_H

@@ -183,7 +183,7 @@ struct RowsConfig {
     static constexpr int kOffStart = kOffSegs + kSegments * (int)sizeof(Segment);
     static constexpr int kOffSums = (kOffStart + (int)sizeof(Start) + 15) / 16 * 16;
     static constexpr int kOffFlags = kOffSums + kThreads / 32 * 16;
-    static constexpr int kSmem = kOffFlags + 16;
+    static constexpr int kSmem = kOffFlags + 32;
     static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
     static_assert(kColO + MT * D <= kCols, "TMEM");
 };
@@ -200,20 +200,27 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
 
-// Wait of at most 2^20 polls, each of which the hardware may suspend for a time of its own choosing;
-// while rows are mended (failed[1]), which ends by itself but takes long, they start anew. False, for
-// the whole CTA, if it runs out. One poll in the code instead of one in front of the loop and one in
-// it: 32 prompts of 300 tokens 68 -> 62 us, one of 8000 339 -> 343.
+// Wait of at most 2^20 polls, each of which the hardware may suspend for a time of its own choosing (130
+// ms were seen to pass within them). They start anew while rows are mended (failed[1]), which ends by
+// itself but takes long. LONG, the waits for a segment, which may lie behind millions of keys or of empty
+// sequences: also whenever the CTA has come further in the meantime, a load of K or V issued (failed[3]) or
+// a sequence passed (failed[4]). All others end within a step or two. False, for the whole CTA, if it runs
+// out. One poll in the code instead of one in front of the loop and one in it: 32 prompts of 300 tokens
+// 68 -> 62 us, one of 8000 339 -> 343. (LONG everywhere: the ragged batch 174.5 -> 177 us.)
+template <bool LONG = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, int parity, volatile int* failed)
 {
     bool done = false;
-    for (int i = 0; !done && i < (1 << 20); ++i) {
+    for (int i = 0, seen = 0; !done && i < (1 << 20); ++i) {
         done = mbar_try(bar, parity);
         if ((i & 255) == 255) {
             if (*failed)
                 break;
-            if (failed[1])
+            const int now = LONG ? failed[3] + failed[4] : 0;
+            if (failed[1] || now != seen) {
+                seen = now;
                 i = 0;
+            }
         }
     }
     if (!done)
@@ -648,9 +655,9 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
 }
 
 // The segments of a CTA's share, in order, each given to f. Returns the unit that the share begins
-// and others end, if there is one. For a whole warp.
+// and others end, if there is one. For a whole warp; in `passed` the waits see that it comes on.
 template <int TN, bool TREE, typename F>
-__device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& start, F&& f)
+__device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& start, volatile int* passed, F&& f)
 {
     Joint joint = {};
     if (!start.found)
@@ -701,11 +708,10 @@ __device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& st
                 s.head = 0;
                 do {
                     const int b = s.b + 1;
-                    if (b == a.B) {
-                        at = end;
-                        break;
-                    }
+                    if (at >= end || b == a.B)
+                        return joint;
                     static_cast<Sequence&>(s) = sequence<TREE>(a, b);
+                    *passed = b;
                 } while (s.units == 0);
             }
         }
@@ -716,11 +722,11 @@ __device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& st
 // A wait has run out: the thread's rows in every segment of the share become NaN, those too that had
 // been finished.
 template <int D, int MT, int PER, bool TREE>
-__device__ __noinline__ void spoil_rows(const RowsArgs& a, const Start& start)
+__device__ __noinline__ void spoil_rows(const RowsArgs& a, const Start& start, volatile int* failed)
 {
     const int row = threadIdx.x, rowTok = divide(row, a.divG);
     const float nan = __int_as_float(0x7fc00000);
-    each_segment<RowsConfig<D, MT, PER>::kTile, TREE>(a, start, [&](const Segment& s) {
+    each_segment<RowsConfig<D, MT, PER>::kTile, TREE>(a, start, failed + 4, [&](const Segment& s) {
         if (rowTok >= a.tokens || s.tok0 + rowTok >= s.nq)
             return;
         if (s.slot >= 0) {
@@ -820,7 +826,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         }
         mbar_init(drained, 1);
         *failed = (base & 1023) | a.fail;      // tiles of 1024 bytes: 0
-        failed[1] = 0;
+        failed[1] = failed[3] = failed[4] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kLoad && lane < 3) {
@@ -843,7 +849,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     int segments = 0;
     auto next = [&](Segment& s) -> bool {
         const int i = segments % kSegments;
-        if (!wait_warp(segFull + 8 * i, (segments / kSegments) & 1, failed))
+        if (!wait_warp<true>(segFull + 8 * i, (segments / kSegments) & 1, failed))
             return false;
         s = ring[i];
         __syncwarp();
@@ -866,6 +872,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 const int st = n % NS;
                 ok = ok && (n < NS || wait_warp(empty + 8 * st, (n / NS - 1) & 1, failed));
                 if (ok && elect_one()) {
+                    failed[3] = n + 1;
                     mbar_expect(full + 8 * st, C::kTileBytes);
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
@@ -1011,7 +1018,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         int n = 0;
         auto publish = [&](const Segment& s) {
             const int i = n % kSegments;
-            ok = ok && (n < kSegments || wait_warp(segFree + 8 * i, (n / kSegments - 1) & 1, failed));
+            ok = ok && (n < kSegments || wait_warp<true>(segFree + 8 * i, (n / kSegments - 1) & 1, failed));
             if (ok && lane == 0) {
                 ring[i] = s;
                 mbar_arrive(segFull + 8 * i);
@@ -1019,7 +1026,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             __syncwarp();
             ++n;
         };
-        const Joint joint = each_segment<TN, TREE>(a, start, publish);
+        const Joint joint = each_segment<TN, TREE>(a, start, failed + 4, publish);
         Segment s;
         s.head = -1;
         publish(s);
@@ -1038,7 +1045,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         int items = 0;
         for (; ok; ++segments) {
             const int at4 = segments % kSegments;
-            ok = wait_warp(segFull + 8 * at4, (segments / kSegments) & 1, failed);
+            ok = wait_warp<true>(segFull + 8 * at4, (segments / kSegments) & 1, failed);
             const Segment& seg = ring[at4];                     // given back when its rows have left
             if (!ok || seg.head < 0)
                 break;
@@ -1223,7 +1230,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 mbar_arrive(segFree + 8 * at4);
         }
         if (__any_sync(0xffffffffu, !ok || *failed != 0))
-            spoil_rows<D, MT, PER, TREE>(a, start);
+            spoil_rows<D, MT, PER, TREE>(a, start, failed);
     } else {
         few_registers<C>();
     }

@@ -91,3 +91,25 @@ def test_waits_that_run_out_leave_nan_in_every_row():
         call()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [((40, 41), 8, 2, 64), ((5000, 5001), 8, 2, 64), ((2000, 700), 16, 2, 128),
+                                           ((300, 1), 4, 1, 256)])
+def test_a_million_empty_sequences_between_two(lens, Hq, Hkv, D):
+    """What is shared out ends behind the first sequence, or goes on behind all the empty ones."""
+    import rope_kv_cache_gb300 as rk
+    B = 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(D)
+    T = sum(lens)
+    r = lambda H: torch.randn(T, H, D, generator=g, device=DEV).half()
+    q, k, v, out = r(Hq), r(Hkv), r(Hkv), torch.full((T, Hq, D), float("nan"), dtype=torch.float16, device=DEV)
+    lse = torch.full((T, Hq), float("nan"), device=DEV)
+    starts = torch.full((B + 1,), lens[0], dtype=torch.int32, device=DEV)
+    starts[0], starts[-1] = 0, T
+    rk.prompt_attention(q, k, v, starts, out, lse=lse)
+    torch.cuda.synchronize()
+    for at in (slice(0, lens[0]), slice(lens[0], T)):
+        n = at.stop - at.start
+        o, l, to, tl = sp.attend(q[at], k[at], v[at], sp.causal(n, n, DEV))
+        sp.check(out[at], o, to, "out")
+        sp.check(lse[at], l, tl, "lse")
