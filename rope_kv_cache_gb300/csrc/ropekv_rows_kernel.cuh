@@ -833,12 +833,14 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         const CUtensorMap* map = lane == 0 ? &mapQ : lane == 1 ? &mapK : &mapV;
         asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // TMEM is taken only now: a CTA that held some while it waits for a grid in front, one of whose own
+    // CTAs has yet to take its share on this SM, would wait for ever
     if (warp == kAlloc) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :: "r"(smem_u32(tmemSlot)), "n"(C::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     find_start<D, MT, PER, TREE>(a, reinterpret_cast<long long*>(smem + C::kOffSums), &start);
     tmem_fence_before();
     __syncthreads();

@@ -113,3 +113,44 @@ def test_a_million_empty_sequences_between_two(lens, Hq, Hkv, D):
         o, l, to, tl = sp.attend(q[at], k[at], v[at], sp.causal(n, n, DEV))
         sp.check(out[at], o, to, "out")
         sp.check(lse[at], l, tl, "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_both_tensor_core_attentions_in_turn(D):
+    """A shared prefix's attention and one of many short prompts, launched one behind the other without a
+    gap: kernels of half an SM that could start beside the other's."""
+    import rope_kv_cache_gb300 as rk
+    g = torch.Generator(device=DEV).manual_seed(D)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).half()
+    B, S, Hq, Hkv, tpp, P, M = 16, 3, 8, 2, 16, 600, 4
+    prefix = P // tpp + 1
+    pages = prefix + B * M
+    pool, q1, att = r(2, pages, tpp, Hkv, D), r(B, S, Hq, D), torch.zeros(B, S, Hq, D, dtype=torch.float16, device=DEV)
+    ids = torch.arange(pages, device=DEV).int()
+    shared = torch.stack([ids[:prefix], ids[:prefix] + pages])
+    own = ids[prefix:].view(B, 1, M)
+    table = torch.cat([shared[0].expand(B, 1, -1), own], 2)
+    table = torch.cat([table, table + pages], 1).contiguous()
+    lens = (P + S + torch.arange(B, device=DEV) * 2).int()
+    n = 250
+    x, out = r(n * 30, Hq + 2 * Hkv, D), torch.zeros(n * 30, Hq, D, dtype=torch.float16, device=DEV)
+    starts = (torch.arange(n + 1, device=DEV) * 30).int()
+
+    def step(wait=lambda: None):
+        for _ in range(3):
+            rk.paged_attention_shared_prefix(q1, pool, shared, P, table, lens, att)
+            wait()
+            rk.prompt_attention(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], starts, out)
+            wait()
+    step(torch.cuda.synchronize)
+    want = att.clone(), out.clone()
+    assert all(w.isfinite().all() and w.abs().sum() > 0 for w in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(20):
+        att.zero_()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(att, want[0]) and torch.equal(out, want[1])
