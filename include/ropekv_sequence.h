@@ -15,7 +15,8 @@
  * means nothing afterwards; calls that may run at the same time, from graphs too,
  * need workspaces of their own. They are one or two launches whose split follows
  * from the sizes and lengths alone, so equal calls give equal bits. Scores, sums and
- * partial results are FP32; the weights of V are rounded to FP16 once. A value that is
+ * partial results are FP32; the weights of V are rounded to FP16 once, which is 2^-11 of a
+ * weight, or 2^-32 of the row's largest where that is more. A value that is
  * not finite reaches only the rows that see its token; in V one costs such rows, and
  * those of the same tile that do not see it, a much slower path. Waits inside the kernels
  * are bounded while nothing comes on; should one run out, all rows that a CTA had taken on, and

@@ -37,8 +37,12 @@
 // the softmax warps' own last products: K and V of the next are on their way. What such a
 // change costs counts as kSwitch steps at the head of every unit. Short units are not split.
 //
-// m moves only when a row's scores exceed it by more than 8 (2^8 stays far inside FP16
-// and FP32), in which case the row's O is rescaled in TMEM; the first tile sets it.
+// m moves only when a row's scores exceed it by more than 8, in which case the row's O is rescaled in
+// TMEM; the first tile sets it. The weights are 2^(s - m + 7): at most 2^15, inside FP16's range, of
+// which they use what lies above 1 too. So a weight keeps FP16's 2^-11 down to 2^-21 of the largest and is
+// off by 2^-32 of that below (without the 7: 2^-14, 2^-25; 3000 tokens that score 16 nats below a
+// first one of small V: out off by 4e-2 to 6e-2, now 1.3e-3 to 1.8e-3). O is held in FP32, l sums the weights as they were
+// before the rounding; the 7 leaves with the division.
 //
 // Masked scores become -infinity by selection, whatever they were. A V that is not finite
 // and that some rows of a tile see and others do not (a weight of 0 times infinity) shows
@@ -158,6 +162,8 @@ struct Start {
 };
 
 constexpr int kSegments = 4;   // that are known ahead
+
+constexpr float kRaise = 7.0f; // binary digits that weights are raised by
 
 template <int D, int MT, int PER>
 struct RowsConfig {
@@ -1124,7 +1130,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                         }
                     }
                 }
-                const float mm = M == -INFINITY ? 0.0f : M;
+                const float mm = (M == -INFINITY ? 0.0f : M) - kRaise;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k = 0; k < TN; k += 32) {
@@ -1214,16 +1220,16 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             tmem_fence_before();
             if (live) {
                 if (slot >= 0)
-                    a.partL[(size_t)slot * (MT * 128) + row] = none ? -INFINITY : M + log2f(l);
+                    a.partL[(size_t)slot * (MT * 128) + row] = none ? -INFINITY : (M - kRaise) + log2f(l);
                 else if (a.lse != nullptr)
-                    a.lse[at] = none ? -INFINITY : kLn2 * (M + log2f(l));
+                    a.lse[at] = none ? -INFINITY : kLn2 * ((M - kRaise) + log2f(l));
             }
             const bool strange = live && !none && fabsf(l) < INFINITY && !(nan0 + nan1 == 0.0f);
             if (__any_sync(0xffffffffu, strange)) {
                 __syncwarp();
                 if (lane == 0)
                     atomicAdd(const_cast<int*>(failed) + 1, 1);
-                mend_rows<D, MT>(a, seg, oAddr, strange, M, l);
+                mend_rows<D, MT>(a, seg, oAddr, strange, M - kRaise, l);
                 if (lane == 0)
                     atomicSub(const_cast<int*>(failed) + 1, 1);
             }

@@ -154,3 +154,32 @@ def test_both_tensor_core_attentions_in_turn(D):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(att, want[0]) and torch.equal(out, want[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("distance", [10, 12, 14, 16])
+@pytest.mark.parametrize("nq,nk", [(3000, 3000), (40, 3000), (4, 20000)])
+def test_many_small_weights_beside_a_large_one(nq, nk, distance, D):
+    """The first token holds most of the weight and has a zero V, all others score `distance` lower. A
+    weight is rounded to FP16 as 2^7 times what it is relative to the largest (or more, where the
+    running maximum lags): 2^-11 of itself, or 2^-25 of 2^-7 below FP16's normal range. To that come
+    2^-17 for what roundings of scores up to 16 (five of 2^-24) and ex2 (2^-22) do to a weight, the sums'
+    N 2^-23 (of O and l) and the result's rounding, 2^-11 or 2^-25. lse: ten roundings of at most 24 2^-24
+    in log2 units, and the sum's."""
+    g = torch.Generator(device=DEV).manual_seed(distance)
+    q = torch.zeros(nq, 4, D, dtype=torch.float16, device=DEV)
+    q[..., 0] = 1
+    k = torch.zeros(nk, 2, D, dtype=torch.float16, device=DEV)
+    k[0, :, 0] = distance
+    v = (100 * (1 + torch.rand(nk, 2, D, generator=g, device=DEV))).half()
+    v[0] = 0
+    n = nk - nq + 1 + torch.arange(nq, device=DEV, dtype=torch.float64)          # keys of each row
+    sums = v.double().cumsum(0)[nk - nq:].repeat_interleave(2, 1)                  # of the V of those but the first
+    w = torch.tensor(-float(distance), dtype=torch.float64, device=DEV).exp()
+    L = (1 + (n - 1) * w)[:, None, None]
+    want = w * sums / L
+    tol = sums / L * max(2.0 ** -11 * w, 2.0 ** -32) + want * (2.0 ** -11 + 2.0 ** -17 + 2 * n[:, None, None] * 2.0 ** -23) + 2.0 ** -25
+    for call in (lambda: prompt(q, k, v, nq, nk, sm_scale=1.0), lambda: decode(q, k, v, sm_scale=1.0)):
+        out, lse = call()
+        sp.check(out, want, tol, "out")
+        sp.check(lse, (distance + L[..., 0].log()).expand(nq, 4), torch.full((1, 1), 2.0 ** -16, dtype=torch.float64, device=DEV) + n[:, None] * 2.0 ** -23, "lse")
