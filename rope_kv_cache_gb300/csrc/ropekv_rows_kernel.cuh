@@ -41,17 +41,17 @@
 // TMEM; the first tile sets it. The weights are 2^(s - m + 7): at most 2^15, inside FP16's range, of
 // which they use what lies above 1 too. So a weight keeps FP16's 2^-11 down to 2^-21 of the largest and is
 // off by 2^-32 of that below (without the 7: 2^-14, 2^-25; 3000 tokens that score 16 nats below a
-// first one of small V: out off by 4e-2 to 6e-2, now 1.3e-3 to 1.8e-3). O is held in FP32, l sums the weights as they were
-// before the rounding; the 7 leaves with the division.
+// first one of small V: out off by 4e-2 to 6e-2, now 1.3e-3 to 1.8e-3). O is held in FP32, l sums the
+// weights as they were before the rounding; the 7 leaves with the division.
 //
-// Masked scores become -infinity by selection, whatever they were. A V that is not finite
-// and that some rows of a tile see and others do not (a weight of 0 times infinity) shows
-// as a row of O that is not finite although its sum is. Which of its elements a value that it
-// does not see has spoilt is then looked up in V, and those are computed again from the keys
-// that it sees, a row by a warp, in FP32. A prompt of 6000 tokens (220 us) takes 3.9 ms if all
-// of V is NaN, 13 ms with one NaN or infinity in the middle and 49 ms with it at the end, where
-// the rows just before it are long (a thread a row, each row in full: 68 to 100 ms). Looking for
-// such values in shared memory and taking them out before the product makes that 0.5 to 2 ms, but
+// Masked scores become -infinity by selection, whatever they were. A V that is not finite and whose
+// weight is 0, because a row of the tile does not see it or because FP16 does not hold the weight, shows as
+// a NaN in a row of O although its sum is finite. Unless a NaN that the row sees is the reason, such an
+// element is computed again from the keys that it sees, a row by a warp, in FP32, where weights stay above
+// 0: an infinity that a row sees is one in out, whatever its weight. A prompt of 6000 tokens (220 us)
+// takes 0.8 ms if all of V is NaN, 8.2 ms with one infinity in the middle (8.5 with a NaN token) and 31 ms
+// at the end, where the rows just before it are long (a thread a row, each row in full: 68 to 100 ms).
+// Looking for such values in shared memory and taking them out before the product makes that 0.5 to 2 ms, but
 // cost prompts of 300 tokens 10 % (68 -> 75 us) when there are none.
 //
 // Bounds and figures (32 query and 8 KV heads of 128). A step of two row tiles is 2048 cycles of
@@ -336,10 +336,17 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* r, bool who
     }
 }
 
-// Halves of a word that are infinities or NaN, and those that are NaN alone: bits 0 and 1.
-__device__ __forceinline__ uint32_t strange2(uint32_t w, uint32_t least)
+// Halves of a word that are NaN: bits 0 and 1.
+__device__ __forceinline__ uint32_t nan2(uint32_t w)
 {
-    return ((w & 0x7fffu) >= least ? 1u : 0u) | ((w >> 16 & 0x7fffu) >= least ? 2u : 0u);
+    return ((w & 0x7fffu) > 0x7c00u ? 1u : 0u) | ((w >> 16 & 0x7fffu) > 0x7c00u ? 2u : 0u);
+}
+
+// A weight that FP32 does not hold, but which is above 0 (so an infinity of such a weight stays one; the
+// product with a finite value is nothing beside FP16's least).
+__device__ __forceinline__ float above_zero(float w)
+{
+    return w < 1e-37f ? 1e-37f : w;
 }
 
 template <int N>
@@ -357,9 +364,11 @@ __device__ __forceinline__ void load_words(uint32_t* w, const uint16_t* p)
 }
 
 // Rows (`mine`, one a lane) of which an element of O / l is not finite although the sum is. Out has
-// held infinities as +-65504: it gets them. Then, row by row with the whole warp, an element whose
-// column has a value that is not finite in a key of the segment that the row does not see (its
-// weight of 0 made it NaN), and no NaN in one that it sees, is computed again from the latter alone.
+// held infinities as +-65504: it gets them. Then, row by row with the whole warp, a NaN element whose
+// column has no NaN in a key of the segment that the row sees is computed again from those keys alone:
+// a value that is not finite met a weight of 0, of a key that the row does not see, or of one whose
+// weight FP16 does not hold (or that was scaled by 0 when m rose). Weights of the latter are kept above 0
+// here, as they are in truth, so that an infinity is one in out whatever its weight.
 template <int D, int MT>
 __device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint32_t oAddr, bool mine, float m, float l)
 {
@@ -369,17 +378,22 @@ __device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint
     const int lane = threadIdx.x & 31, row = threadIdx.x;
     const int rowTok = divide(row, a.divG), token = s.tok0 + rowTok;
     const int at = (s.qRow + token) * a.Hq + s.head * a.G + row - rowTok * a.G;
-#pragma unroll 1
-    for (int k = 0; s.slot < 0 && k < D; k += 16) {
+    uint32_t lost[D / 32];                                     // the lane's row: its NaN elements
+#pragma unroll
+    for (int k = 0; k < D; k += 16) {
         float o[16];
         tmem_load16(o, oAddr + k);
         tmem_wait_load();
         pin<16>(o);
+        uint32_t bits = 0;
 #pragma unroll
-        for (int x = 0; x < 16; x += 2)
-            if (mine)
+        for (int x = 0; x < 16; x += 2) {
+            bits |= (o[x] != o[x] ? 1u : 0u) << x | (o[x + 1] != o[x + 1] ? 2u : 0u) << x;
+            if (mine && s.slot < 0)
                 *reinterpret_cast<uint32_t*>(a.out + (size_t)at * D + k + x) =
                     half2_bits(within_half(o[x] / l), within_half(o[x + 1] / l));
+        }
+        lost[k / 32] = k % 32 == 0 ? bits : lost[k / 32] | bits << 16;
     }
     tmem_fence_before();
     __syncwarp();
@@ -387,6 +401,42 @@ __device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint
     const uint16_t* kBase = a.k + kv + (size_t)s.kvRow * a.kTok + (lane % kLanes) * 8;
     const uint16_t* vBase = a.v + kv + (size_t)s.kvRow * a.vTok + lane * (2 * kWords);
     const int first = s.j0 * TN, end = min(s.nk, s.j1 * TN);
+    // the lane's columns of a row's D bits
+    auto columns = [&](const uint32_t (&row)[D / 32]) -> uint32_t {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+            bits = w == lane * (2 * kWords) / 32 ? row[w] >> lane * (2 * kWords) % 32 & ((1u << 2 * kWords) - 1) : bits;
+        return bits;
+    };
+    // those with a NaN in one of the keys t0 .. t0 + 31 that are seen
+    auto nan_columns = [&](int t0, uint32_t seen) -> uint32_t {
+        uint32_t found = 0;
+#pragma unroll 1
+        for (int y0 = 0; y0 < 32; y0 += kBatch) {
+            uint32_t w[kBatch][kWords];
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y)
+                load_words<kWords>(w[y], vBase + (size_t)min(t0 + y0 + y, end - 1) * a.vTok);
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y)
+#pragma unroll
+                for (int x = 0; x < kWords; ++x)
+                    found |= seen >> (y0 + y) & 1 ? nan2(w[y][x]) << 2 * x : 0u;
+        }
+        return found;
+    };
+    // first of the keys that all the rows see, for all of them at once
+    const int limitAll = a.treeMask != nullptr ? min(s.nk, s.base) : row_limit(a, s, token);
+    const int common = max(first, __reduce_min_sync(0xffffffffu, mine ? min(limitAll, end) : end) & ~31);
+    uint32_t any[D / 32], knownAll = 0;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w)
+        any[w] = __reduce_or_sync(0xffffffffu, mine ? lost[w] : 0u);
+    const uint32_t wanted = columns(any);
+#pragma unroll 1
+    for (int t0 = first; t0 < common && __any_sync(0xffffffffu, wanted & ~knownAll); t0 += 32)
+        knownAll |= nan_columns(t0, 0xffffffffu);
 #pragma unroll 1
     for (uint32_t left = __ballot_sync(0xffffffffu, mine); left != 0; left &= left - 1) {
         const int src = __ffs(left) - 1;
@@ -395,42 +445,15 @@ __device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint
         const float mRow = __shfl_sync(0xffffffffu, m, src), lRow = __shfl_sync(0xffffffffu, l, src);
         const int limit = min(row_limit(a, s, tok), end);
         const int32_t* words = a.treeMask != nullptr ? a.treeMask + ((size_t)s.b * a.S + tok) * a.W : nullptr;
-        // columns of the lane, a bit each: of the values that the row does not see ..
-        uint32_t spoiled = 0, known = 0;
+        uint32_t rowLost[D / 32], known = knownAll;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+            rowLost[w] = __shfl_sync(0xffffffffu, lost[w], src);
+        const uint32_t bits = columns(rowLost);
 #pragma unroll 1
-        for (int t0 = max(first, (words != nullptr ? s.base : limit) & ~31); t0 < end; t0 += 32) {
-            const uint32_t hidden = ~sees32(a, words, s.base, limit, t0);
-#pragma unroll 1
-            for (int y0 = 0; y0 < 32; y0 += kBatch) {
-                uint32_t w[kBatch][kWords];
-#pragma unroll
-                for (int y = 0; y < kBatch; ++y)
-                    load_words<kWords>(w[y], vBase + (size_t)min(t0 + y0 + y, end - 1) * a.vTok);
-#pragma unroll
-                for (int y = 0; y < kBatch; ++y)
-#pragma unroll
-                    for (int x = 0; x < kWords; ++x)
-                        spoiled |= t0 + y0 + y < end && hidden >> (y0 + y) & 1 ? strange2(w[y][x], 0x7c00u) << 2 * x : 0u;
-            }
-        }
-        // .. and of those that it sees
-#pragma unroll 1
-        for (int t0 = first; t0 < limit && __any_sync(0xffffffffu, spoiled & ~known); t0 += 32) {
-            const uint32_t seen = sees32(a, words, s.base, limit, t0);
-#pragma unroll 1
-            for (int y0 = 0; y0 < 32; y0 += kBatch) {
-                uint32_t w[kBatch][kWords];
-#pragma unroll
-                for (int y = 0; y < kBatch; ++y)
-                    load_words<kWords>(w[y], vBase + (size_t)min(t0 + y0 + y, end - 1) * a.vTok);
-#pragma unroll
-                for (int y = 0; y < kBatch; ++y)
-#pragma unroll
-                    for (int x = 0; x < kWords; ++x)
-                        known |= seen >> (y0 + y) & 1 ? strange2(w[y][x], 0x7c01u) << 2 * x : 0u;
-            }
-        }
-        const uint32_t again = spoiled & ~known;
+        for (int t0 = common; t0 < limit && __any_sync(0xffffffffu, bits & ~known); t0 += 32)
+            known |= nan_columns(t0, sees32(a, words, s.base, limit, t0));
+        const uint32_t again = bits & ~known;
         if (!__any_sync(0xffffffffu, again))
             continue;
         float q[8], o[2 * kWords];
@@ -478,7 +501,8 @@ __device__ __noinline__ void mend_rows(const RowsArgs& a, const Segment& s, uint
                     score = lane / kKeys == x0 + x ? d : score;
                 }
             }
-            const float p = seen >> lane & 1 ? exp2_fast(score * a.scaleLog2 - mRow) / lRow : 0.0f;
+            const float e = score * a.scaleLog2 - mRow;
+            const float p = seen >> lane & 1 && e > -INFINITY ? above_zero(exp2_fast(e) / lRow) : 0.0f;
 #pragma unroll 1
             for (int y0 = 0; y0 < 32; y0 += kBatch) {
                 uint32_t w[kBatch][kWords];
@@ -1289,7 +1313,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
         for (int j = 0; j < 4; ++j)
             top = fmaxf(top, x[j]);
         const float mm = top == -INFINITY ? 0.0f : top;
-        const float f = exp2_fast(m - mm);
+        const float f = above_zero(exp2_fast(m - mm));
         m = top;
         l *= f;
 #pragma unroll
@@ -1297,7 +1321,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
             o[y] *= f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float w = exp2_fast(x[j] - mm);
+            const float w = above_zero(exp2_fast(x[j] - mm));
             const float* y = reinterpret_cast<const float*>(v[j]);
             if (x[j] != -INFINITY) {
                 l += w;

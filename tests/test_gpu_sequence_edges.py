@@ -183,3 +183,44 @@ def test_many_small_weights_beside_a_large_one(nq, nk, distance, D):
         out, lse = call()
         sp.check(out, want, tol, "out")
         sp.check(lse, (distance + L[..., 0].log()).expand(nq, 4), torch.full((1, 1), 2.0 ** -16, dtype=torch.float64, device=DEV) + n[:, None] * 2.0 ** -23, "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,nk", [(300, 300), (5, 1200), (1, 20000), (90, 91)])
+def test_infinities_of_any_weight_reach_the_rows_that_see_them(nq, nk, D):
+    """Tokens that score 20 to 2000 lower than the others: their weights are positive all the same,
+    so that an infinity among their V is one in out (two of both signs: NaN)."""
+    g = torch.Generator(device=DEV).manual_seed(D + nq)
+    q = torch.randn(nq, 4, D, generator=g, device=DEV).half()
+    k, v = (torch.randn(nk, 2, D, generator=g, device=DEV).half() for _ in range(2))
+    q[..., 0], k[..., 0] = 1, 0
+    lower = [20, 60, 100, 300, 2000]
+    for i, d in enumerate(lower):
+        at = [0, nk // 3, nk // 2, nk - 2, nk - 1][i]
+        k[at, :, 0] = -d
+        v[at, i % 2, 7 * i + 1] = float("inf") if i != 2 else -float("inf")
+        v[at, 1, 50] = float("inf")
+        if i == 4:
+            v[at, 1, 50] = -float("inf")
+    o, l, to, tl = sp.attend(q, k, v, sp.causal(nq, nk, DEV), 0.5)
+    for call in (lambda: prompt(q, k, v, nq, nk, sm_scale=0.5), lambda: decode(q, k, v, sm_scale=0.5)):
+        out, lse = call()
+        sp.check(out, o, to, "out")
+        sp.check(lse, l, tl, "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinities_before_scores_that_rise_far(D):
+    """Infinities that O holds when the running maximum rises by more than FP32's exponents."""
+    nk = 700
+    q = torch.zeros(nk, 2, D, dtype=torch.float16, device=DEV)
+    q[..., 0] = 8
+    k = torch.zeros(nk, 1, D, dtype=torch.float16, device=DEV)
+    k[:, 0, 0] = torch.linspace(0, 1000, nk, device=DEV).half()
+    v = torch.randn(nk, 1, D, generator=torch.Generator(device=DEV).manual_seed(D), device=DEV).half()
+    v[3, 0, 5], v[200, 0, 6], v[400, 0, 7] = float("inf"), -float("inf"), float("nan")
+    o, l, to, tl = sp.attend(q, k, v, sp.causal(nk, nk, DEV))
+    for call in (lambda: prompt(q, k, v, nk, nk), lambda: decode(q, k, v)):
+        out, lse = call()
+        sp.check(out, o, to, "out")
+        sp.check(lse, l, tl, "lse")
