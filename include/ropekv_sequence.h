@@ -187,7 +187,10 @@ ROPEKV_API int64_t paged_kv_fork_workspace_size(int32_t numForks, int32_t batch)
  * tokensPerPage tokens go to a free page, which gets refCounts 1; forks take the
  * lowest free pages in the order of i. Where none is left, or the parent's partly
  * filled page is unmapped, the child ends with its last whole page. The child's
- * other entries become -1, kvLens[child] its length.
+ * other entries become -1, kvLens[child] its length. Pages that an empty child's row
+ * still names (as paged_kv_accept_drafts leaves them where nothing is accepted) are
+ * given up, their refCounts shrink by one; they are free for later calls, not for
+ * forks of this one.
  *   pageTable  [batch, 2, maxPagesPerSeq] INT32, in and out.
  *   kvLens     [batch] INT32, in and out.
  *   parents, children  [numForks] INT32.

@@ -405,9 +405,12 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ 
         int32_t* to = a.pageTable + (size_t)f.child * 2 * a.M;
         for (int k = threadIdx.x; k < a.M; k += blockDim.x) {
             const int id = k < whole ? from[k] : -1;
+            const int old = to[k];               // an empty child may still name pages: it gives them up
             const bool mapped = id >= 0 && id < a.numPages;
             if (mapped)
                 atomicAdd(a.refCounts + id, 1);
+            if (old >= 0 && old < a.numPages)
+                atomicSub(a.refCounts + old, 1);
             const int mine = mapped ? id : k == whole ? fresh : -1;
             to[k] = mine;
             to[a.M + k] = mine >= 0 ? mine + a.numPages : -1;

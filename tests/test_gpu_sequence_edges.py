@@ -224,3 +224,43 @@ def test_infinities_before_scores_that_rise_far(D):
         out, lse = call()
         sp.check(out, o, to, "out")
         sp.check(lse, l, tl, "lse")
+
+
+@pytest.mark.parametrize("fmt", ["f16", "int8"])
+def test_a_child_whose_row_still_names_pages_gives_them_up(fmt):
+    """Sequences of length 0 with mapped pages, as no accepted draft leaves them: a fork counts their old
+    entries down, and afterwards every count is the number of table entries that name the page."""
+    import rope_kv_cache_gb300 as rk
+    B, M, P, tpp, S = 7, 4, 30, 16, 20
+    dt = torch.float16 if fmt == "f16" else torch.int8
+    cache = torch.randint(-100, 100, (2, P, tpp, 2, 64), device=DEV, dtype=torch.int8).to(dt)
+    scales = None if fmt == "f16" else torch.rand(2, P, 2, tpp, device=DEV)
+    table = torch.full((B, 2, M), -1, dtype=torch.int32)
+    rows = {0: [3, 9, 4], 1: [3, 11], 2: [20, 21], 3: [22, 23, 24], 4: [3, 9, 25, 26], 5: [27]}
+    for b, r in rows.items():
+        table[b, 0, :len(r)] = torch.tensor(r)
+        table[b, 1, :len(r)] = torch.tensor(r) + P
+    table[4, 0, 3], table[4, 1, 3] = 999, -7                  # names no page
+    count = lambda t: torch.bincount(t[:, 0][(t[:, 0] >= 0) & (t[:, 0] < P)].long().flatten().cpu(), minlength=P).int()
+    refs = count(table).to(DEV)
+    table = table.to(DEV)
+    lens = i32([40, 20, S, S, S, S, 0])
+    # nothing of the drafts is accepted: lengths of 0, pages still mapped
+    rk.paged_kv_accept_drafts(cache, table, lens, S, torch.zeros(B, 0, dtype=torch.int32, device=DEV),
+                              i32([0] * B), lens, kv_scales=scales)
+    assert lens.tolist() == [20, 0, 0, 0, 0, 0, 0]
+    lens[1] = 20                                              # sequences 0 and 1 go on
+    # 3 and 4 from sequence 0 (of whose pages 4 shares two), 2 and 6 from 1; 5 twice: skipped
+    before, bits = table.clone(), cache.clone()
+    rk.paged_kv_fork(cache, table, lens, refs, i32([0, 0, 1, 1, 0, 1]), i32([3, 4, 2, 6, 5, 5]), kv_scales=scales)
+    torch.cuda.synchronize()
+    assert torch.equal(count(table), refs.cpu()), "counts are not the numbers of entries"
+    assert lens.tolist() == [20, 20, 20, 20, 20, 0, 20] and torch.equal(table[[0, 1, 5]], before[[0, 1, 5]])
+    # the free pages before the call, the lowest first, one for each fork's partly filled page
+    assert table[:, 0].tolist()[2:5] + table[6:, 0].tolist() == [[3, 2, -1, -1], [3, 0, -1, -1], [3, 1, -1, -1], [3, 5, -1, -1]]
+    assert torch.equal(cache[:, [2, 5], :4], bits[:, [11, 11], :4]) and torch.equal(cache[:, [0, 1], :4], bits[:, [9, 9], :4])
+    for p in (20, 21, 22, 23, 24, 25):
+        assert refs[p] == 0, f"page {p} is nobody's and not free"
+    rk.paged_kv_free(table, lens, refs, i32(list(range(B))))
+    torch.cuda.synchronize()
+    assert (refs == 0).all() and (table == -1).all()
