@@ -493,6 +493,14 @@ int check_table(int32_t batch, int32_t M, int32_t tpp)
     return batch < 0 || M < 0 || tpp <= 0 || (long long)M * tpp > (1LL << 30) ? ROPEKV_ERR_SHAPE : ROPEKV_OK;
 }
 
+constexpr int32_t kMostSequences = 1 << 18;
+
+// Shared memory of the plan of forks: three bits a sequence.
+int fork_smem(int32_t batch)
+{
+    return 3 * ((batch + 31) / 32) * 4;
+}
+
 int64_t up16(int64_t n)
 {
     return (n + 15) / 16 * 16;
@@ -584,7 +592,7 @@ int paged_kv_copy_pages(void* kvCache, float* kvScales, const int32_t* srcPages,
 
 int64_t paged_kv_fork_workspace_size(int32_t numForks, int32_t batch)
 {
-    if (numForks < 0 || numForks > (1 << 20) || batch < 0 || batch > (1 << 18))
+    if (numForks < 0 || numForks > (1 << 20) || batch < 0 || batch > kMostSequences)
         return ROPEKV_ERR_SHAPE;
     return 16 + (int64_t)sizeof(Fork) * numForks + up16(4LL * numForks);
 }
@@ -623,9 +631,10 @@ int paged_kv_fork(void* kvCache, float* kvScales, int32_t* pageTable, int32_t* k
     if (chunks * numForks > 0x7FFFFFFFLL)
         return ROPEKV_ERR_SHAPE;
     a.chunks = (int32_t)chunks;
-    const int smem = 3 * ((batch + 31) / 32) * 4;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // the limit belongs to the kernel, not to the call: always the same, as calls may overlap
+    const int smem = fork_smem(batch);
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 fork_smem(kMostSequences)) != cudaSuccess)
         return ROPEKV_ERR_LAUNCH;
     rc = launch(fork_plan_kernel, 1, 1024, smem, (cudaStream_t)stream, a);
     return rc != ROPEKV_OK ? rc : launch(fork_copy_kernel, chunks * numForks, 256, 0, (cudaStream_t)stream, a);

@@ -264,3 +264,49 @@ def test_a_child_whose_row_still_names_pages_gives_them_up(fmt):
     rk.paged_kv_free(table, lens, refs, i32(list(range(B))))
     torch.cuda.synchronize()
     assert (refs == 0).all() and (table == -1).all()
+
+
+def test_forks_of_batches_of_very_different_sizes_at_once():
+    """Host threads, each with a stream and tensors of its own: batches that need from 48 to 96 KB of
+    shared memory for their plans. (By ctypes, which lets the calls overlap.)"""
+    import ctypes
+    import threading
+
+    import rope_kv_cache_gb300 as rk
+    lib, failures = rk.load_serving_library(), []
+
+    class Batch:
+        def __init__(self, B):
+            self.B, self.stream = B, torch.cuda.Stream()
+            self.table = torch.full((B, 2, 2), -1, dtype=torch.int32, device=DEV)
+            self.table[0, :, 0] = i32([1, 9])
+            self.lens, self.refs = torch.zeros(B, dtype=torch.int32, device=DEV), i32([0, 1, 0, 0, 0, 0, 0, 0])
+            self.lens[0] = 3
+            self.cache = torch.randn(2, 8, 4, 1, 64, device=DEV).half()
+            self.parent, self.kid = i32([0]), i32([B - 1])
+            self.ws = torch.empty(rk.paged_kv_fork_workspace_size(1, B), dtype=torch.uint8, device=DEV)
+
+        def fork(self):
+            p = lambda t: ctypes.c_void_p(t.data_ptr())
+            return lib.paged_kv_fork(p(self.cache), None, p(self.table), p(self.lens), p(self.refs), p(self.parent),
+                                     p(self.kid), p(self.ws), self.ws.numel(), 1, self.B, 1, 64, 8, 2, 4, 0,
+                                     ctypes.c_void_p(self.stream.cuda_stream))
+
+    def work(b):
+        for _ in range(20000):                       # (after the first: the child is not empty, nothing to do)
+            rc = b.fork()
+            if rc != 0:
+                failures.append((b.B, rc))
+                return
+    batches = [Batch(B) for B in (1 << 18, 200000, 150000, 140000)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(b,)) for b in batches]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, failures
+    for b in batches:
+        assert b.lens[b.B - 1] == 3 and b.table[b.B - 1, 0].tolist() == [0, -1] and b.refs.tolist()[:2] == [1, 1]
+        assert torch.equal(b.cache[:, 0, :3], b.cache[:, 1, :3])
