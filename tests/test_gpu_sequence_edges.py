@@ -310,3 +310,78 @@ def test_forks_of_batches_of_very_different_sizes_at_once():
     for b in batches:
         assert b.lens[b.B - 1] == 3 and b.table[b.B - 1, 0].tolist() == [0, -1] and b.refs.tolist()[:2] == [1, 1]
         assert torch.equal(b.cache[:, 0, :3], b.cache[:, 1, :3])
+
+
+@pytest.mark.parametrize("fmt", ["f16", "e4m3", "int8"])
+def test_forked_pages_copied_away_in_a_graph(fmt):
+    """Free, fork, copy the forks' own pages away, launched without a gap: the copies take what the forks
+    have just written. Before every replay, pages written by forks and copies are filled with other bits."""
+    import rope_kv_cache_gb300 as rk
+    B, M, P, tpp, Hkv, D, live = 40, 8, 400, 16, 2, 64, 10
+    g = torch.Generator(device=DEV).manual_seed(5)
+    dt = {"f16": torch.float16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[fmt]
+    raw = torch.randint(0, 256, (2, P, tpp, Hkv, D * (2 if fmt == "f16" else 1)), generator=g, device=DEV, dtype=torch.uint8)
+    cache = raw.view(dt)
+    scales = None if fmt == "f16" else torch.rand(2, P, Hkv, tpp, generator=g, device=DEV)
+    table, lens = torch.full((B, 2, M), -1, dtype=torch.int32), [0] * B
+    refs = torch.zeros(P, dtype=torch.int32)
+    refs[300:] = 1                                     # where the copies go: nobody's to fork into
+    for b in range(live):
+        lens[b] = 16 * (b % M) + 1 + b                 # none is a multiple of a page
+        ids = torch.arange(8 * b + 100, 8 * b + 100 + -(-lens[b] // tpp))
+        table[b, 0, :len(ids)], table[b, 1, :len(ids)] = ids.int(), ids.int() + P
+        refs[ids] += 1
+        assert (refs[:300] <= 1).all()
+    table, lens, refs = table.to(DEV), i32(lens), refs.to(DEV)
+    kids, parents = i32(list(range(live, B))), i32([(7 * i) % live for i in range(B - live)])
+    n = B - live                                       # the forks' pages: the lowest free ones, 0 .. n - 1
+    src, dst = i32(list(range(n)) + [100]), i32(list(range(300, 300 + n + 1)))
+    ws = torch.empty(rk.paged_kv_fork_workspace_size(n, B), dtype=torch.uint8, device=DEV)
+
+    def step(wait=lambda: None):
+        rk.paged_kv_free(table, lens, refs, kids)
+        wait()
+        rk.paged_kv_fork(cache, table, lens, refs, parents, kids, kv_scales=scales, workspace=ws)
+        wait()
+        rk.paged_kv_copy_pages(cache, src, dst, kv_scales=scales)
+        wait()
+
+    def spoil(x):
+        raw[:, :n] = raw[:, 300:301 + n][:, :n] = x
+        raw[:, 300 + n] = x
+        if scales is not None:
+            scales[:, :n] = scales[:, 300:300 + n] = scales[:, 300 + n:301 + n] = float(x)
+    spoil(1)
+    step(torch.cuda.synchronize)
+    state = [t.clone() for t in (table, lens, refs)]
+    # by hand: the forks' pages and their copies hold the first tokens of the parents' last pages
+    for i in range(n):
+        b = int(parents[i])
+        full, rest = divmod(int(lens[b]), tpp)
+        tail = int(table[b, 0, full])
+        for p in (i, 300 + i):
+            assert torch.equal(raw[:, p, :rest], raw[:, tail, :rest]) and (raw[:, p, rest:] == 1).all()
+            assert scales is None or torch.equal(scales[:, p, :, :rest], scales[:, tail, :, :rest])
+    assert torch.equal(raw[:, 300 + n], raw[:, 100])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x in range(2, 30):
+        spoil(x)
+        torch.cuda.synchronize()
+        want, wscales = raw.clone(), None if scales is None else scales.clone()
+        for i in range(n):
+            b = int(parents[i])
+            full, rest = divmod(int(lens[b]), tpp)
+            tail = int(table[b, 0, full])
+            for p in (i, 300 + i):
+                want[:, p, :rest] = raw[:, tail, :rest]
+                if scales is not None:
+                    wscales[:, p, :, :rest] = scales[:, tail, :, :rest]
+        want[:, 300 + n] = raw[:, 100]
+        if scales is not None:
+            wscales[:, 300 + n] = scales[:, 100]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(raw, want) and (scales is None or torch.equal(scales, wscales))
+        assert all(torch.equal(a, b) for a, b in zip((table, lens, refs), state))
