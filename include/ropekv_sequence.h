@@ -63,11 +63,12 @@ ROPEKV_API int64_t prompt_attention_workspace_size(const ropekv_prompt_dims* dim
  *   lse          [numTokens, Hq] FP32 natural logarithm of the softmax sum, or NULL.
  * Starts are taken within [0, numTokens] and [0, numKVTokens]. Rows of no sequence
  * (before the first start, behind the last) are left as they were. A query that sees
- * nothing (nk < nq) gets a zero row and lse = -infinity.
+ * nothing (nk < nq), or whose scores are all -infinity, gets a zero row and lse =
+ * -infinity; a score of +infinity makes its row NaN.
  * Host errors: negative sizes, numTokens or numKVTokens > 2^28, batch > 2^20,
  * strides too small, not multiples of 8 or > 2^36, numTokens * Hq > 2^31 - 1, smScale
- * not finite, out overlapping q, k or v -> ROPEKV_ERR_SHAPE; workspaceBytes too small ->
- * ROPEKV_ERR_CAPACITY.
+ * or smScale * log2 e not finite, out overlapping q, k or v -> ROPEKV_ERR_SHAPE;
+ * workspaceBytes too small -> ROPEKV_ERR_CAPACITY.
  */
 ROPEKV_API int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k,
                                 int64_t kTokenStride, const uint16_t* v, int64_t vTokenStride,
@@ -103,12 +104,12 @@ ROPEKV_API int64_t tree_attention_workspace_size(const ropekv_tree_dims* dims);
  *   out             [B, S, Hq, D] FP16, every row written; may not overlap q or kvCache.
  *   lse             [B, S, Hq] FP32 natural logarithm of the softmax sum, or NULL.
  * Slots outside [0, kvCapacity) are not seen. A token that sees nothing (an inactive
- * sequence, kvCacheEndLens[b] = 0, for one) gets a zero row and lse = -infinity. What
- * lies in slots that no token sees does not matter, whatever its bits.
+ * sequence, kvCacheEndLens[b] = 0, for one), or whose scores are all -infinity, gets a zero
+ * row and lse = -infinity; a score of +infinity makes its row NaN. What lies in slots that no token sees does not matter, whatever its bits.
  * Host errors: negative sizes, seqLen > 2^15, kvCapacity > 2^28, batch * seqLen * Hq >
- * 2^31 - 1, kvCapacity * Hkv * D > 2^37 or, times batch, 2^40, smScale not finite, out
- * overlapping q or kvCache -> ROPEKV_ERR_SHAPE; workspaceBytes too small ->
- * ROPEKV_ERR_CAPACITY.
+ * 2^31 - 1, kvCapacity * Hkv * D > 2^37 or, times batch, 2^40, smScale or smScale *
+ * log2 e not finite, out overlapping q or kvCache -> ROPEKV_ERR_SHAPE; workspaceBytes too
+ * small -> ROPEKV_ERR_CAPACITY.
  */
 ROPEKV_API int tree_attention(const uint16_t* q, const uint16_t* kvCache,
                               const int32_t* kvCacheEndLens, const int32_t* treeMask, uint16_t* out,

@@ -262,6 +262,12 @@ Plan plan_of(const ropekv_tree_dims* d)
                      d->kvCapacity);
 }
 
+// Scores are held in binary digits.
+float scale_log2(float smScale)
+{
+    return smScale * 1.4426950408889634f;
+}
+
 bool overlap(const uint16_t* p, int64_t n, const uint16_t* q, int64_t m)
 {
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
@@ -300,7 +306,7 @@ int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k,
     const int64_t most = 1LL << 36, Hq = dims->numQHeads, Hkv = dims->numKVHeads, D = dims->headDim;
     if (qTokenStride < Hq * D || kTokenStride < Hkv * D || vTokenStride < Hkv * D || qTokenStride % 8 != 0 ||
         kTokenStride % 8 != 0 || vTokenStride % 8 != 0 || qTokenStride > most || kTokenStride > most ||
-        vTokenStride > most || !isfinite(smScale))
+        vTokenStride > most || !isfinite(scale_log2(smScale)))
         return ROPEKV_ERR_SHAPE;
     if (dims->numTokens == 0 || dims->batch == 0)
         return ROPEKV_OK;
@@ -331,7 +337,7 @@ int prompt_attention(const uint16_t* q, int64_t qTokenStride, const uint16_t* k,
     a.vTok = vTokenStride;
     a.kvHead = D;
     a.kvBatch = 0;            // one run of keys for all sequences
-    a.scaleLog2 = smScale * 1.4426950408889634f;
+    a.scaleLog2 = scale_log2(smScale);
     a.T = dims->numTokens;
     a.Tk = dims->numKVTokens;
     a.B = dims->batch;
@@ -357,7 +363,7 @@ int tree_attention(const uint16_t* q, const uint16_t* kvCache, const int32_t* kv
     const int rc = check_tree(dims);
     if (rc != ROPEKV_OK)
         return rc;
-    if (!isfinite(smScale))
+    if (!isfinite(scale_log2(smScale)))
         return ROPEKV_ERR_SHAPE;
     if (dims->batch == 0 || dims->seqLen == 0)
         return ROPEKV_OK;
@@ -386,7 +392,7 @@ int tree_attention(const uint16_t* q, const uint16_t* kvCache, const int32_t* kv
     a.kTok = a.vTok = dims->headDim;
     a.kvHead = cap * dims->headDim;
     a.kvBatch = 2 * plane;
-    a.scaleLog2 = smScale * 1.4426950408889634f;
+    a.scaleLog2 = scale_log2(smScale);
     a.T = (int32_t)T;
     a.B = dims->batch;
     a.S = dims->seqLen;

@@ -385,3 +385,23 @@ def test_forked_pages_copied_away_in_a_graph(fmt):
         torch.cuda.synchronize()
         assert torch.equal(raw, want) and (scales is None or torch.equal(scales, wscales))
         assert all(torch.equal(a, b) for a, b in zip((table, lens, refs), state))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_whose_scores_are_all_minus_infinity(D):
+    """Tokens 0 to 149 score -infinity for every query: a zero row and an lse of -infinity before token 150,
+    without them behind, in whole units and in cut ones."""
+    g = torch.Generator(device=DEV).manual_seed(D)
+    for nq, nk in ((300, 300), (160, 9000)):
+        q, k, v = (torch.randn(n, H, D, generator=g, device=DEV).half() for n, H in ((nq, 4), (nk, 2), (nk, 2)))
+        q[..., 0] = 1
+        hidden = nk - nq + 150
+        k[:hidden, :, 0] = -float("inf")
+        i, t = torch.arange(nq, device=DEV)[:, None] + nk - nq, torch.arange(nk, device=DEV)[None]
+        clean = k.clone()
+        clean[:hidden] = 0
+        o, l, to, tl = sp.attend(q, clean, v, (t <= i) & (t >= hidden))
+        for out, lse in (prompt(q, k, v, nq, nk), decode(q, k, v)):
+            assert (out[:150] == 0).all() and (lse[:150] == -float("inf")).all()
+            sp.check(out, o, to, "out")
+            sp.check(lse, l, tl, "lse")

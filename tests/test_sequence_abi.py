@@ -326,3 +326,10 @@ def test_outputs_over_inputs_are_refused():
     cache, lens = torch.zeros(5, 2, 2, 9, 64, dtype=torch.float16, device="cuda:0"), torch.ones(5, dtype=torch.int32, device="cuda:0")
     with pytest.raises(rk.RopeKVError):
         rk.tree_attention(q[:, None], cache, lens, q[:, None])
+
+
+def test_scales_that_fp32_does_not_hold_in_binary_digits_are_refused(lib):
+    for scale in (3e38, -3e38):
+        assert prompt(lib, scale=scale) == SHAPE and tree(lib, scale=scale) == SHAPE
+    # one that it does hold: the next check is reached
+    assert prompt(lib, scale=2e38, ptrs=[A] * 3 + [NUL] + [A] * 4) == NULL and tree(lib, scale=-2e38, ptrs=[NUL] * 7) == NULL
