@@ -189,7 +189,7 @@ struct RowsConfig {
     static constexpr int kOffStart = kOffSegs + kSegments * (int)sizeof(Segment);
     static constexpr int kOffSums = (kOffStart + (int)sizeof(Start) + 15) / 16 * 16;
     static constexpr int kOffFlags = kOffSums + kThreads / 32 * 16;
-    static constexpr int kSmem = kOffFlags + 32;
+    static constexpr int kSmem = kOffFlags + 16;
     static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
     static_assert(kColO + MT * D <= kCols, "TMEM");
 };
@@ -207,26 +207,23 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
 }
 
 // Wait of at most 2^20 polls, each of which the hardware may suspend for a time of its own choosing (130
-// ms were seen to pass within them). They start anew while rows are mended (failed[1]), which ends by
-// itself but takes long. LONG, the waits for a segment, which may lie behind millions of keys or of empty
-// sequences: also whenever the CTA has come further in the meantime, a load of K or V issued (failed[3]) or
-// a sequence passed (failed[4]). All others end within a step or two. False, for the whole CTA, if it runs
-// out. One poll in the code instead of one in front of the loop and one in it: 32 prompts of 300 tokens
-// 68 -> 62 us, one of 8000 339 -> 343. (LONG everywhere: the ragged batch 174.5 -> 177 us.)
+// ms were seen to pass within them): a step or two of the others' work. While one of them does what ends by
+// itself but takes long (failed[1]: rows are mended, empty sequences passed) they start anew. LONG, for the
+// segment warp, which waits for a whole segment: 2^31 polls, minutes, where 2^28 keys take 8 s; if nothing
+// comes on, one of the others' waits runs out before and ends this one too. False, for the whole CTA, if it
+// runs out. One poll in the code instead of one in front of the loop and one in it: 32 prompts of 300 tokens
+// 68 -> 62 us, one of 8000 339 -> 343.
 template <bool LONG = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, int parity, volatile int* failed)
 {
     bool done = false;
-    for (int i = 0, seen = 0; !done && i < (1 << 20); ++i) {
+    for (int i = 0; !done && i < (LONG ? 0x7fffffff : 1 << 20); ++i) {
         done = mbar_try(bar, parity);
         if ((i & 255) == 255) {
             if (*failed)
                 break;
-            const int now = LONG ? failed[3] + failed[4] : 0;
-            if (failed[1] || now != seen) {
-                seen = now;
+            if (failed[1])
                 i = 0;
-            }
         }
     }
     if (!done)
@@ -685,9 +682,9 @@ __device__ __forceinline__ void find_start(const RowsArgs& a, long long* sums, S
 }
 
 // The segments of a CTA's share, in order, each given to f. Returns the unit that the share begins
-// and others end, if there is one. For a whole warp; in `passed` the waits see that it comes on.
+// and others end, if there is one. For a whole warp.
 template <int TN, bool TREE, typename F>
-__device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& start, volatile int* passed, F&& f)
+__device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& start, volatile int* failed, F&& f)
 {
     Joint joint = {};
     if (!start.found)
@@ -736,13 +733,20 @@ __device__ __forceinline__ Joint each_segment(const RowsArgs& a, const Start& st
             unit = 0;
             if (++s.head == a.heads) {
                 s.head = 0;
-                do {
-                    const int b = s.b + 1;
-                    if (at >= end || b == a.B)
+                int b = s.b + 1;
+                if (at >= end || b == a.B)
+                    return joint;
+                static_cast<Sequence&>(s) = sequence<TREE>(a, b);
+                if (s.units == 0) {
+                    if (lane == 0)
+                        atomicAdd(const_cast<int*>(failed) + 1, 1);
+                    while (s.units == 0 && ++b < a.B)
+                        static_cast<Sequence&>(s) = sequence<TREE>(a, b);
+                    if (lane == 0)
+                        atomicSub(const_cast<int*>(failed) + 1, 1);
+                    if (b == a.B)
                         return joint;
-                    static_cast<Sequence&>(s) = sequence<TREE>(a, b);
-                    *passed = b;
-                } while (s.units == 0);
+                }
             }
         }
     }
@@ -756,7 +760,7 @@ __device__ __noinline__ void spoil_rows(const RowsArgs& a, const Start& start, v
 {
     const int row = threadIdx.x, rowTok = divide(row, a.divG);
     const float nan = __int_as_float(0x7fc00000);
-    each_segment<RowsConfig<D, MT, PER>::kTile, TREE>(a, start, failed + 4, [&](const Segment& s) {
+    each_segment<RowsConfig<D, MT, PER>::kTile, TREE>(a, start, failed, [&](const Segment& s) {
         if (rowTok >= a.tokens || s.tok0 + rowTok >= s.nq)
             return;
         if (s.slot >= 0) {
@@ -856,7 +860,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         }
         mbar_init(drained, 1);
         *failed = (base & 1023) | a.fail;      // tiles of 1024 bytes: 0
-        failed[1] = failed[3] = failed[4] = 0;
+        failed[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kLoad && lane < 3) {
@@ -881,7 +885,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
     int segments = 0;
     auto next = [&](Segment& s) -> bool {
         const int i = segments % kSegments;
-        if (!wait_warp<true>(segFull + 8 * i, (segments / kSegments) & 1, failed))
+        if (!wait_warp(segFull + 8 * i, (segments / kSegments) & 1, failed))
             return false;
         s = ring[i];
         __syncwarp();
@@ -904,7 +908,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
                 const int st = n % NS;
                 ok = ok && (n < NS || wait_warp(empty + 8 * st, (n / NS - 1) & 1, failed));
                 if (ok && elect_one()) {
-                    failed[3] = n + 1;
                     mbar_expect(full + 8 * st, C::kTileBytes);
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
@@ -1058,7 +1061,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
             __syncwarp();
             ++n;
         };
-        const Joint joint = each_segment<TN, TREE>(a, start, failed + 4, publish);
+        const Joint joint = each_segment<TN, TREE>(a, start, failed, publish);
         Segment s;
         s.head = -1;
         publish(s);
@@ -1077,7 +1080,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensor
         int items = 0;
         for (; ok; ++segments) {
             const int at4 = segments % kSegments;
-            ok = wait_warp<true>(segFull + 8 * at4, (segments / kSegments) & 1, failed);
+            ok = wait_warp(segFull + 8 * at4, (segments / kSegments) & 1, failed);
             const Segment& seg = ring[at4];                     // given back when its rows have left
             if (!ok || seg.head < 0)
                 break;
