@@ -195,8 +195,10 @@ ROPEKV_API int64_t paged_kv_fork_workspace_size(int32_t numForks, int32_t batch)
  *   pageTable  [batch, 2, maxPagesPerSeq] INT32, in and out.
  *   kvLens     [batch] INT32, in and out.
  *   parents, children  [numForks] INT32.
- * Skipped: a fork whose parent or child is out of range, whose child is not empty
- * (kvLens[child] > 0; see paged_kv_free), is named by two forks, or is a parent too.
+ * Skipped, without a sign but that table and lengths stay as they were: a fork whose parent
+ * or child is out of range, whose child is not empty (kvLens[child] > 0; see paged_kv_free),
+ * is named by two forks, or is a parent too. So beams that go on take empty sequences, and
+ * the old ones are given up afterwards: a beam search keeps twice its sequences in the table.
  * Host errors: as paged_kv_read; batch > 2^18 or numForks > 2^20 -> ROPEKV_ERR_SHAPE;
  * workspaceBytes too small -> ROPEKV_ERR_CAPACITY.
  */
@@ -213,6 +215,8 @@ ROPEKV_API int paged_kv_fork(void* kvCache, float* kvScales, int32_t* pageTable,
  * -1, its page's refCounts shrinks by one, and kvLens[s] becomes min(kvLens[s],
  * keepLens[i]). A sequence may be named more than once: the smallest length counts.
  *   keepLens  [numSequences] INT32, or NULL: 0 for all. Negative ones count as 0.
+ * A page that keepLens ends in stays, shared as it was: before tokens are written behind a
+ * shorter length into a page of refCounts above 1, the sequence needs a copy of its own.
  * Sequences out of range are skipped.
  * Host errors: as paged_kv_read.
  */

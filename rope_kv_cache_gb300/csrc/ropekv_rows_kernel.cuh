@@ -59,7 +59,7 @@
 // memory, 128 bytes a cycle. It takes about 3000: a tile's own chain is the wait for its scores
 // (250 cycles), their maximum (400), 128 exponentials a thread (850: a lone warp of a scheduler
 // issues one in 6.5 cycles, two warps one in 4.3) and the products behind it (1150), and the
-// other tile fills what it can. 12001 tokens: 785 to 820 us, 1.44 to 1.5 PFLOP/s, with the
+// other tile fills what it can. 12001 tokens: 785 to 830 us, 1.42 to 1.5 PFLOP/s, with the
 // power limit reached at 1.65 to 1.75 GHz; with the products alone 672 us, with the softmax
 // alone 632. A change of units costs 5000 cycles, half of them the rows on their way out: 24
 // sequences of 1 to 1200 tokens, half behind a context, 175 us. One row tile and long contexts
