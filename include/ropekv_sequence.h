@@ -16,13 +16,12 @@
  * need workspaces of their own. They are one or two launches whose split follows
  * from the sizes and lengths alone, so equal calls give equal bits. Scores, sums and
  * partial results are FP32; the weights of V are rounded to FP16 once, which is 2^-11 of a
- * weight, or 2^-32 of the row's largest where that is more. A value that is
- * not finite reaches only the rows that see its token; an infinity in V is one in out
- * whatever its weight, and one or a NaN costs such rows, and those of the same tile that do
- * not see it, a much slower path. Waits inside the kernels
- * are bounded while nothing comes on; should one run out, all rows that a CTA had taken on, and
- * all rows of units that it shares with others, are NaN in out and lse, but for such as it had
- * finished.
+ * weight, or 2^-32 of the row's largest where that is more. A value that is not finite
+ * reaches only the rows that see its token; an infinity in V is one in out whatever its
+ * weight, and one or a NaN costs such rows, and those of the same tile that do not see it, a
+ * much slower path. Waits inside the kernels are bounded; should one run out, which takes a
+ * fault and no argument, all rows that a CTA had taken on, and all rows of units that it
+ * shares with others, are NaN in out and lse, but for such as it had finished.
  */
 #ifndef ROPEKV_SEQUENCE_H
 #define ROPEKV_SEQUENCE_H

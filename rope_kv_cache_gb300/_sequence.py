@@ -131,8 +131,8 @@ def paged_kv_fork(kv_cache: torch.Tensor, page_table: torch.Tensor, kv_lens: tor
     whole pages are shared (ref_counts [P] int32 grows), a partly filled last page is copied to
     the lowest free page (one with ref_counts 0). page_table [B, 2, M] int32 and kv_lens [B]
     int32 get the children's rows; pages that an empty child's row still names are given up. A fork
-    into a sequence that is not empty, or is itself a parent in this call, is skipped. workspace: a uint8 tensor of paged_kv_fork_workspace_size
-    bytes, or None."""
+    into a sequence that is not empty, or is itself a parent in this call, is skipped. workspace:
+    a uint8 tensor of paged_kv_fork_workspace_size bytes, or None."""
     _check("paged_kv_fork", _native().fork(kv_cache, page_table, kv_lens, ref_counts, parents, children, kv_scales,
                                            workspace, stream))
 
